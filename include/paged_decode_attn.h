@@ -329,6 +329,83 @@ int paged_decode_attn_remap_table(int32_t* block_table, int batch, int max_block
                                   const int32_t* lens, int block_size, const int32_t* new_id,
                                   int64_t num_blocks, int* err, int device, void* stream);
 
+/* ------------------------ block-scaled FP8 caches ------------------------
+ * (Landing page, "Next boundaries": FP8 KV-cache compression; the block
+ * scales are this library's design.) k_cache and v_cache are
+ * [num_blocks, block_size, Hkv, D] E4M3 bytes, k_scale and v_scale
+ * [num_blocks, Hkv] fp32; byte y of a block's head stands for scale * y.
+ *
+ * The writers choose power-of-two scales: 2^e with the smallest e >= -60 for
+ * which the largest finite |x| of the block and head is at most 448 * 2^e,
+ * and store y = x / 2^e rounded to nearest, ties to even. A power of two
+ * costs an E4M3 value no precision, and x / 2^e and 2^e * y are exact. NaN
+ * and infinities are stored as NaN and do not take part in the scale. The
+ * readers take any finite scale >= 0. */
+
+/* Quantise rows and append them. Sequence b < batch gets the rows
+ * cu_rows[b] .. cu_rows[b + 1] - 1 of k and v ([num_rows, Hkv, D], dtype
+ * PDA_BF16 or PDA_FP16, token strides in elements, 0 = packed) as its last
+ * n_b = cu_rows[b + 1] - cu_rows[b] tokens: positions context_lens[b] - n_b ..
+ * context_lens[b] - 1 of its pages, so context_lens (the new tokens included)
+ * is what the next paged_decode_attn_run_block_scaled takes. n_b = 0 is fine; one
+ * new token per sequence (a decode step) and whole prompts are the same call.
+ * Rows before cu_rows[0] or from cu_rows[batch] on are not read.
+ *
+ * A block whose first token is written by the call starts anew: its old
+ * scale is not read. A block with earlier tokens keeps the larger of its
+ * scale and the one the new rows need; where that is larger, the earlier
+ * values y become y * old / new, rounded again (an old scale that is not
+ * positive and finite counts as 0, and the values as zeros). So the blocks
+ * that a call writes must belong to one sequence each: copy a block shared
+ * with another sequence (paged_decode_attn_copy_blocks, and its scales)
+ * before appending to it.
+ *
+ * head_dim 64 or 128, block_size 16, 32 or 64. Pointers and strides 16-byte
+ * aligned (index arrays and scales: their element size). `err` (optional
+ * device int[2]) receives the first problem found: code 1 (cu_rows not
+ * ascending within num_rows, or a context length below n_b or above
+ * max_blocks * block_size; the sequence is skipped) or 2 (a block id outside
+ * [0, num_blocks); the block is skipped), and the sequence. Outputs must not
+ * overlap inputs or each other (PDA_EALIAS). Asynchronous on `stream`;
+ * allocates nothing; graph-capturable. */
+int paged_decode_attn_append_kv_fp8(const void* k, int64_t k_token_stride, const void* v,
+                                    int64_t v_token_stride, int64_t num_rows, int num_kv_heads,
+                                    int head_dim, int dtype, void* k_cache, void* v_cache,
+                                    float* k_scale, float* v_scale, int64_t num_blocks,
+                                    int block_size, const int32_t* block_table, int max_blocks,
+                                    const int32_t* context_lens, const int64_t* cu_rows,
+                                    int batch, int* err, int device, void* stream);
+
+/* The same after rotary positions, in one launch: q and k are rotated as in
+ * paged_decode_attn_rope_kv_write (positions [num_rows] int32, cos_sin_cache,
+ * rot_dim, neox_style; exactly rounded to dtype), the rotated q rows go to
+ * q_out (q_out == q with equal strides rotates in place) and the rotated k
+ * rows, as dtype values, and the v rows are quantised and appended as above.
+ * Rows that belong to no sequence are neither read nor written. A row with a
+ * position outside [0, max_position) writes nothing (code 4 and the row). */
+int paged_decode_attn_rope_append_kv_fp8(
+    const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,
+    int64_t v_token_stride, const int32_t* positions, const float* cos_sin_cache,
+    int max_position, int rot_dim, int neox_style, int64_t num_rows, int num_q_heads,
+    int num_kv_heads, int head_dim, int dtype, void* q_out, int64_t q_out_token_stride,
+    void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t num_blocks,
+    int block_size, const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+    const int64_t* cu_rows, int batch, int* err, int device, void* stream);
+
+/* Read back: as paged_decode_attn_gather_kv, with scale * y (one rounding to
+ * out_dtype PDA_BF16, PDA_FP16 or PDA_F32 from the fp32 product) in place of
+ * the raw bytes. k_out and v_out are [out_rows, Hkv, D]; rows no sequence
+ * names are left alone. err: code 1 (a length above max_len or below 0, which
+ * is cut) or 2 (a block id outside [0, num_blocks), or a row outside
+ * [0, out_rows); the block is skipped), and the sequence. */
+int paged_decode_attn_gather_kv_fp8(const void* k_cache, const void* v_cache,
+                                    const float* k_scale, const float* v_scale,
+                                    int64_t num_blocks, int block_size, int num_kv_heads,
+                                    int head_dim, const int32_t* block_table, int max_blocks,
+                                    const int32_t* lens, const int64_t* cu_rows, int batch,
+                                    int max_len, void* k_out, void* v_out, int64_t out_rows,
+                                    int out_dtype, int* err, int device, void* stream);
+
 /* Decode attention for callers that cannot allocate device memory.
  * (No counterpart in the paper: this entry point exists for integration.)
  *

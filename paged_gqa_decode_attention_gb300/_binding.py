@@ -46,6 +46,9 @@ EXPORTS = [
     "paged_decode_attn_gather_kv",
     "paged_decode_attn_scatter_kv",
     "paged_decode_attn_remap_table",
+    "paged_decode_attn_append_kv_fp8",
+    "paged_decode_attn_rope_append_kv_fp8",
+    "paged_decode_attn_gather_kv_fp8",
 ]
 
 
@@ -122,6 +125,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.paged_decode_attn_scatter_kv.restype = I
         lib.paged_decode_attn_remap_table.argtypes = [P, I, I, P, I, P, I64, P, I, P]
         lib.paged_decode_attn_remap_table.restype = I
+        cache_args = [P, P, P, P, I64, I, P, I, P, P, I, P, I, P]
+        lib.paged_decode_attn_append_kv_fp8.argtypes = [P, I64, P, I64, I64, I, I, I] + cache_args
+        lib.paged_decode_attn_append_kv_fp8.restype = I
+        lib.paged_decode_attn_rope_append_kv_fp8.argtypes = (
+            [P, I64, P, I64, P, I64, P, P, I, I, I, I64, I, I, I, I, P, I64] + cache_args)
+        lib.paged_decode_attn_rope_append_kv_fp8.restype = I
+        lib.paged_decode_attn_gather_kv_fp8.argtypes = [P, P, P, P, I64, I, I, I, P, I, P, P, I, I,
+                                                        P, P, I64, I, P, I, P]
+        lib.paged_decode_attn_gather_kv_fp8.restype = I
         if lib.paged_decode_attn_abi_version() != ABI_VERSION:
             raise RuntimeError("ABI version mismatch between binding and library")
         if path is None:
@@ -445,3 +457,166 @@ def remap_table(block_table, lens, block_size: int, new_id, err=None, stream=Non
         block_table.shape[1], _dev_ptr(lens, "lens", torch.int32), int(block_size),
         _dev_ptr(new_id, "new_id", torch.int32), new_id.shape[0], _opt_err(err),
         _device_of(block_table), _stream_ptr(stream)))
+
+
+# --------------------------- block-scaled FP8 caches ---------------------------
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _stream_on(stream, device: int) -> int:
+    """`stream`, or torch's current stream of `device` (which need not be the current one)."""
+    return _stream_ptr(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _fp8_cache(k_cache, v_cache, k_scale, v_scale):
+    """Pointers of a block-scaled FP8 cache: [num_blocks, block_size, Hkv, D] E4M3 bytes and
+    [num_blocks, Hkv] fp32 scales."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [num_blocks, block_size, Hkv, D] alike")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"{name} must be float8_e4m3fn or uint8")
+    if k_scale.shape != (shape[0], shape[2]) or v_scale.shape != (shape[0], shape[2]):
+        raise ValueError("k_scale and v_scale must be [num_blocks, Hkv]")
+    return (_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+            _dev_ptr(k_scale, "k_scale", torch.float32),
+            _dev_ptr(v_scale, "v_scale", torch.float32))
+
+
+def _append_args(k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, cu_rows,
+                 err, stream):
+    """Checks shared by the two appends; the cache and sequence arguments of the C calls."""
+    ptrs = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    nb, bs, Hkv, D = k_cache.shape
+    if k.shape != v.shape or k.shape[1:] != (Hkv, D):
+        raise ValueError("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_blocks]")
+    B = block_table.shape[0]
+    if context_lens.shape != (B,) or cu_rows.shape != (B + 1,):
+        raise ValueError("context_lens must be [batch] and cu_rows [batch + 1]")
+    _same_device(k_cache.device, k=k, v=v, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                 block_table=block_table, context_lens=context_lens, cu_rows=cu_rows, err=err)
+    dev = _device_of(k_cache)
+    return ptrs + (nb, bs, _dev_ptr(block_table, "block_table", torch.int32),
+                   block_table.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
+                   _dev_ptr(cu_rows, "cu_rows", torch.int64), B, _opt_err(err),
+                   dev, _stream_on(stream, dev))
+
+
+def append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                  context_lens: torch.Tensor, cu_rows: torch.Tensor,
+                  err: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise the rows of k and v and append them to a block-scaled FP8
+    cache (in place: caches and scales).
+
+    k, v [rows, Hkv, D] (bf16/fp16; token-strided views allowed), caches
+    [num_blocks, block_size, Hkv, D] float8_e4m3fn or uint8, scales
+    [num_blocks, Hkv] fp32, block_table [batch, max_blocks] int32. Sequence b's
+    last tokens, up to context_lens[b] (int32, the new ones included), are the
+    rows cu_rows[b] .. cu_rows[b + 1] - 1 (cu_rows: int64, [batch + 1])."""
+    lib = load_library()
+    kp, ks = _token_rows(k, "k", k.dtype)
+    vp, vs = _token_rows(v, "v", k.dtype)
+    if k.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("k and v must be bfloat16 or float16")
+    args = _append_args(k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+                        cu_rows, err, stream)
+    T, Hkv, D = k.shape
+    _check(lib, lib.paged_decode_attn_append_kv_fp8(kp, ks, vp, vs, T, Hkv, D, _DT[k.dtype], *args))
+
+
+def rope_append_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor, cos_sin_cache: torch.Tensor,
+                       k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                       v_scale: torch.Tensor, block_table: torch.Tensor,
+                       context_lens: torch.Tensor, cu_rows: torch.Tensor, neox: bool = True,
+                       q_out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """RoPE on q and k, then append_kv_fp8 of the rotated k and of v, in one
+    launch. positions [rows] int32, cos_sin_cache [max_position, rot_dim] fp32
+    (cosines then sines), neox as in rope_kv_write. Returns q_out (a new
+    tensor, or ``q_out``; pass ``q_out=q`` to rotate in place); its rows that
+    belong to no sequence are not written."""
+    lib = load_library()
+    dt = q.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise ValueError("q, k and v must be bfloat16 or float16")
+    qp, qs = _token_rows(q, "q", dt)
+    kp, ks = _token_rows(k, "k", dt)
+    vp, vs = _token_rows(v, "v", dt)
+    T, Hq, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("k and v must have q's rows and head_dim")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    qop, qos = _token_rows(q_out, "q_out", dt)
+    if cos_sin_cache.dim() != 2:
+        raise ValueError("cos_sin_cache must be [max_position, rot_dim]")
+    if positions.shape != (T,):
+        raise ValueError("positions must be [rows]")
+    args = _append_args(k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+                        cu_rows, err, stream)
+    _same_device(k_cache.device, q=q, q_out=q_out, positions=positions,
+                 cos_sin_cache=cos_sin_cache)
+    max_pos, rot_dim = cos_sin_cache.shape
+    _check(lib, lib.paged_decode_attn_rope_append_kv_fp8(
+        qp, qs, kp, ks, vp, vs, _dev_ptr(positions, "positions", torch.int32),
+        _dev_ptr(cos_sin_cache, "cos_sin_cache", torch.float32), max_pos, rot_dim,
+        int(bool(neox)), T, Hq, k.shape[1], D, _DT[dt], qop, qos, *args))
+    return q_out
+
+
+def gather_kv_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_rows=None,
+                  max_len: int | None = None, k_out=None, v_out=None, dtype=torch.bfloat16,
+                  err=None, stream=None):
+    """gather_kv from a block-scaled FP8 cache: each sequence's tokens, in
+    order, dequantised (scale * value) into contiguous [rows, Hkv, D] buffers
+    of ``dtype`` (or k_out's): sequence b from row cu_rows[b] (int64; default:
+    exclusive prefix sums of lens, computed on the host from lens). Returns
+    (k_out, v_out)."""
+    lib = load_library()
+    ptrs = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    nb, bs, Hkv, D = k_cache.shape
+    if (k_out is None) != (v_out is None):
+        raise ValueError("pass both k_out and v_out, or neither")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_blocks]")
+    B = block_table.shape[0]
+    if cu_rows is None or max_len is None or k_out is None:
+        lens_h = lens.cpu().to(torch.int64)
+        total = int(lens_h.sum())
+        if cu_rows is None:
+            cu_rows = (torch.cumsum(lens_h, 0) - lens_h).to(k_cache.device)
+        elif B:
+            total = int((cu_rows.cpu() + lens_h).max())
+        if max_len is None:
+            max_len = int(lens_h.max()) if B else 0
+        if k_out is None:
+            k_out = torch.empty((total, Hkv, D), dtype=dtype, device=k_cache.device)
+            v_out = torch.empty((total, Hkv, D), dtype=dtype, device=k_cache.device)
+    if lens.shape != (B,) or cu_rows.shape != (B,):
+        raise ValueError("lens and cu_rows must be [batch]")
+    if k_out.shape[1:] != (Hkv, D) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out must be [rows, Hkv, D] alike")
+    if k_out.dtype not in _DT:
+        raise ValueError("k_out and v_out must be bfloat16, float16 or float32")
+    _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                 block_table=block_table, lens=lens, cu_rows=cu_rows, k_out=k_out, v_out=v_out,
+                 err=err)
+    dev = _device_of(k_cache)
+    _check(lib, lib.paged_decode_attn_gather_kv_fp8(
+        *ptrs, nb, bs, Hkv, D, _dev_ptr(block_table, "block_table", torch.int32),
+        block_table.shape[1], _dev_ptr(lens, "lens", torch.int32),
+        _dev_ptr(cu_rows, "cu_rows", torch.int64), B, int(max_len), _dev_ptr(k_out, "k_out"),
+        _dev_ptr(v_out, "v_out"), k_out.shape[0], _DT[k_out.dtype], _opt_err(err),
+        dev, _stream_on(stream, dev)))
+    return k_out, v_out

@@ -1,0 +1,767 @@
+// The block-scaled FP8 cache: quantising K/V rows as they are written, with or
+// without rotary positions, and reading them back. The decode kernels read the
+// same cache (paged_decode_attn_run_block_scaled).
+//
+// A cache is [num_blocks, block_size, Hkv, D] of E4M3 values with one fp32
+// scale per block and kv head, [num_blocks, Hkv]; a stored value y stands for
+// s * y. For the values x of a block and head,
+//   s = 2^e with the smallest e >= kMinScaleExp for which max |x| <= 448 * 2^e,
+//   y = rn_e4m3(x / s)   (to nearest, ties to even).
+// A power of two costs an E4M3 value no precision (its steps are relative) and
+// makes x / s and s * y exact, so a stored value depends on nothing but the
+// block's exponent, and raising the exponent of a block rounds only values
+// that become subnormal.
+//
+// A block that a call appends to behind tokens it holds keeps
+// s' = max(s, needed by the new rows); where s' > s its earlier values become
+// rn_e4m3(y * s / s'). One warp (two for 64-token blocks of 128 dims) owns the
+// tile of one (block, K or V, head): nothing is exchanged between blocks of
+// threads, no atomics, the result does not depend on any order.
+//
+// Bound by memory traffic: a row costs 2 bytes read and 1 written per value.
+// A tile's rows are held in registers between the maximum and the rounding
+// (NV 16-byte vectors a lane), so each is read once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <string>
+
+#include "paged_decode_attn.h"
+#include "pda_internal.h"
+#include "rope_math.cuh"
+#include "row_sets.h"
+
+namespace pda {
+namespace {
+
+constexpr int kAppendWarps = 8;
+constexpr int kAppendThreads = 32 * kAppendWarps;
+constexpr int kMinScaleExp = -60;
+constexpr unsigned kAll = 0xffffffffu;
+
+struct AppendParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride, qo_stride;  // elements between rows
+  const int32_t* positions;  // [T] (rope)
+  const float* cos_sin;      // [max_position, rot_dim] (rope)
+  uint16_t* q_out;
+  uint8_t* k_cache;  // [num_blocks, block_size, Hkv, D]
+  uint8_t* v_cache;
+  float* k_scale;    // [num_blocks, Hkv]
+  float* v_scale;
+  const int32_t* table;  // [B, max_blocks]
+  const int32_t* lens;   // [B], the new rows included
+  const int64_t* cu;     // [B + 1]
+  int* err;              // optional {code, detail}
+  int64_t num_blocks;
+  int64_t T;
+  int B, Hq, Hkv, block_size, max_blocks, max_position, rot_dim;
+  int groups;      // CTAs per unit: ceil(2 Hkv / tiles per CTA)
+  int64_t kv_ctas; // units * groups; later CTAs rotate q rows
+};
+
+__device__ __forceinline__ void record(int* err, int code, int detail) {
+  if (err != nullptr && atomicCAS(err, 0, code) == 0) err[1] = detail;
+}
+
+// Work units: sequence b's new rows cu[b] .. cu[b + 1] get the unit slots
+// base(b) .. base(b + 1) - 1, base(b) = floor(cu[b] / block_size) + b. That is
+// at least floor(n / block_size) + 1 slots for n rows, which touch at most
+// floor((n - 2) / block_size) + 2 blocks (n >= 2), so slot j takes the j-th
+// touched block and the last slot also the one after it. The unit count
+// floor(T / block_size) + B needs no device value.
+//
+// Returns the sequence of unit u (-1: none): a 32-way search for the last b
+// with base(b) <= u, one round of loads per factor of 32 of the batch.
+__device__ __forceinline__ int unit_sequence(const int64_t* cu, int B, int block_size, int64_t u,
+                                             int lane) {
+  int lo = 0, n = B;
+  while (true) {
+    const int step = (n + 31) >> 5;
+    const int i = lane * step;
+    bool le = false;
+    if (i < n) le = __ldg(cu + lo + i) / block_size + (lo + i) <= u;
+    const int cnt = __popc(__ballot_sync(kAll, le));
+    if (cnt == 0) return -1;
+    lo += (cnt - 1) * step;
+    if (step == 1) return lo;
+    n = min(step, n - (cnt - 1) * step);
+  }
+}
+
+// The vector of 8 elements at column `col` of a head row, rotated: pairs
+// (j, j + half) need the vector `half` columns away, which another lane of the
+// same row group holds; interleaved pairs lie inside the vector.
+template <typename F, bool kNeox>
+__device__ __forceinline__ uint4 rotate_vec(uint4 x, const float* cs, int col, int half, int lane) {
+  uint4 y = x;
+  if constexpr (kNeox) {
+    const int rot = 2 * half;
+    const int hop = col < half ? (half >> 3) : (col < rot ? -(half >> 3) : 0);
+    uint4 o;
+    o.x = __shfl_sync(kAll, x.x, lane + hop);
+    o.y = __shfl_sync(kAll, x.y, lane + hop);
+    o.z = __shfl_sync(kAll, x.z, lane + hop);
+    o.w = __shfl_sync(kAll, x.w, lane + hop);
+    if (hop != 0 && cs != nullptr) {
+      // lower half: x cos - o sin; upper half: x cos + o sin
+      const int j = col < half ? col : col - half;
+      const float sg = col < half ? -1.f : 1.f;
+      const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + j));
+      const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + j + 4));
+      const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half + j));
+      const float4 s1 = __ldg(reinterpret_cast<const float4*>(cs + half + j + 4));
+      y.x = rounded_dot2_x2<F>(F::lo_f(x.x), c0.x, sg * F::lo_f(o.x), s0.x,
+                               F::hi_f(x.x), c0.y, sg * F::hi_f(o.x), s0.y);
+      y.y = rounded_dot2_x2<F>(F::lo_f(x.y), c0.z, sg * F::lo_f(o.y), s0.z,
+                               F::hi_f(x.y), c0.w, sg * F::hi_f(o.y), s0.w);
+      y.z = rounded_dot2_x2<F>(F::lo_f(x.z), c1.x, sg * F::lo_f(o.z), s1.x,
+                               F::hi_f(x.z), c1.y, sg * F::hi_f(o.z), s1.y);
+      y.w = rounded_dot2_x2<F>(F::lo_f(x.w), c1.z, sg * F::lo_f(o.w), s1.z,
+                               F::hi_f(x.w), c1.w, sg * F::hi_f(o.w), s1.w);
+    }
+  } else {
+    if (col < 2 * half && cs != nullptr) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (col >> 1)));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + (col >> 1)));
+      auto pair = [](uint32_t w, float cc, float ss) {
+        const float a = F::lo_f(w), b = F::hi_f(w);
+        return rounded_dot2_x2<F>(a, cc, -b, ss, b, cc, a, ss);
+      };
+      y.x = pair(x.x, c.x, s.x);
+      y.y = pair(x.y, c.y, s.y);
+      y.z = pair(x.z, c.z, s.z);
+      y.w = pair(x.w, c.w, s.w);
+    }
+  }
+  return y;
+}
+
+template <typename F>
+struct Inf16;
+template <>
+struct Inf16<Bf16> {
+  static constexpr uint32_t bits = 0x7f80u;
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
+};
+template <>
+struct Inf16<Fp16> {
+  static constexpr uint32_t bits = 0x7c00u;
+  static __device__ __forceinline__ float value(uint32_t b) {
+    return __half2float(__ushort_as_half((unsigned short)b));
+  }
+};
+
+// Largest |x| of a 16-bit pair pattern, as a pattern; non-finite ones count 0.
+__device__ __forceinline__ uint32_t finite_max(uint32_t w, uint32_t inf) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  return max(lo < inf ? lo : 0u, hi < inf ? hi : 0u);
+}
+
+// 2^e as above for a largest magnitude a (448 = 1.75 * 2^8).
+__device__ __forceinline__ float block_scale(float a) {
+  const uint32_t u = __float_as_uint(a);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, kMinScaleExp);  // also zeros and subnormals
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ bool is_normal_power_of_two(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x7fffffu) == 0 && u >= (1u << 23) && u <= (253u << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Four E4M3 bytes times f (requantisation, read-back).
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&x)[4]) {
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
+  x[0] = fa.x;
+  x[1] = fa.y;
+  x[2] = fb.x;
+  x[3] = fb.y;
+}
+
+// One vector of 8 16-bit elements over the scale s, as 8 E4M3 bytes. E4M3 has
+// no infinity: a non-finite element is stored as NaN.
+template <typename F, bool kPow2, bool kNonFinite>
+__device__ __forceinline__ uint2 quantise(uint4 x, float s, float inv) {
+  auto q = [&](float a) {
+    if (kNonFinite && isinf(a)) return __uint_as_float(0x7fc00000u);
+    return kPow2 ? a * inv : __fdiv_rn(a, s);
+  };
+  uint2 y;
+  y.x = e4m3x4(q(F::lo_f(x.x)), q(F::hi_f(x.x)), q(F::lo_f(x.y)), q(F::hi_f(x.y)));
+  y.y = e4m3x4(q(F::lo_f(x.z)), q(F::hi_f(x.z)), q(F::lo_f(x.w)), q(F::hi_f(x.w)));
+  return y;
+}
+
+enum Rope { kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2 };
+
+// CTAs below p.kv_ctas: a unit's tiles, W warps per tile; the others (rope):
+// one q row per warp.
+template <typename F, int D, int NV, int W, int kRope>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  constexpr int kCols = D / 8;           // vectors of a head row (8 or 16)
+  constexpr int kRowsPerStep = 32 / kCols;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = (lane & (kCols - 1)) * 8;
+  const int half = p.rot_dim >> 1;
+
+  if (kRope != kRopeNone && blockIdx.x >= p.kv_ctas) {
+    const int64_t r = ((int64_t)blockIdx.x - p.kv_ctas) * kAppendWarps + warp;
+    const int64_t r_lo = __ldg(p.cu), r_hi = __ldg(p.cu + p.B);
+    if (r < r_lo || r >= r_hi || r >= p.T) return;
+    const int pos = __ldg(p.positions + r);
+    if (pos < 0 || pos >= p.max_position) {
+      if (lane == 0) record(p.err, kErrPosition, (int)r);
+      return;
+    }
+    const float* cs = p.cos_sin + (int64_t)pos * p.rot_dim;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + r * p.q_stride);
+    uint4* dst = reinterpret_cast<uint4*>(p.q_out + r * p.qo_stride);
+    const int n = p.Hq * kCols;
+    for (int i0 = 0; i0 < n; i0 += 32 * 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int idx = i0 + i * 32 + lane;
+        x[i] = idx < n ? src[idx] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int idx = i0 + i * 32 + lane;
+        const uint4 y = rotate_vec<F, kRope == kRopeHalves>(x[i], cs, col, half, lane);
+        if (idx < n) dst[idx] = y;
+      }
+    }
+    return;
+  }
+
+  __shared__ uint32_t s_max[kAppendWarps];
+  const int64_t u = blockIdx.x / p.groups;
+  const int grp = blockIdx.x - (int)(u * p.groups);
+  const int b = unit_sequence(p.cu, p.B, p.block_size, u, lane);
+  if (b < 0) return;
+  const int64_t r_lo = __ldg(p.cu + b), r_hi = __ldg(p.cu + b + 1);
+  const int len = __ldg(p.lens + b);
+  const int64_t n = r_hi - r_lo;
+  const int bs = p.block_size;
+  const int64_t base = r_lo / bs + b, slots = r_hi / bs + b + 1 - base;
+  const int64_t j = u - base;
+  if (n == 0 || j >= slots) return;
+  if (r_lo < 0 || n < 0 || r_hi > p.T || n > len || (int64_t)len > (int64_t)p.max_blocks * bs) {
+    if (threadIdx.x == 0) record(p.err, kErrContextLen, b);
+    return;
+  }
+  const int start = len - (int)n;
+  const int last_page = (len - 1) / bs;
+  const int tile = grp * (kAppendWarps / W) + warp / W;
+  const int wsub = warp % W;
+  const bool has_tile = tile < 2 * p.Hkv;
+  const bool is_v = tile >= p.Hkv;
+  const int h = is_v ? tile - p.Hkv : tile;
+  const uint16_t* x_rows = is_v ? p.v : p.k;
+  const int64_t x_stride = is_v ? p.v_stride : p.k_stride;
+  uint8_t* cache = is_v ? p.v_cache : p.k_cache;
+  float* scales = is_v ? p.v_scale : p.k_scale;
+
+  for (int page = start / bs + (int)j; page <= last_page; ++page) {
+    const int blk = __ldg(p.table + (int64_t)b * p.max_blocks + page);
+    const bool blk_ok = blk >= 0 && blk < p.num_blocks;
+    if (!blk_ok && threadIdx.x == 0) record(p.err, kErrBlockId, b);
+    const int t_lo = max(start, page * bs), t_hi = min(len, (page + 1) * bs);
+    const int off = t_lo - page * bs, nr = t_hi - t_lo;
+    const int64_t row0 = r_lo + (t_lo - start);
+    const bool active = has_tile && blk_ok;
+    const int64_t sidx = (int64_t)(blk_ok ? blk : 0) * p.Hkv + (has_tile ? h : 0);
+    float old = 0.f;
+    if (active && off > 0) old = scales[sidx];
+    uint4 x[NV];
+    bool live[NV];  // the row is written
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int row = (i * W + wsub) * kRowsPerStep + lane / kCols;
+      live[i] = active && row < nr;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (live[i])
+        x[i] = __ldg(reinterpret_cast<const uint4*>(x_rows + (row0 + row) * x_stride + h * D + col));
+    }
+    if constexpr (kRope != kRopeNone) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int row = (i * W + wsub) * kRowsPerStep + lane / kCols;
+        const float* cs = nullptr;
+        if (live[i]) {
+          const int pos = __ldg(p.positions + row0 + row);
+          live[i] = pos >= 0 && pos < p.max_position;
+          cs = p.cos_sin + (int64_t)pos * p.rot_dim;
+          if (!live[i]) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            cs = nullptr;
+          }
+        }
+        if (!is_v) x[i] = rotate_vec<F, kRope == kRopeHalves>(x[i], cs, col, half, lane);
+      }
+    }
+    // largest magnitude of the tile
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+    }
+    uint32_t m = __reduce_max_sync(kAll, max(m2 & 0xffffu, m2 >> 16));
+    const bool nonfinite = m >= Inf16<F>::bits;  // warp-uniform, rare
+    if (nonfinite) {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        m = max(m, max(max(finite_max(x[i].x, Inf16<F>::bits), finite_max(x[i].y, Inf16<F>::bits)),
+                       max(finite_max(x[i].z, Inf16<F>::bits), finite_max(x[i].w, Inf16<F>::bits))));
+      m = __reduce_max_sync(kAll, m);
+    }
+    if constexpr (W > 1) {
+      if (lane == 0) s_max[warp] = m;
+      __syncthreads();  // also: every warp of the tile has read the old scale
+#pragma unroll
+      for (int w = 0; w < W; ++w) m = max(m, s_max[warp - wsub + w]);
+      __syncthreads();
+    }
+    if (active) {
+      if (!(old > 0.f && old <= 3.402823466e38f)) old = 0.f;
+      const float s = fmaxf(old, block_scale(Inf16<F>::value(m)));
+      uint8_t* tile_base = cache + ((int64_t)blk * bs * p.Hkv + h) * D;
+      const int64_t row_bytes = (int64_t)p.Hkv * D;
+      if (off > 0 && s > old) {
+        // the block's earlier values, 16 bytes a lane
+        constexpr int kV16 = D / 16;
+        const float f = __fdiv_rn(old, s);
+        for (int i = wsub * 32 + lane; i < off * kV16; i += 32 * W) {
+          uint4* a = reinterpret_cast<uint4*>(tile_base + (i / kV16) * row_bytes + (i % kV16) * 16);
+          uint4 w = *a;
+          uint32_t* ww = &w.x;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            float y[4];
+            e4m3x4_to_float(ww[t], y);
+            ww[t] = e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+          }
+          *a = w;
+        }
+      }
+      if (wsub == 0 && lane == 0) scales[sidx] = s;
+      const bool pow2 = is_normal_power_of_two(s);
+      const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (live[i]) {
+          const int row = (i * W + wsub) * kRowsPerStep + lane / kCols;
+          uint2 y;
+          if (pow2 && !nonfinite) y = quantise<F, true, false>(x[i], s, inv);
+          else y = quantise<F, false, true>(x[i], s, inv);
+          *reinterpret_cast<uint2*>(tile_base + (off + row) * row_bytes + col) = y;
+        }
+      }
+    }
+    if (j != slots - 1) break;  // only a sequence's last slot goes on to the next block
+  }
+}
+
+// --------------------------------- read-back ---------------------------------
+
+template <typename T>
+struct Pack;  // four fp32 values of a 16-byte store, or eight of a 16-bit one
+template <>
+struct Pack<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ uint4 pack(const float* x) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+  }
+};
+template <typename F>
+struct Pack16 {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ uint4 pack(const float* x) {
+    return make_uint4(F::pack2(x[0], x[1]), F::pack2(x[2], x[3]), F::pack2(x[4], x[5]),
+                      F::pack2(x[6], x[7]));
+  }
+};
+template <>
+struct Pack<Bf16> : Pack16<Bf16> {};
+template <>
+struct Pack<Fp16> : Pack16<Fp16> {};
+
+struct GatherParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* lens;
+  const int64_t* cu_rows;
+  uint4* k_out;
+  uint4* v_out;
+  int* err;
+  int64_t num_blocks, out_rows;
+  int block_size, max_blocks, max_len, Hkv, D;
+};
+
+constexpr int kGatherThreads = 256;
+constexpr int kGatherVec = 4;  // vectors in flight per thread
+
+// grid (pages, sequences, 2): one block's tokens of K (z = 0) or V. A block's
+// rows are contiguous in the cache and in the output.
+template <typename T>
+__global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const GatherParams p) {
+  constexpr int E = Pack<T>::n;  // elements of an output vector
+  const int b = blockIdx.y, page = blockIdx.x;
+  int L = __ldg(p.lens + b);
+  if (L > p.max_len || L < 0) {
+    if (page == 0 && blockIdx.z == 0 && threadIdx.x == 0) record(p.err, kErrContextLen, b);
+    L = L < 0 ? 0 : p.max_len;
+  }
+  const int t0 = page * p.block_size;
+  if (t0 >= L) return;
+  const int nr = min(p.block_size, L - t0);
+  const int blk = __ldg(p.table + (int64_t)b * p.max_blocks + page);
+  const int64_t row0 = __ldg(p.cu_rows + b) + t0;
+  if (blk < 0 || blk >= p.num_blocks || row0 < 0 || row0 + nr > p.out_rows) {
+    if (threadIdx.x == 0) record(p.err, kErrBlockId, b);
+    return;
+  }
+  const bool is_v = blockIdx.z != 0;
+  const int64_t row_elems = (int64_t)p.Hkv * p.D;
+  const uint8_t* src = (is_v ? p.v : p.k) + (int64_t)blk * p.block_size * row_elems;
+  uint4* dst = (is_v ? p.v_out : p.k_out) + row0 * row_elems / E;
+  const float* sc = (is_v ? p.v_scale : p.k_scale) + (int64_t)blk * p.Hkv;
+  const int n = nr * (int)row_elems / E;
+  const int per_head = p.D / E;
+  for (int i0 = threadIdx.x; i0 < n; i0 += kGatherThreads * kGatherVec) {
+    uint2 w[kGatherVec];
+    float s[kGatherVec];
+#pragma unroll
+    for (int t = 0; t < kGatherVec; ++t) {
+      const int i = i0 + t * kGatherThreads;
+      if (i < n) {
+        if constexpr (E == 8) w[t] = __ldg(reinterpret_cast<const uint2*>(src) + i);
+        else w[t].x = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
+        s[t] = __ldg(sc + (i / per_head) % p.Hkv);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kGatherVec; ++t) {
+      const int i = i0 + t * kGatherThreads;
+      if (i < n) {
+        float x[8];
+        float y[4];
+        e4m3x4_to_float(w[t].x, y);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = y[q] * s[t];
+        if constexpr (E == 8) {
+          e4m3x4_to_float(w[t].y, y);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[4 + q] = y[q] * s[t];
+        }
+        dst[i] = Pack<T>::pack(x);
+      }
+    }
+  }
+}
+
+// ----------------------------------- host -----------------------------------
+
+int fail(int code, const std::string& msg) { return set_last_error(code, msg.c_str()); }
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Selects `device` for the scope and restores the caller's.
+struct Dev {
+  int prev = -1;
+  cudaError_t err = cudaSuccess;
+  explicit Dev(int d) {
+    err = cudaGetDevice(&prev);
+    if (err == cudaSuccess && prev != d) err = cudaSetDevice(d);
+    else prev = -1;
+  }
+  ~Dev() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(PDA_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return PDA_OK;
+}
+
+Rows span(const void* p, int64_t bytes) {
+  return Rows{(int64_t)reinterpret_cast<uintptr_t>(p), bytes, p ? bytes : 0, 1};
+}
+
+// Geometry that the FP8 decode kernels read.
+int check_cache(int num_kv_heads, int head_dim, int block_size, int64_t num_blocks) {
+  if (num_kv_heads < 1 || num_kv_heads > 65535)
+    return fail(PDA_EINVAL, "num_kv_heads must be in [1, 65535]");
+  if (head_dim < 1 || block_size < 1) return fail(PDA_EINVAL, "head_dim and block_size must be positive");
+  if (head_dim != 64 && head_dim != 128) return fail(PDA_EUNSUPPORTED, "head_dim must be 64 or 128");
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(PDA_EUNSUPPORTED, "block_size must be 16, 32 or 64");
+  if (num_blocks < 1 || num_blocks * block_size > (int64_t)INT_MAX)
+    return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
+  return PDA_OK;
+}
+
+template <typename F, int D, int NV, int W>
+void launch_append(const AppendParams& p, int rope, unsigned grid, cudaStream_t s) {
+  if (rope == kRopeNone) append_kernel<F, D, NV, W, kRopeNone><<<grid, kAppendThreads, 0, s>>>(p);
+  else if (rope == kRopeHalves) append_kernel<F, D, NV, W, kRopeHalves><<<grid, kAppendThreads, 0, s>>>(p);
+  else append_kernel<F, D, NV, W, kRopePairs><<<grid, kAppendThreads, 0, s>>>(p);
+}
+
+template <typename F>
+void launch_append_geometry(const AppendParams& p, int D, int rope, unsigned grid, cudaStream_t s) {
+  // NV * W * 256 = block_size * D / 8 vectors of a tile
+  const int tile = p.block_size * D;
+  if (D == 64) {
+    if (tile == 1024) launch_append<F, 64, 4, 1>(p, rope, grid, s);
+    else if (tile == 2048) launch_append<F, 64, 8, 1>(p, rope, grid, s);
+    else launch_append<F, 64, 16, 1>(p, rope, grid, s);
+  } else {
+    if (tile == 2048) launch_append<F, 128, 8, 1>(p, rope, grid, s);
+    else if (tile == 4096) launch_append<F, 128, 16, 1>(p, rope, grid, s);
+    else launch_append<F, 128, 16, 2>(p, rope, grid, s);
+  }
+}
+
+// Both append entry points; rope == kRopeNone: no q, no positions.
+int append_impl(AppendParams p, int D, int dtype, int rope, int device, void* stream) {
+  if (p.B < 0 || p.T < 0 || p.T > INT_MAX || p.max_blocks < 0 || device < 0)
+    return fail(PDA_EINVAL, "negative size or device, or num_rows >= 2^31");
+  if (dtype != PDA_BF16 && dtype != PDA_FP16) return fail(PDA_EINVAL, "dtype must be bf16 or fp16");
+  const int st = check_cache(p.Hkv, D, p.block_size, p.num_blocks);
+  if (st != PDA_OK) return st;
+  const int64_t hkv_d = (int64_t)p.Hkv * D, hq_d = (int64_t)p.Hq * D;
+  if (p.k_stride == 0) p.k_stride = hkv_d;
+  if (p.v_stride == 0) p.v_stride = hkv_d;
+  if (p.k_stride < hkv_d || p.v_stride < hkv_d)
+    return fail(PDA_EINVAL, "a token stride is smaller than its row of heads");
+  if ((p.k_stride | p.v_stride) % 8 != 0)
+    return fail(PDA_EINVAL, "token strides must be multiples of 8 elements (16 bytes)");
+  if (rope != kRopeNone) {
+    if (p.Hq < 1 || p.Hq > 65535) return fail(PDA_EINVAL, "num_q_heads must be in [1, 65535]");
+    if (p.rot_dim < 0 || p.rot_dim > D || p.rot_dim % 16 != 0)
+      return fail(PDA_EINVAL, "rot_dim must be a multiple of 16 in [0, head_dim]");
+    if (p.max_position < 0) return fail(PDA_EINVAL, "max_position < 0");
+    if (p.q_stride == 0) p.q_stride = hq_d;
+    if (p.qo_stride == 0) p.qo_stride = hq_d;
+    if (p.q_stride < hq_d || p.qo_stride < hq_d)
+      return fail(PDA_EINVAL, "a token stride is smaller than its row of heads");
+    if ((p.q_stride | p.qo_stride) % 8 != 0)
+      return fail(PDA_EINVAL, "token strides must be multiples of 8 elements (16 bytes)");
+  }
+  if (p.B == 0 || p.T == 0) return PDA_OK;
+  if (p.max_blocks < 1) return fail(PDA_EINVAL, "max_blocks < 1");
+  if (!p.k || !p.v || !p.k_cache || !p.v_cache || !p.k_scale || !p.v_scale || !p.table || !p.lens ||
+      !p.cu || (rope != kRopeNone && (!p.q || !p.q_out || !p.positions || (p.rot_dim > 0 && !p.cos_sin))))
+    return fail(PDA_EINVAL, "a required pointer is NULL");
+  if (!aligned(p.k, 16) || !aligned(p.v, 16) || !aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) ||
+      !aligned(p.q, 16) || !aligned(p.q_out, 16) || !aligned(p.cos_sin, 16))
+    return fail(PDA_EINVAL, "rows, caches and the cos/sin table must be 16-byte aligned");
+  if (!aligned(p.k_scale, 4) || !aligned(p.v_scale, 4) || !aligned(p.table, 4) ||
+      !aligned(p.lens, 4) || !aligned(p.cu, 8) || !aligned(p.positions, 4) || !aligned(p.err, 4))
+    return fail(PDA_EINVAL, "misaligned scales or index arrays");
+  auto rows = [&](const void* x, int64_t stride, int64_t len) {
+    return Rows{(int64_t)reinterpret_cast<uintptr_t>(x), stride * 2, x ? len * 2 : 0, p.T};
+  };
+  const int64_t cache_bytes = p.num_blocks * p.block_size * hkv_d;
+  const int64_t scale_bytes = p.num_blocks * p.Hkv * 4;
+  const Rows outs[6] = {span(p.k_cache, cache_bytes), span(p.v_cache, cache_bytes),
+                        span(p.k_scale, scale_bytes), span(p.v_scale, scale_bytes),
+                        span(p.err, 8), rows(p.q_out, p.qo_stride, hq_d)};
+  const Rows ins[7] = {rows(p.k, p.k_stride, hkv_d), rows(p.v, p.v_stride, hkv_d),
+                       span(p.table, (int64_t)p.B * p.max_blocks * 4), span(p.lens, p.B * 4ll),
+                       span(p.cu, (p.B + 1) * 8ll), span(p.positions, p.T * 4),
+                       span(p.cos_sin, (int64_t)p.max_position * p.rot_dim * 4)};
+  const Rows rq = rows(p.q, p.q_stride, hq_d);
+  for (int o = 0; o < 6; ++o) {
+    for (const Rows& in : ins)
+      if (overlaps(outs[o], in)) return fail(PDA_EALIAS, "an output overlaps an input");
+    for (int j = o + 1; j < 6; ++j)
+      if (overlaps(outs[o], outs[j])) return fail(PDA_EALIAS, "two outputs overlap");
+    if (o < 5 && overlaps(outs[o], rq)) return fail(PDA_EALIAS, "an output overlaps q");
+  }
+  const bool q_in_place = p.q == p.q_out && p.q_stride == p.qo_stride;
+  if (rope != kRopeNone && !q_in_place && overlaps(outs[5], rq))
+    return fail(PDA_EALIAS, "q_out overlaps q (only the exact in-place form is allowed)");
+
+  const int W = (p.block_size * D == 8192) ? 2 : 1;  // warps per tile
+  const int tiles = kAppendWarps / W;
+  p.groups = (2 * p.Hkv + tiles - 1) / tiles;
+  p.kv_ctas = (p.T / p.block_size + p.B) * p.groups;
+  const int64_t grid = p.kv_ctas + (rope != kRopeNone ? (p.T + kAppendWarps - 1) / kAppendWarps : 0);
+  if (grid > INT_MAX) return fail(PDA_EINVAL, "too many rows for one launch");
+  Dev guard(device);
+  if (guard.err != cudaSuccess) return fail(PDA_ECUDA, "cudaSetDevice failed");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == PDA_BF16) launch_append_geometry<Bf16>(p, D, rope, (unsigned)grid, s);
+  else launch_append_geometry<Fp16>(p, D, rope, (unsigned)grid, s);
+  return launched("append launch");
+}
+
+}  // namespace
+}  // namespace pda
+
+using pda::fail;
+
+extern "C" int paged_decode_attn_append_kv_fp8(
+    const void* k, int64_t k_token_stride, const void* v, int64_t v_token_stride, int64_t num_rows,
+    int num_kv_heads, int head_dim, int dtype, void* k_cache, void* v_cache, float* k_scale,
+    float* v_scale, int64_t num_blocks, int block_size, const int32_t* block_table, int max_blocks,
+    const int32_t* context_lens, const int64_t* cu_rows, int batch, int* err, int device,
+    void* stream) {
+  pda::AppendParams p = {};
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_stride = k_token_stride;
+  p.v_stride = v_token_stride;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.lens = context_lens;
+  p.cu = cu_rows;
+  p.err = err;
+  p.num_blocks = num_blocks;
+  p.T = num_rows;
+  p.B = batch;
+  p.Hkv = num_kv_heads;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  return pda::append_impl(p, head_dim, dtype, pda::kRopeNone, device, stream);
+}
+
+extern "C" int paged_decode_attn_rope_append_kv_fp8(
+    const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,
+    int64_t v_token_stride, const int32_t* positions, const float* cos_sin_cache,
+    int max_position, int rot_dim, int neox_style, int64_t num_rows, int num_q_heads,
+    int num_kv_heads, int head_dim, int dtype, void* q_out, int64_t q_out_token_stride,
+    void* k_cache, void* v_cache, float* k_scale, float* v_scale, int64_t num_blocks,
+    int block_size, const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+    const int64_t* cu_rows, int batch, int* err, int device, void* stream) {
+  pda::AppendParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_token_stride;
+  p.k_stride = k_token_stride;
+  p.v_stride = v_token_stride;
+  p.qo_stride = q_out_token_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin_cache;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.lens = context_lens;
+  p.cu = cu_rows;
+  p.err = err;
+  p.num_blocks = num_blocks;
+  p.T = num_rows;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  p.max_position = max_position;
+  p.rot_dim = rot_dim;
+  return pda::append_impl(p, head_dim, dtype, neox_style ? pda::kRopeHalves : pda::kRopePairs,
+                          device, stream);
+}
+
+extern "C" int paged_decode_attn_gather_kv_fp8(
+    const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+    int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+    const int32_t* block_table, int max_blocks, const int32_t* lens, const int64_t* cu_rows,
+    int batch, int max_len, void* k_out, void* v_out, int64_t out_rows, int out_dtype, int* err,
+    int device, void* stream) {
+  if (max_blocks < 0 || batch < 0 || max_len < 0 || out_rows < 0 || device < 0)
+    return fail(PDA_EINVAL, "negative size or device");
+  if (batch > 65535) return fail(PDA_EINVAL, "batch > 65535");
+  if (out_dtype != PDA_BF16 && out_dtype != PDA_FP16 && out_dtype != PDA_F32)
+    return fail(PDA_EINVAL, "out_dtype must be PDA_BF16, PDA_FP16 or PDA_F32");
+  const int st = pda::check_cache(num_kv_heads, head_dim, block_size, num_blocks);
+  if (st != PDA_OK) return st;
+  if ((int64_t)num_kv_heads * head_dim * block_size > INT_MAX)
+    return fail(PDA_EINVAL, "a block holds more than 2^31 values");
+  if (batch == 0 || max_len == 0) return PDA_OK;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !lens || !cu_rows ||
+      (out_rows > 0 && (!k_out || !v_out)))
+    return fail(PDA_EINVAL, "a required pointer is NULL");
+  if (!pda::aligned(k_cache, 16) || !pda::aligned(v_cache, 16) || !pda::aligned(k_out, 16) ||
+      !pda::aligned(v_out, 16) || !pda::aligned(k_scale, 4) || !pda::aligned(v_scale, 4) ||
+      !pda::aligned(block_table, 4) || !pda::aligned(lens, 4) || !pda::aligned(cu_rows, 8) ||
+      !pda::aligned(err, 4))
+    return fail(PDA_EINVAL, "misaligned pointer");
+  if ((int64_t)max_len > (int64_t)max_blocks * block_size)
+    return fail(PDA_EINVAL, "max_len exceeds max_blocks * block_size");
+  const int64_t elems = out_rows * num_kv_heads * head_dim;
+  const int64_t out_bytes = elems * (out_dtype == PDA_F32 ? 4 : 2);
+  const int64_t cache_bytes = num_blocks * block_size * num_kv_heads * head_dim;
+  const pda::Rows outs[3] = {pda::span(k_out, out_bytes), pda::span(v_out, out_bytes),
+                             pda::span(err, 8)};
+  const pda::Rows ins[7] = {pda::span(k_cache, cache_bytes), pda::span(v_cache, cache_bytes),
+                            pda::span(k_scale, num_blocks * num_kv_heads * 4),
+                            pda::span(v_scale, num_blocks * num_kv_heads * 4),
+                            pda::span(block_table, (int64_t)batch * max_blocks * 4),
+                            pda::span(lens, batch * 4ll), pda::span(cu_rows, batch * 8ll)};
+  for (int o = 0; o < 3; ++o) {
+    for (const pda::Rows& in : ins)
+      if (pda::overlaps(outs[o], in)) return fail(PDA_EALIAS, "an output overlaps an input");
+    for (int j = o + 1; j < 3; ++j)
+      if (pda::overlaps(outs[o], outs[j])) return fail(PDA_EALIAS, "two outputs overlap");
+  }
+  pda::GatherParams p;
+  p.k = static_cast<const uint8_t*>(k_cache);
+  p.v = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.lens = lens;
+  p.cu_rows = cu_rows;
+  p.k_out = static_cast<uint4*>(k_out);
+  p.v_out = static_cast<uint4*>(v_out);
+  p.err = err;
+  p.num_blocks = num_blocks;
+  p.out_rows = out_rows;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  p.max_len = max_len;
+  p.Hkv = num_kv_heads;
+  p.D = head_dim;
+  pda::Dev guard(device);
+  if (guard.err != cudaSuccess) return fail(PDA_ECUDA, "cudaSetDevice failed");
+  const dim3 grid((unsigned)((max_len + block_size - 1) / block_size), (unsigned)batch, 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (out_dtype == PDA_BF16) pda::gather_fp8_kernel<pda::Bf16><<<grid, pda::kGatherThreads, 0, s>>>(p);
+  else if (out_dtype == PDA_FP16) pda::gather_fp8_kernel<pda::Fp16><<<grid, pda::kGatherThreads, 0, s>>>(p);
+  else pda::gather_fp8_kernel<float><<<grid, pda::kGatherThreads, 0, s>>>(p);
+  return pda::launched("gather launch");
+}
