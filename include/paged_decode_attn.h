@@ -406,6 +406,20 @@ int paged_decode_attn_gather_kv_fp8(const void* k_cache, const void* v_cache,
                                     int max_len, void* k_out, void* v_out, int64_t out_rows,
                                     int out_dtype, int* err, int device, void* stream);
 
+/* Decode attention over a block-scaled cache (handle created with kv_fp8):
+ * paged_decode_attn_run_ex with
+ *   k_t = k_scale[blk, h] * k_cache[blk, t % block_size, h, :],  v_t alike,
+ * blk = block_table[b, t / block_size]. k_scale and v_scale are [num_blocks,
+ * Hkv] fp32, finite and >= 0, whatever wrote them (powers of two or not); a
+ * block id outside [0, num_blocks) reads zeros. The largest and the smallest
+ * nonzero V scale that a sequence uses may lie a factor of 2^100 apart. */
+int paged_decode_attn_run_block_scaled(pda_handle handle, const void* q, const void* k_cache,
+                                       const void* v_cache, const float* k_scale,
+                                       const float* v_scale, const int32_t* block_table,
+                                       const int32_t* context_lens, int batch, int max_blocks,
+                                       int64_t num_blocks, float scale, void* out, void* stream,
+                                       int num_splits, int max_context_len_hint, int out_dtype);
+
 /* Decode attention for callers that cannot allocate device memory.
  * (No counterpart in the paper: this entry point exists for integration.)
  *

@@ -49,6 +49,7 @@ EXPORTS = [
     "paged_decode_attn_append_kv_fp8",
     "paged_decode_attn_rope_append_kv_fp8",
     "paged_decode_attn_gather_kv_fp8",
+    "paged_decode_attn_run_block_scaled",
 ]
 
 
@@ -125,6 +126,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.paged_decode_attn_scatter_kv.restype = I
         lib.paged_decode_attn_remap_table.argtypes = [P, I, I, P, I, P, I64, P, I, P]
         lib.paged_decode_attn_remap_table.restype = I
+        lib.paged_decode_attn_run_block_scaled.argtypes = [P, P, P, P, P, P, P, P, I, I, I64, F, P,
+                                                           P, I, I, I]
+        lib.paged_decode_attn_run_block_scaled.restype = I
         cache_args = [P, P, P, P, I64, I, P, I, P, P, I, P, I, P]
         lib.paged_decode_attn_append_kv_fp8.argtypes = [P, I64, P, I64, I64, I, I, I] + cache_args
         lib.paged_decode_attn_append_kv_fp8.restype = I
@@ -226,7 +230,8 @@ class PagedDecodeAttention:
         """out[B, Hq, D] = paged decode attention; asynchronous on ``stream``
         (default: torch's current stream). With FP8 caches (kv_fp8), k_cache
         and v_cache are torch.float8_e4m3fn (or uint8) tensors; k_scale and
-        v_scale are fp32 device tensors of Hkv (per kv head) or 1 values."""
+        v_scale are fp32 device tensors of Hkv (per kv head) or 1 values, or,
+        for a block-scaled cache (append_kv_fp8), both [num_blocks, Hkv]."""
         c = self.config
         B = q.shape[0]
         if scale is None:
@@ -243,6 +248,23 @@ class PagedDecodeAttention:
         else:
             kp = _dev_ptr(k_cache, "k_cache", self.dtype)
             vp = _dev_ptr(v_cache, "v_cache", self.dtype)
+        if self.kv_fp8 and any(t is not None and t.dim() == 2 for t in (k_scale, v_scale)):
+            want = (k_cache.shape[0], c.num_kv_heads)
+            if k_scale is None or v_scale is None or k_scale.shape != want or v_scale.shape != want:
+                raise ValueError("block scales: k_scale and v_scale must both be [num_blocks, Hkv]")
+            _same_device(q.device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
+                         v_scale=v_scale, block_table=block_table, context_lens=context_lens,
+                         out=out)
+            _check(self.lib, self.lib.paged_decode_attn_run_block_scaled(
+                self.handle, _dev_ptr(q, "q", self.dtype), kp, vp,
+                _dev_ptr(k_scale, "k_scale", torch.float32),
+                _dev_ptr(v_scale, "v_scale", torch.float32),
+                _dev_ptr(block_table, "block_table", torch.int32),
+                _dev_ptr(context_lens, "context_lens", torch.int32), B, block_table.shape[1],
+                k_cache.shape[0], float(scale), _dev_ptr(out, "out", out_dtype),
+                _stream_on(stream, self.device), int(num_splits), int(max_context_len_hint),
+                _DT[out_dtype]))
+            return out
         per_head = 0
         for t in (k_scale, v_scale):
             if t is not None:

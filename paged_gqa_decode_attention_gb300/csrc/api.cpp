@@ -324,6 +324,130 @@ LaunchShape launch_shape(const pda_handle_s* h, int batch, int max_blocks, int h
   return r;
 }
 
+// Every run call. block_scales: k_scale and v_scale are [num_blocks, Hkv].
+int run_any(pda_handle h, const void* q, const void* k_cache, const void* v_cache,
+            const int32_t* block_table, const int32_t* context_lens, int batch, int max_blocks,
+            int64_t num_blocks, float scale, const float* k_scale, const float* v_scale,
+            int scale_per_head, bool block_scales, void* out, void* stream, int num_splits,
+            int max_context_len_hint, int out_dtype) {
+  if (!h) return fail(PDA_EINVAL, "handle is NULL");
+  const pda_config& c = h->cfg;
+  if (batch < 0 || batch > c.max_batch) return fail(PDA_EINVAL, "batch out of [0, max_batch]");
+  if (batch == 0) return PDA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !context_lens || !out)
+    return fail(PDA_EINVAL, "a tensor pointer is NULL");
+  if (block_scales && !c.kv_fp8)
+    return fail(PDA_EINVAL, "block scales need a handle with kv_fp8");
+  if (block_scales && (!k_scale || !v_scale))
+    return fail(PDA_EINVAL, "k_scale and v_scale must hold [num_blocks, Hkv] block scales");
+  if (max_blocks < 1 || max_blocks > c.max_blocks_per_seq)
+    return fail(PDA_EINVAL, "max_blocks out of [1, max_blocks_per_seq]");
+  if (num_blocks < 1 || num_blocks * c.block_size > (int64_t)INT_MAX)
+    return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
+  if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
+  if (num_splits < 0 || num_splits > c.max_splits)
+    return fail(PDA_EINVAL, "num_splits out of [0, max_splits]");
+  if (max_context_len_hint < 0) return fail(PDA_EINVAL, "max_context_len_hint < 0");
+  if (out_dtype == -1) out_dtype = c.dtype;
+  if (out_dtype != c.dtype && out_dtype != PDA_F32)
+    return fail(PDA_EINVAL, "out_dtype must be -1, the input dtype or PDA_F32");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return fail(PDA_EINVAL, "q, k_cache, v_cache and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens)) & 3u)
+    return fail(PDA_EINVAL, "block_table and context_lens must be 4-byte aligned");
+
+  if (scale_per_head != 0 && scale_per_head != 1)
+    return fail(PDA_EINVAL, "scale_per_head must be 0 or 1");
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
+    return fail(PDA_EINVAL, "k_scale and v_scale must be 4-byte aligned");
+  const size_t esz = 2;
+  const size_t kv_esz = c.kv_fp8 ? 1 : 2;
+  const size_t out_esz = out_dtype == PDA_F32 ? 4 : 2;
+  const size_t n_q = (size_t)batch * c.num_q_heads * c.head_dim;
+  const size_t cache_bytes =
+      (size_t)num_blocks * c.block_size * c.num_kv_heads * c.head_dim * kv_esz;
+  const size_t scale_bytes =
+      (block_scales ? (size_t)num_blocks * c.num_kv_heads : scale_per_head ? (size_t)c.num_kv_heads : 1) * 4;
+  const size_t out_bytes = n_q * out_esz;
+  if (overlaps(out, out_bytes, q, n_q * esz) || overlaps(out, out_bytes, k_cache, cache_bytes) ||
+      overlaps(out, out_bytes, v_cache, cache_bytes) ||
+      overlaps(out, out_bytes, block_table, (size_t)batch * max_blocks * 4) ||
+      overlaps(out, out_bytes, context_lens, (size_t)batch * 4) ||
+      overlaps(out, out_bytes, k_scale, k_scale ? scale_bytes : 0) ||
+      overlaps(out, out_bytes, v_scale, v_scale ? scale_bytes : 0))
+    return fail(PDA_EALIAS, "out overlaps an input");
+
+  DeviceGuard guard(c.device);
+  if (guard.err != cudaSuccess) return cuda_fail("cudaSetDevice", guard.err);
+
+  if (h->tm_k != k_cache || h->tm_v != v_cache || h->tm_nb != num_blocks) {
+    int st = encode_cache_map(&h->tmap_k, k_cache, c.num_kv_heads, c.head_dim, c.block_size,
+                              num_blocks, c.kv_fp8 != 0);
+    if (st == PDA_OK)
+      st = encode_cache_map(&h->tmap_v, v_cache, c.num_kv_heads, c.head_dim, c.block_size,
+                            num_blocks, c.kv_fp8 != 0);
+    if (st != PDA_OK) {
+      h->tm_k = h->tm_v = nullptr;
+      h->tm_nb = -1;
+      return st;
+    }
+    h->tm_k = k_cache;
+    h->tm_v = v_cache;
+    h->tm_nb = num_blocks;
+  }
+
+  const LaunchShape shape =
+      launch_shape(h, batch, max_blocks, max_context_len_hint, num_splits);
+  const int S = shape.splits, chunk = shape.chunk_pages;
+  const int64_t units = shape.units;
+  if (units > INT_MAX) return fail(PDA_EINVAL, "splits * num_kv_heads * batch exceeds 2^31");
+  alignas(64) CUtensorMap tmap_q;
+  if (shape.kernel == pda::kPartialTensorCore) {
+    int st = encode_q_map(&tmap_q, q, (int64_t)batch * c.num_q_heads, c.head_dim, h->group);
+    if (st != PDA_OK) return st;
+  } else {
+    std::memset(&tmap_q, 0, sizeof tmap_q);
+  }
+
+  pda::PartialParams p;
+  p.q = q;
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.ws_o = h->ws_o;
+  p.ws_lse = h->ws_lse;
+  p.err = h->err;
+  p.counters = h->counters;
+  p.sched = h->counters + (size_t)c.max_batch * c.num_kv_heads;
+  p.Hq = c.num_q_heads;
+  p.Hkv = c.num_kv_heads;
+  p.max_blocks = max_blocks;
+  p.chunk_pages = chunk;
+  p.num_splits = S;
+  p.qscale = scale * pda::kLog2e;
+  p.num_units = (int)units;
+  p.max_ctas = h->num_sms * shape.ctas_per_sm;
+  p.out_f32 = out_dtype == PDA_F32;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.scale_per_head = scale_per_head;
+  p.cluster = shape.cluster;
+  p.num_blocks = num_blocks;
+  if (h->test_stall_runs > 0 && shape.kernel == pda::kPartialTensorCore) {
+    --h->test_stall_runs;
+    p.stall_units = 1;
+    p.wait_ns = 1000ull * 1000ull;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = pda::launch_partial(shape.kernel, h->group, c.head_dim, c.block_size, c.dtype,
+                                      block_scales    ? pda::kKvFp8Block
+                                      : c.kv_fp8 != 0 ? pda::kKvFp8
+                                                      : pda::kKv16,
+                                      &h->tmap_k, &h->tmap_v, &tmap_q, p, batch, s);
+  if (e != cudaSuccess) return cuda_fail("partial kernel launch", e);
+  return PDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -372,7 +496,11 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
   // records error code 3 and the next run must be exact.
   if (const char* env = std::getenv("PDA_TEST_STALL_RUNS"))
     if (h->kernel == pda::kPartialTensorCore) h->test_stall_runs = std::atoi(env);
-  e = pda::partial_prepare(h->kernel, h->group, cfg->head_dim, cfg->block_size, cfg->dtype, kv8);
+  e = pda::partial_prepare(h->kernel, h->group, cfg->head_dim, cfg->block_size, cfg->dtype,
+                           kv8 ? pda::kKvFp8 : pda::kKv16);
+  if (e == cudaSuccess && kv8)  // either call may follow on an FP8 handle
+    e = pda::partial_prepare(h->kernel, h->group, cfg->head_dim, cfg->block_size, cfg->dtype,
+                             pda::kKvFp8Block);
   if (e != cudaSuccess) {
     delete h;
     return cuda_fail("cudaFuncSetAttribute", e);
@@ -391,7 +519,7 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
   h->ctas_per_sm = occ < hint ? occ : hint;
   if (h->small_cc) {
     e = pda::partial_prepare(pda::kPartialCudaCore, h->group, cfg->head_dim, cfg->block_size,
-                             cfg->dtype, false);
+                             cfg->dtype, pda::kKv16);
     if (e != cudaSuccess) {
       delete h;
       return cuda_fail("cudaFuncSetAttribute", e);
@@ -474,114 +602,20 @@ int paged_decode_attn_run_scaled(pda_handle h, const void* q, const void* k_cach
                                  const float* v_scale, int scale_per_head, void* out,
                                  void* stream, int num_splits, int max_context_len_hint,
                                  int out_dtype) {
-  if (!h) return fail(PDA_EINVAL, "handle is NULL");
-  const pda_config& c = h->cfg;
-  if (batch < 0 || batch > c.max_batch) return fail(PDA_EINVAL, "batch out of [0, max_batch]");
-  if (batch == 0) return PDA_OK;
-  if (!q || !k_cache || !v_cache || !block_table || !context_lens || !out)
-    return fail(PDA_EINVAL, "a tensor pointer is NULL");
-  if (max_blocks < 1 || max_blocks > c.max_blocks_per_seq)
-    return fail(PDA_EINVAL, "max_blocks out of [1, max_blocks_per_seq]");
-  if (num_blocks < 1 || num_blocks * c.block_size > (int64_t)INT_MAX)
-    return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
-  if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
-  if (num_splits < 0 || num_splits > c.max_splits)
-    return fail(PDA_EINVAL, "num_splits out of [0, max_splits]");
-  if (max_context_len_hint < 0) return fail(PDA_EINVAL, "max_context_len_hint < 0");
-  if (out_dtype == -1) out_dtype = c.dtype;
-  if (out_dtype != c.dtype && out_dtype != PDA_F32)
-    return fail(PDA_EINVAL, "out_dtype must be -1, the input dtype or PDA_F32");
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
-    return fail(PDA_EINVAL, "q, k_cache, v_cache and out must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens)) & 3u)
-    return fail(PDA_EINVAL, "block_table and context_lens must be 4-byte aligned");
+  return run_any(h, q, k_cache, v_cache, block_table, context_lens, batch, max_blocks, num_blocks,
+                 scale, k_scale, v_scale, scale_per_head, false, out, stream, num_splits,
+                 max_context_len_hint, out_dtype);
+}
 
-  if (scale_per_head != 0 && scale_per_head != 1)
-    return fail(PDA_EINVAL, "scale_per_head must be 0 or 1");
-  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
-    return fail(PDA_EINVAL, "k_scale and v_scale must be 4-byte aligned");
-  const size_t esz = 2;
-  const size_t kv_esz = c.kv_fp8 ? 1 : 2;
-  const size_t out_esz = out_dtype == PDA_F32 ? 4 : 2;
-  const size_t n_q = (size_t)batch * c.num_q_heads * c.head_dim;
-  const size_t cache_bytes =
-      (size_t)num_blocks * c.block_size * c.num_kv_heads * c.head_dim * kv_esz;
-  const size_t scale_bytes = (scale_per_head ? (size_t)c.num_kv_heads : 1) * 4;
-  const size_t out_bytes = n_q * out_esz;
-  if (overlaps(out, out_bytes, q, n_q * esz) || overlaps(out, out_bytes, k_cache, cache_bytes) ||
-      overlaps(out, out_bytes, v_cache, cache_bytes) ||
-      overlaps(out, out_bytes, block_table, (size_t)batch * max_blocks * 4) ||
-      overlaps(out, out_bytes, context_lens, (size_t)batch * 4) ||
-      overlaps(out, out_bytes, k_scale, k_scale ? scale_bytes : 0) ||
-      overlaps(out, out_bytes, v_scale, v_scale ? scale_bytes : 0))
-    return fail(PDA_EALIAS, "out overlaps an input");
-
-  DeviceGuard guard(c.device);
-  if (guard.err != cudaSuccess) return cuda_fail("cudaSetDevice", guard.err);
-
-  if (h->tm_k != k_cache || h->tm_v != v_cache || h->tm_nb != num_blocks) {
-    int st = encode_cache_map(&h->tmap_k, k_cache, c.num_kv_heads, c.head_dim, c.block_size,
-                              num_blocks, c.kv_fp8 != 0);
-    if (st == PDA_OK)
-      st = encode_cache_map(&h->tmap_v, v_cache, c.num_kv_heads, c.head_dim, c.block_size,
-                            num_blocks, c.kv_fp8 != 0);
-    if (st != PDA_OK) {
-      h->tm_k = h->tm_v = nullptr;
-      h->tm_nb = -1;
-      return st;
-    }
-    h->tm_k = k_cache;
-    h->tm_v = v_cache;
-    h->tm_nb = num_blocks;
-  }
-
-  const LaunchShape shape =
-      launch_shape(h, batch, max_blocks, max_context_len_hint, num_splits);
-  const int S = shape.splits, chunk = shape.chunk_pages;
-  const int64_t units = shape.units;
-  if (units > INT_MAX) return fail(PDA_EINVAL, "splits * num_kv_heads * batch exceeds 2^31");
-  alignas(64) CUtensorMap tmap_q;
-  if (shape.kernel == pda::kPartialTensorCore) {
-    int st = encode_q_map(&tmap_q, q, (int64_t)batch * c.num_q_heads, c.head_dim, h->group);
-    if (st != PDA_OK) return st;
-  } else {
-    std::memset(&tmap_q, 0, sizeof tmap_q);
-  }
-
-  pda::PartialParams p;
-  p.q = q;
-  p.block_table = block_table;
-  p.context_lens = context_lens;
-  p.out = out;
-  p.ws_o = h->ws_o;
-  p.ws_lse = h->ws_lse;
-  p.err = h->err;
-  p.counters = h->counters;
-  p.sched = h->counters + (size_t)c.max_batch * c.num_kv_heads;
-  p.Hq = c.num_q_heads;
-  p.Hkv = c.num_kv_heads;
-  p.max_blocks = max_blocks;
-  p.chunk_pages = chunk;
-  p.num_splits = S;
-  p.qscale = scale * pda::kLog2e;
-  p.num_units = (int)units;
-  p.max_ctas = h->num_sms * shape.ctas_per_sm;
-  p.out_f32 = out_dtype == PDA_F32;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.scale_per_head = scale_per_head;
-  p.cluster = shape.cluster;
-  if (h->test_stall_runs > 0 && shape.kernel == pda::kPartialTensorCore) {
-    --h->test_stall_runs;
-    p.stall_units = 1;
-    p.wait_ns = 1000ull * 1000ull;
-  }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pda::launch_partial(shape.kernel, h->group, c.head_dim, c.block_size, c.dtype,
-                                      c.kv_fp8 != 0, &h->tmap_k, &h->tmap_v, &tmap_q, p, batch,
-                                      s);
-  if (e != cudaSuccess) return cuda_fail("partial kernel launch", e);
-  return PDA_OK;
+int paged_decode_attn_run_block_scaled(pda_handle h, const void* q, const void* k_cache,
+                                       const void* v_cache, const float* k_scale,
+                                       const float* v_scale, const int32_t* block_table,
+                                       const int32_t* context_lens, int batch, int max_blocks,
+                                       int64_t num_blocks, float scale, void* out, void* stream,
+                                       int num_splits, int max_context_len_hint, int out_dtype) {
+  return run_any(h, q, k_cache, v_cache, block_table, context_lens, batch, max_blocks, num_blocks,
+                 scale, k_scale, v_scale, 0, true, out, stream, num_splits, max_context_len_hint,
+                 out_dtype);
 }
 
 int paged_decode_attn_run(pda_handle h, const void* q, const void* k_cache, const void* v_cache,

@@ -157,6 +157,12 @@ __host__ __device__ constexpr int epi_heads(int G) { return G > 8 ? 16 : 8; }
 __host__ __device__ constexpr int epi_floats(int G) { return epi_heads(G) * 128 + 2 * epi_heads(G) + 4; }
 __host__ __device__ constexpr int epi_slots(int G, bool kv8) { return G > 8 && !kv8 ? 1 : 2; }
 constexpr float kP8Scale = 256.f;          // FP8 K/V: P is split at p * 256
+// Block-scaled FP8 K/V: the smallest V scale that enters a weight's exponent;
+// a smaller one (a block of zeros) multiplies the weight instead.
+constexpr float kMinBlockScale = 0x1p-60f;
+// fp8 terms of Q: two hold a bf16 exactly; the block-scaled kernel takes three
+// for fp16.
+__host__ __device__ constexpr int q_terms(bool fp16, bool bsc) { return fp16 && bsc ? 3 : 2; }
 
 // Shared-memory layout. 16-bit K/V at D 128: 3-slot rings of 32 KiB slots
 // (two 64-dim halves of 128 tokens). 16-bit K/V at D 64: 6-slot rings of
@@ -164,7 +170,15 @@ constexpr float kP8Scale = 256.f;          // FP8 K/V: P is split at p * 256
 // rings of 80 KiB in slots of one D-byte row per token (5 x 16 KiB at D 128,
 // 10 x 8 KiB at D 64 with 64-byte swizzled rows), two fp8 terms of Q next to
 // the 16-bit Q tile, three fp8 terms of P in the P buffers.
-template <bool KV8, int D = 128, int G = 8>
+//
+// Block-scaled FP8 K/V (BSC): QT fp8 terms of Q (three for fp16 queries, whose
+// 11 significant bits two E4M3 terms do not hold) and a ring of block scales,
+// [kScRing] x (kMaxPps K scales, kMaxPps V scales). The K producer fills
+// chunk c's entry when it issues the chunk's pages, that is after QK^T of chunk
+// c - kStages, whose issue waited for the softmax's read of S(c - kStages - 2);
+// the softmax reads a chunk's scales before it releases S, so kStages + 2
+// entries suffice without an "empty" barrier.
+template <bool KV8, int D = 128, int G = 8, bool BSC = false, int QT = 2>
 struct Layout {
   static constexpr int kStages = KV8 ? (D == 64 ? 10 : 5) : (D == 64 ? 6 : 3);
   static constexpr int kSlotBytes = KV8 ? kT * D : (D / 64) * kHalf;
@@ -172,20 +186,24 @@ struct Layout {
   static constexpr int kOffV = kStages * kSlotBytes;
   static constexpr int kOffQ = 2 * kStages * kSlotBytes;  // [2 buffers] Q tiles (TMA)
   static constexpr int kOffQ8 = kOffQ + 2 * kOpBytes;     // [2 buffers] fp8 Q terms (KV8)
-  static constexpr int kOffP = kOffQ8 + (KV8 ? 2 * kOpBytes : 0);  // [2 buffers] P operands
+  static constexpr int kQ8Bytes = QT * kOpHalf;           // one buffer of fp8 Q terms
+  static constexpr int kOffP = kOffQ8 + (KV8 ? 2 * kQ8Bytes : 0);  // [2 buffers] P operands
   // [2 buffers][epi_heads(G)] 1/sigma per row (KV8)
   static constexpr int kOffQs = kOffP + 4 * kOpBytes;
   // per softmax group: 2 x [4 warps][8] floats (chunk maxima), [4 warps][8] (final sums)
   static constexpr int kOffRed = kOffQs + 2 * epi_heads(G) * 4;
   static constexpr int kOffLred = kOffRed + 2 * 2 * 4 * 8 * 4;
   static constexpr int kOffBar = kOffLred + 2 * 4 * 8 * 4;
-  static constexpr int kNumBars = 4 * kStages + 14 + 2 * kUnitRing + 4 + 2 + 1;
+  static constexpr int kScRing = BSC ? kStages + 2 : 0;
+  static constexpr int kMaxPps = kT / 16;
+  static constexpr int kNumBars = 4 * kStages + 14 + 2 * kUnitRing + 4 + 2 + 1 + kScRing;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   // [kUnitRing] unit index + decoded unit, so no reader repeats its global loads
   static constexpr int kOffURing = kOffTmem + 16;
   static constexpr int kOffUBcast = kOffURing + kUnitRing * kUnitInts * 4;  // same, softmax warp 0 -> rest
   static constexpr int kOffEpiFlag = kOffUBcast + kUnitInts * 4;  // epilogue group's wait outcome
-  static constexpr int kOffEpi = (kOffEpiFlag + 4 + 15) & ~15;
+  static constexpr int kOffSc = (kOffEpiFlag + 4 + 15) & ~15;  // block scales (BSC)
+  static constexpr int kOffEpi = kOffSc + kScRing * 2 * kMaxPps * 4;
   static constexpr size_t kSmemBytes = 1024 + kOffEpi + epi_slots(G, KV8) * epi_floats(G) * 4;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -367,7 +385,7 @@ struct Cursor {
   }
 };
 
-template <int G, int D, int BS, bool FP16, bool KV8>
+template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
     paged_partial_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v,
@@ -377,8 +395,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   // bytes of one token row of one head in a K/V ring slot (FP8: D, 64-byte
   // swizzled rows at D 64; 16-bit: 128, one 64-dim half)
   constexpr int kKVRow = KV8 ? D : kRowBytes;
-  using L = Layout<KV8, D, G>;
+  static_assert(KV8 || !BSC, "block scales belong to FP8 caches");
+  constexpr int QT = q_terms(FP16, BSC);
+  using L = Layout<KV8, D, G, BSC, QT>;
   constexpr int kStages = L::kStages;
+  constexpr int kScRing = L::kScRing;
+  constexpr int kMaxPps = L::kMaxPps;
   constexpr int kSlotBytes = L::kSlotBytes;
   constexpr int kOffK = L::kOffK;
   constexpr int kOffV = L::kOffV;
@@ -439,6 +461,8 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   // cluster launches: every other CTA of the cluster has its split's partial
   // in its state slot (one arrival per other CTA)
   const uint32_t cl_bar = bar0 + 8u * (4 * kStages + 20 + 2 * kUnitRing);
+  // block scales: the scales of the chunk's pages are in ring entry s
+  auto sc_full = [&](int s) { return bar0 + 8u * (4 * kStages + 21 + 2 * kUnitRing + s); };
   volatile int* uring = reinterpret_cast<volatile int*>(base + kOffURing);
 
   const int warp = threadIdx.x >> 5;
@@ -579,6 +603,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
       mbar_init(q8_full(b2), 1);
     }
     if (p.cluster > 1) mbar_init(cl_bar, (uint32_t)(p.cluster - 1));
+    for (int s = 0; s < kScRing; ++s) mbar_init(sc_full(s), 32);
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -603,10 +628,28 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   // grid in the stream may still be writing (programmatic dependent launch).
   griddep_wait();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + kOffTmem);
-  constexpr int kSCols = KV8 ? 2 * kN : kN;  // S columns per buffer
+  constexpr int kSCols = KV8 ? QT * kN : kN;  // S columns per buffer
   constexpr int kOCols = KV8 ? 3 * kN : 2 * kN;  // O columns per buffer
   auto tS = [&](int b2) { return tmem + (uint32_t)(b2 * kSCols); };
   auto tO = [&](int b2) { return tmem + (uint32_t)(2 * kSCols + b2 * kOCols); };
+  static_assert(2 * (kSCols + kOCols) <= (int)kTmemCols, "TMEM columns");
+  // BSC, a K producer warp: lane i requests the K and V scale of page i of chunk
+  // c (block bl; one outside the cache gets 0, as its page reads zeros) into
+  // the chunk's ring entry. Asynchronous: nothing waits for them but the
+  // softmax, on sc_full.
+  auto load_scales = [&](int c, int npg, int bl, int h) {
+    if constexpr (BSC) {
+      const int e = c % kScRing;
+      if (lane < npg) {
+        const bool in = bl >= 0 && bl < p.num_blocks;
+        const int64_t i = in ? (int64_t)bl * p.Hkv + h : 0;
+        const uint32_t dst = base_u32 + L::kOffSc + (uint32_t)(e * 2 * kMaxPps + lane) * 4u;
+        cp_async_4(dst, p.k_scale + i, in);
+        cp_async_4(dst + kMaxPps * 4u, p.v_scale + i, in);
+      }
+      cp_async_arrive(sc_full(e));
+    }
+  };
 
   if (!kDual && (warp == kWarpProducerK || warp == kWarpProducerV)) {
     // one producer warp per ring (this loop measured a few percent faster
@@ -693,10 +736,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
           for (int bx = 0; bx < kBoxes; ++bx)
             tma_load_2d(st + bx * kHalf + ro, map, U.h * D + bx * kBoxElems, bl * BS, fb);
         }
+        if (BSC && r == 0) load_scales(c, npg, bl, U.h);
       }
       __syncwarp();
       if (r == 0) cur_k.advance(p, fetch); else cur_v.advance(p, ring);
     }
+    if constexpr (BSC) cp_async_wait_all();  // none in flight at exit, whatever failed
     if (r == 0) fetch.done();  // counted already unless a wait timed out
   } else if (kDual && (warp == kWarpProducerK || warp == kWarpProducerV ||
                         warp == kWarpProducerK2 || warp == kWarpProducerV2)) {
@@ -789,11 +834,13 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
             for (int bx = 0; bx < kBoxes; ++bx)
               tma_load_2d(st + bx * kHalf + ro, map, U.h * D + bx * kBoxElems, bl * BS, fb);
           }
+          if (BSC && r == 0) load_scales(c, npg, bl, U.h);
         }
         __syncwarp();
       }
       if (fetcher) cur_k.advance(p, fetch); else cur_v.advance(p, ring);
     }
+    if constexpr (BSC) cp_async_wait_all();  // none in flight at exit, whatever failed
     if (fetcher) fetch.done();  // counted already unless a wait timed out
   } else if (warp == kWarpMma || warp == kWarpMmaPV || (kDualPV && warp == kWarpMmaPV2)) {
     // ------------------------------ MMA issue -----------------------------
@@ -819,7 +866,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
           // Done here, not in the K producer, so the TMA rings never wait for
           // a unit's Q.
           const uint8_t* qt = base + kOffQ + qb * kOpBytes;
-          uint8_t* q8 = base + kOffQ8 + qb * kOpBytes;
+          uint8_t* q8 = base + kOffQ8 + qb * L::kQ8Bytes;
           float* qs = reinterpret_cast<float*>(base + kOffQs) + qb * kGE;
           const int d0 = 4 * lane;  // lanes past D read the tile's zero half
 #pragma unroll
@@ -845,18 +892,22 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
             int e = 0;
             if (mx > 0.f) frexpf(mx, &e);
             const float sig = ldexpf(1.f, 8 - e);
-            uint32_t hw = 0, lw = 0;
+            uint32_t hw = 0, lw = 0, lw2 = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float y = x[i] * sig;
               const uint8_t hb = to_e4m3(y);
-              const uint8_t lb = to_e4m3(y - e4m3_to_float(hb));
+              const float r = y - e4m3_to_float(hb);
+              const uint8_t lb = to_e4m3(r);
               hw |= (uint32_t)hb << (8 * i);
               lw |= (uint32_t)lb << (8 * i);
+              if constexpr (QT == 3) lw2 |= (uint32_t)to_e4m3(r - e4m3_to_float(lb)) << (8 * i);
             }
             if (d0 < D) {
               *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(g, d0)) = hw;
               *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(kN + g, d0)) = lw;
+              if constexpr (QT == 3)
+                *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(2 * kN + g, d0)) = lw2;
             }
             if (lane == 0) qs[g] = 1.f / sig;
           }
@@ -875,7 +926,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         if constexpr (KV8) {
           // S = K . [Q_hi; Q_lo]^T (N = 32: rows 16..31 of the operand are q_lo):
           // 32 fp8 dims (32 bytes) per step
-          const uint32_t q8 = base_u32 + kOffQ8 + qb * kOpBytes;
+          const uint32_t q8 = base_u32 + kOffQ8 + qb * L::kQ8Bytes;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             const uint64_t a = sdesc_rows<kKVRow>(kb + k * 32, 16);
@@ -1095,7 +1146,9 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         }
         // logit scale per row: softmax scale (base 2) x K dequantisation
         // scale (x 1 / sigma of the row's fp8 q terms)
-        const float ksc = p.k_scale ? __ldg(p.k_scale + (p.scale_per_head ? U.h : 0)) : 1.f;
+        // (BSC: the K scale belongs to the token's block, below)
+        const float ksc =
+            !BSC && p.k_scale ? __ldg(p.k_scale + (p.scale_per_head ? U.h : 0)) : 1.f;
         float qsc[kGA];
         if constexpr (KV8) {
           const bool okq = !failed && mbar_wait(q8_full(jq & 1), (jq >> 1) & 1, wlim);
@@ -1113,19 +1166,45 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
           bool ok = !failed && mbar_wait(s_full(c & 1), (c >> 1) & 1, wlim);
           if (!__all_sync(kFull, ok)) failed = true;
           tc_fence_after();
-          float s[kLd], s2[kLd];
+          float s[kLd], s2[kLd], s3[kLd];
           tld(tS(c & 1) + lane_base + (uint32_t)g0, s);
           if constexpr (KV8) tld(tS(c & 1) + lane_base + (uint32_t)(kN + g0), s2);
+          if constexpr (QT == 3) tld(tS(c & 1) + lane_base + (uint32_t)(2 * kN + g0), s3);
+          // BSC: k_t = ks k8_t and v_t = vs v8_t with the scales of token t's
+          // block. ks multiplies the logit. vs is taken into the weight: with
+          // s'_t = s_t + log2(vs), P'_t = 2^(s'_t - m') is what multiplies the raw
+          // V bytes, its largest value is 1 as the fp8 split wants, and the
+          // weight 2^(s_t - m') = P'_t / vs goes into the sum. A unit's maximum
+          // m' then stands where m does everywhere below (accumulators, sums and
+          // log-sum-exp are all relative to it). A scale below kMinBlockScale
+          // (a block of zeros) enters s' as that and multiplies P' by the rest.
+          float kst = 1.f, lvs = 0.f, ivs = 1.f, p8 = kP8Scale;
+          if constexpr (BSC) {
+            const int e = c % kScRing;
+            ok = !failed && mbar_wait(sc_full(e), (c / kScRing) & 1, wlim);
+            if (!__all_sync(kFull, ok)) failed = true;
+            const float* sc = reinterpret_cast<const float*>(base + L::kOffSc) + e * 2 * kMaxPps;
+            const int pi = (t < n_valid ? t : 0) / BS;  // entries past the chunk's pages are stale
+            kst = sc[pi];
+            const float vst = sc[kMaxPps + pi];
+            const float vse = fmaxf(vst, kMinBlockScale);
+            lvs = log2f(vse);
+            ivs = 1.f / vse;
+            if (vst < kMinBlockScale) p8 = kP8Scale * (vst * ivs);
+          }
           tmem_ld_wait();
           if constexpr (KV8) {
 #pragma unroll
-            for (int j = 0; j < kLd; ++j) s[j] += s2[j];
+            for (int j = 0; j < kLd; ++j) s[j] += QT == 3 ? s2[j] + s3[j] : s2[j];
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free(c & 1));
 #pragma unroll
-          for (int j = 0; j < kGA; ++j) s[j] = (t < n_valid) ? s[j] * qsc[j] : -INFINITY;
+          for (int j = 0; j < kGA; ++j) {
+            if constexpr (BSC) s[j] = (t < n_valid) ? fmaf(s[j] * kst, qsc[j], lvs) : -INFINITY;
+            else s[j] = (t < n_valid) ? s[j] * qsc[j] : -INFINITY;
+          }
           float* rb = red + (c & 1) * 32;
 #pragma unroll
           for (int j = 0; j < kGA; ++j) {
@@ -1149,7 +1228,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
             alpha[j] = exp2f(m_run[j] - mn);
             m_run[j] = mn;
             prs[j] = exp2f(s[j] - mn);
-            l_th[j] = l_th[j] * alpha[j] + prs[j];
+            l_th[j] = l_th[j] * alpha[j] + (BSC ? prs[j] * ivs : prs[j]);
           }
 #pragma unroll
           for (int j = 0; j < kGA; ++j) {
@@ -1158,7 +1237,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
               const int g = g0 + j;
               if constexpr (KV8) {
                 // p * 256 = t0 + t1 + t2 in fp8 (about 12 significant bits)
-                const float x = pr * kP8Scale;
+                const float x = pr * p8;
                 const uint8_t b0 = to_e4m3(x);
                 const float r0 = x - e4m3_to_float(b0);
                 const uint8_t b1 = to_e4m3(r0);
@@ -1268,7 +1347,8 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
       U.n_splits_b = reinterpret_cast<volatile int*>(st)[kStU + 1];
       const int hq0 = U.h * G;
       // V dequantisation scale (and the fp8 split factor of P)
-      const float vsc = (p.v_scale ? __ldg(p.v_scale + (p.scale_per_head ? U.h : 0)) : 1.f) *
+      // (BSC: the V scales are in the weights)
+      const float vsc = (!BSC && p.v_scale ? __ldg(p.v_scale + (p.scale_per_head ? U.h : 0)) : 1.f) *
                         (KV8 ? 1.f / kP8Scale : 1.f);
       if (p.cluster > 1 && U.n_splits_b > 1) {
         // Cluster launch: this split's normalised partial and log-sum-exp stay
@@ -1381,7 +1461,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   if (p.cluster > 1) cluster_sync_all();
 }
 
-template <int G, int D, int BS, bool FP16, bool KV8>
+template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* tq,
                        const PartialParams& p, cudaStream_t stream) {
   const int ctas = p.num_units < p.max_ctas ? p.num_units : p.max_ctas;
@@ -1392,7 +1472,7 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const CUten
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(tc_threads(G, D, KV8));
-  cfg.dynamicSmemBytes = Layout<KV8, D, G>::kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   unsigned n_attr = 0;
@@ -1413,15 +1493,15 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const CUten
   }
   cfg.attrs = attr;
   cfg.numAttrs = n_attr;
-  return cudaLaunchKernelEx(&cfg, paged_partial_tc_kernel<G, D, BS, FP16, KV8>, *tk, *tv, *tq, p);
+  return cudaLaunchKernelEx(&cfg, paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>, *tk, *tv, *tq, p);
 }
 
-template <int G, int D, int BS, bool FP16, bool KV8>
+template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 int max_clusters_one(int cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster * 64u);
   cfg.blockDim = dim3(tc_threads(G, D, KV8));
-  cfg.dynamicSmemBytes = Layout<KV8, D, G>::kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;
@@ -1430,7 +1510,7 @@ int max_clusters_one(int cluster) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, paged_partial_tc_kernel<G, D, BS, FP16, KV8>, &cfg) !=
+  if (cudaOccupancyMaxActiveClusters(&n, paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>, &cfg) !=
       cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -1438,24 +1518,24 @@ int max_clusters_one(int cluster) {
   return n;
 }
 
-template <int G, int D, int BS, bool FP16, bool KV8>
+template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 cudaError_t prepare_one() {
-  cudaError_t e = cudaFuncSetAttribute(paged_partial_tc_kernel<G, D, BS, FP16, KV8>,
+  cudaError_t e = cudaFuncSetAttribute(paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Layout<KV8, D, G>::kSmemBytes);
+                                       (int)Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes);
   // clusters of up to 16 CTAs (the splits of one sequence's kv head)
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_partial_tc_kernel<G, D, BS, FP16, KV8>,
+    e = cudaFuncSetAttribute(paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
 
-template <int G, int D, int BS, bool FP16, bool KV8>
+template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 int occupancy_one() {
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-          &n, paged_partial_tc_kernel<G, D, BS, FP16, KV8>, tc_threads(G, D, KV8),
-          Layout<KV8, D, G>::kSmemBytes) != cudaSuccess)
+          &n, paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>, tc_threads(G, D, KV8),
+          Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes) != cudaSuccess)
     return 1;
   return n > 0 ? n : 1;
 }
@@ -1471,7 +1551,7 @@ __host__ __device__ constexpr bool geometry_supported(int G, int D, bool kv8 = f
 // input dtype and K/V type;
 // each (head dim, dtype, K/V type) and G range GLo..GHi is instantiated in its
 // own translation unit (G 1..8 and G 9..16 compile in parallel).
-template <int D, bool FP16, bool KV8, int GLo = 1, int GHi = 8>
+template <int D, bool FP16, bool KV8, int GLo = 1, int GHi = 8, bool BSC = false>
 struct Dispatch {
   template <int G>
   static constexpr bool kBuilt = G >= GLo && G <= GHi && geometry_supported(G, D, KV8);
@@ -1479,40 +1559,40 @@ struct Dispatch {
   static cudaError_t launch_g(int BS, const CUtensorMap* tk, const CUtensorMap* tv,
                               const CUtensorMap* tq, const PartialParams& p, cudaStream_t s) {
     if constexpr (kBuilt<G>) {
-      if (BS == 16) return launch_one<G, D, 16, FP16, KV8>(tk, tv, tq, p, s);
-      if (BS == 32) return launch_one<G, D, 32, FP16, KV8>(tk, tv, tq, p, s);
+      if (BS == 16) return launch_one<G, D, 16, FP16, KV8, BSC>(tk, tv, tq, p, s);
+      if (BS == 32) return launch_one<G, D, 32, FP16, KV8, BSC>(tk, tv, tq, p, s);
       if constexpr (G <= 8)
-        if (BS == 64) return launch_one<G, D, 64, FP16, KV8>(tk, tv, tq, p, s);
+        if (BS == 64) return launch_one<G, D, 64, FP16, KV8, BSC>(tk, tv, tq, p, s);
     }
     return cudaErrorInvalidValue;
   }
   template <int G>
   static cudaError_t prepare_g(int BS) {
     if constexpr (kBuilt<G>) {
-      if (BS == 16) return prepare_one<G, D, 16, FP16, KV8>();
-      if (BS == 32) return prepare_one<G, D, 32, FP16, KV8>();
+      if (BS == 16) return prepare_one<G, D, 16, FP16, KV8, BSC>();
+      if (BS == 32) return prepare_one<G, D, 32, FP16, KV8, BSC>();
       if constexpr (G <= 8)
-        if (BS == 64) return prepare_one<G, D, 64, FP16, KV8>();
+        if (BS == 64) return prepare_one<G, D, 64, FP16, KV8, BSC>();
     }
     return cudaErrorInvalidValue;
   }
   template <int G>
   static int max_clusters_g(int BS, int cluster) {
     if constexpr (kBuilt<G>) {
-      if (BS == 16) return max_clusters_one<G, D, 16, FP16, KV8>(cluster);
-      if (BS == 32) return max_clusters_one<G, D, 32, FP16, KV8>(cluster);
+      if (BS == 16) return max_clusters_one<G, D, 16, FP16, KV8, BSC>(cluster);
+      if (BS == 32) return max_clusters_one<G, D, 32, FP16, KV8, BSC>(cluster);
       if constexpr (G <= 8)
-        if (BS == 64) return max_clusters_one<G, D, 64, FP16, KV8>(cluster);
+        if (BS == 64) return max_clusters_one<G, D, 64, FP16, KV8, BSC>(cluster);
     }
     return 0;
   }
   template <int G>
   static int occupancy_g(int BS) {
     if constexpr (kBuilt<G>) {
-      if (BS == 16) return occupancy_one<G, D, 16, FP16, KV8>();
-      if (BS == 32) return occupancy_one<G, D, 32, FP16, KV8>();
+      if (BS == 16) return occupancy_one<G, D, 16, FP16, KV8, BSC>();
+      if (BS == 32) return occupancy_one<G, D, 32, FP16, KV8, BSC>();
       if constexpr (G <= 8)
-        if (BS == 64) return occupancy_one<G, D, 64, FP16, KV8>();
+        if (BS == 64) return occupancy_one<G, D, 64, FP16, KV8, BSC>();
     }
     return 1;
   }

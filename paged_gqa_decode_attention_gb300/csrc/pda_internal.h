@@ -57,6 +57,16 @@ struct PartialParams {
   // unit; the splits then merge through distributed shared memory instead
   // of the workspace and the split tickets.
   int cluster = 0;
+  // Block-scaled FP8 K/V: k_scale and v_scale are [num_blocks, Hkv]
+  // (scale_per_head unused).
+  int64_t num_blocks = 0;
+};
+
+// What the K/V caches hold.
+enum KvKind : int {
+  kKv16 = 0,        // the 16-bit dtype of q
+  kKvFp8 = 1,       // E4M3, one scale per kv head (or per tensor)
+  kKvFp8Block = 2,  // E4M3, one scale per block and kv head
 };
 
 struct MergeParams {
@@ -114,7 +124,7 @@ int planning_slots(int kernel, bool kv_fp8, int num_sms, int ctas_per_sm);
 bool partial_supported(int group, int head_dim, int block_size, int dtype, bool kv_fp8);
 bool partial_kernel_supported(int kernel, int group, int head_dim, bool kv_fp8);
 cudaError_t partial_prepare(int kernel, int group, int head_dim, int block_size, int dtype,
-                            bool kv_fp8);
+                            KvKind kv);
 int partial_ctas_per_sm(int kernel, int group, int head_dim, int block_size, int dtype,
                         bool kv_fp8);
 // How many clusters of `cluster` CTAs of the tensor-core kernel can be
@@ -126,7 +136,7 @@ int partial_max_clusters(int group, int head_dim, int block_size, int dtype, boo
 // the tensor-core kernel only; both kernels take the output type from
 // p.out_f32.
 cudaError_t launch_partial(int kernel, int group, int head_dim, int block_size, int dtype,
-                           bool kv_fp8, const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
+                           KvKind kv, const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
                            const CUtensorMap* tmap_q, const PartialParams& p, int batch,
                            cudaStream_t stream);
 

@@ -128,6 +128,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
+// Asynchronous 4-byte copy global -> shared memory by this thread (zeros, and
+// no read, unless `in`).
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4u : 0u)
+               : "memory");
+}
+
+// Arrive on `bar` once this thread's earlier cp_async_4 copies have landed
+// (counts against the barrier's expected arrivals like any other).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Untiled bulk copy shared -> global memory, tracked by the issuing thread's
 // bulk async-groups.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
