@@ -119,8 +119,13 @@ __host__ __device__ constexpr bool dual_pv(int G, int D, bool kv8) {
 __host__ __device__ constexpr bool pv2_from_epilogue(int G, int D, bool kv8) {
   return dual_pv(G, D, kv8) && G >= 5;
 }
-__host__ __device__ constexpr int tc_threads(int G, int D, bool kv8) {
-  return 512 + (dual_producers(G, D, kv8) ? 64 : 0) +
+// Block-scaled FP8 K/V: a warp for the scales and the q terms, where it is free.
+// At G <= 4 the 18 or 19 other warps leave every thread 96 registers with or
+// without it; at G >= 5 a 17th warp would cut them from 128, and the QK^T warp does
+// its work.
+__host__ __device__ constexpr bool scale_warp(int G, bool bsc) { return bsc && G <= 4; }
+__host__ __device__ constexpr int tc_threads(int G, int D, bool kv8, bool bsc) {
+  return (scale_warp(G, bsc) ? 32 : 0) + 512 + (dual_producers(G, D, kv8) ? 64 : 0) +
          (dual_pv(G, D, kv8) && !pv2_from_epilogue(G, D, kv8) ? 32 : 0);
 }
 constexpr int kWarpProducerK = 4;
@@ -131,6 +136,8 @@ constexpr int kWarpSmxB0 = 11;             // warps 11-14: second softmax group
 constexpr int kWarpMmaPV = 15;             // issues PV
 constexpr int kWarpProducerK2 = 16;        // second K producer (odd chunks)
 constexpr int kWarpProducerV2 = 17;        // second V producer (odd chunks)
+// (block scales at G <= 4: the last warp)
+__host__ __device__ constexpr int warp_scale(int D) { return D == 64 ? 19 : 18; }
 // second PV issuer (odd chunks): the warp after the last producer, or at
 // G 5..8 the epilogue group's last warp
 __host__ __device__ constexpr int warp_pv2(int G, int D, bool kv8) {
@@ -160,6 +167,11 @@ constexpr float kP8Scale = 256.f;          // FP8 K/V: P is split at p * 256
 // Block-scaled FP8 K/V: the smallest V scale that enters a weight's exponent;
 // a smaller one (a block of zeros) multiplies the weight instead.
 constexpr float kMinBlockScale = 0x1p-60f;
+// Its units beyond one a CTA are taken longest sequence first, from a directory
+// that every CTA builds of a batch of up to kDirMax sequences.
+constexpr int kDirMax = 1024;
+constexpr int kDirBuckets = 64;
+constexpr int kResolveChunk = 3;  // chunk of a unit at which the next one is looked up
 // fp8 terms of Q: two hold a bf16 exactly; the block-scaled kernel takes three
 // for fp16.
 __host__ __device__ constexpr int q_terms(bool fp16, bool bsc) { return fp16 && bsc ? 3 : 2; }
@@ -175,9 +187,10 @@ __host__ __device__ constexpr int q_terms(bool fp16, bool bsc) { return fp16 && 
 // 11 significant bits two E4M3 terms do not hold) and a ring of block scales,
 // [kScRing] x (kMaxPps K scales, kMaxPps V scales). The K producer fills
 // chunk c's entry when it issues the chunk's pages, that is after QK^T of chunk
-// c - kStages, whose issue waited for the softmax's read of S(c - kStages - 2);
-// the softmax reads a chunk's scales before it releases S, so kStages + 2
-// entries suffice without an "empty" barrier.
+// c - kStages, whose issue waited for the softmax's read of S(c - kStages - 2) and
+// so for the scale warp's read of that chunk's entry: kStages + 2 entries suffice
+// without an "empty" barrier. What the softmax needs of them stands in a
+// float4 per page, double-buffered like S.
 template <bool KV8, int D = 128, int G = 8, bool BSC = false, int QT = 2>
 struct Layout {
   static constexpr int kStages = KV8 ? (D == 64 ? 10 : 5) : (D == 64 ? 6 : 3);
@@ -196,14 +209,19 @@ struct Layout {
   static constexpr int kOffBar = kOffLred + 2 * 4 * 8 * 4;
   static constexpr int kScRing = BSC ? kStages + 2 : 0;
   static constexpr int kMaxPps = kT / 16;
-  static constexpr int kNumBars = 4 * kStages + 14 + 2 * kUnitRing + 4 + 2 + 1 + kScRing;
+  static constexpr int kNumBars =
+      4 * kStages + 14 + 2 * kUnitRing + 4 + 2 + 1 + (BSC ? kScRing + 1 : 0);
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   // [kUnitRing] unit index + decoded unit, so no reader repeats its global loads
   static constexpr int kOffURing = kOffTmem + 16;
   static constexpr int kOffUBcast = kOffURing + kUnitRing * kUnitInts * 4;  // same, softmax warp 0 -> rest
   static constexpr int kOffEpiFlag = kOffUBcast + kUnitInts * 4;  // epilogue group's wait outcome
   static constexpr int kOffSc = (kOffEpiFlag + 4 + 15) & ~15;  // block scales (BSC)
-  static constexpr int kOffEpi = kOffSc + kScRing * 2 * kMaxPps * 4;
+  static constexpr int kOffTs = kOffSc + kScRing * 2 * kMaxPps * 4;  // [2][kMaxPps] float4
+  // sequence directory (BSC): the order of up to kDirMax sequences, bucket counts
+  static constexpr int kOffDirOrd = kOffTs + (BSC ? 2 * kMaxPps * 16 : 0);
+  static constexpr int kOffDirHist = kOffDirOrd + (BSC ? kDirMax * 2 : 0);
+  static constexpr int kOffEpi = kOffDirHist + (BSC ? kDirBuckets * 4 : 0);
   static constexpr size_t kSmemBytes = 1024 + kOffEpi + epi_slots(G, KV8) * epi_floats(G) * 4;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -281,6 +299,25 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t b) {
   return __half2float(__half(h));
 }
 
+// Two values (|x| <= 448) as three E4M3 terms each, t[0] + t[1] + t[2] = x to fp16's
+// precision: byte 0 of a term belongs to a, byte 1 to b.
+__device__ __forceinline__ void split_e4m3x3(float a, float b, uint32_t (&t)[3]) {
+  uint32_t x;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(b), "f"(a));
+  __half2 r = *reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<const uint32_t*>(&r)));
+    t[i] = e;
+    if (i < 2) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(e));
+      r = __hsub2(r, *reinterpret_cast<const __half2*>(&h));
+    }
+  }
+}
+
 // One work unit: (split, kv head, sequence) and its page / token / chunk range.
 struct Unit {
   int b, h, split, n_splits_b;
@@ -318,6 +355,12 @@ __device__ __forceinline__ int unit_get(const volatile int* d, Unit& U) {
 }
 
 template <int BS>
+__device__ __forceinline__ int context_len(const PartialParams& p, int b) {
+  const int L = __ldg(p.context_lens + b), maxL = p.max_blocks * BS;
+  return L < 0 ? 0 : (L > maxL ? maxL : L);
+}
+
+template <int BS>
 __device__ __forceinline__ Unit load_unit(const PartialParams& p, int u) {
   constexpr int PPS = kT / BS;
   Unit U;
@@ -325,9 +368,7 @@ __device__ __forceinline__ Unit load_unit(const PartialParams& p, int u) {
   const int rest = u / p.num_splits;
   U.h = rest % p.Hkv;
   U.b = rest / p.Hkv;
-  int L = __ldg(p.context_lens + U.b);
-  const int maxL = p.max_blocks * BS;
-  L = L < 0 ? 0 : (L > maxL ? maxL : L);
+  const int L = context_len<BS>(p, U.b);
   const int n_pages = (L + BS - 1) / BS;
   int nsb = (n_pages + p.chunk_pages - 1) / p.chunk_pages;
   if (nsb > p.num_splits) nsb = p.num_splits;  // the last split takes the rest
@@ -343,6 +384,76 @@ __device__ __forceinline__ Unit load_unit(const PartialParams& p, int u) {
   U.t1 = min(U.p1 * BS, L);
   U.n_chunks = (U.p1 - U.p0 + PPS - 1) / PPS;
   return U;
+}
+
+// Buckets of lengths in chunks for the longest-first order: exact below 16
+// chunks, then four to a factor of two.
+__device__ __forceinline__ int length_bucket(int n_chunks) {
+  if (n_chunks < 16) return n_chunks;
+  const int e = 31 - __clz(n_chunks);
+  return min(kDirBuckets - 1, 16 + 4 * (e - 4) + ((n_chunks >> (e - 2)) & 3));
+}
+
+// One warp: the order of sequences b0 .. B - 1 (B <= kDirMax), longest bucket
+// first, ascending inside a bucket. Every CTA computes the same
+// order (a counting sort in a fixed sequence of steps, no atomics), so that a
+// position in it means the same unit to all.
+template <int BS>
+__device__ __forceinline__ void build_directory(const PartialParams& p, int b0, int B,
+                                                volatile uint16_t* order, volatile int* hist,
+                                                int lane) {
+  for (int i = lane; i < kDirBuckets; i += 32) hist[i] = 0;
+  __syncwarp();
+  for (int b = b0; b < B; b += 128) {  // four rounds' loads in flight
+    int L[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int bb = b + r * 32 + lane;
+      L[r] = bb < B ? context_len<BS>(p, bb) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int bb = b + r * 32 + lane;
+      const int key = bb < B ? length_bucket((L[r] + kT - 1) / kT) : kDirBuckets;
+      const unsigned same = __match_any_sync(kFull, key);
+      if (bb < B && lane == __ffs(same) - 1) hist[key] += __popc(same);
+      __syncwarp();
+    }
+  }
+  {  // counts -> first positions, the longest bucket first: lane i has buckets 63 - 2i, 62 - 2i
+    const int hi = kDirBuckets - 1 - 2 * lane;
+    const int n0 = hist[hi], n1 = hist[hi - 1];
+    int sum = n0 + n1;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kFull, sum, off);
+      if (lane >= off) sum += v;
+    }
+    hist[hi] = sum - n0 - n1;
+    hist[hi - 1] = sum - n1;
+    __syncwarp();
+  }
+  for (int b = b0; b < B; b += 128) {  // the lengths again, from the cache
+    int L[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int bb = b + r * 32 + lane;
+      L[r] = bb < B ? context_len<BS>(p, bb) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int bb = b + r * 32 + lane;
+      const int key = bb < B ? length_bucket((L[r] + kT - 1) / kT) : kDirBuckets;
+      const unsigned same = __match_any_sync(kFull, key);
+      const int at = bb < B ? hist[key] : 0;
+      __syncwarp();
+      if (bb < B) {
+        order[at + __popc(same & ((1u << lane) - 1u))] = (uint16_t)bb;
+        if (lane == __ffs(same) - 1) hist[key] = at + __popc(same);
+      }
+      __syncwarp();
+    }
+  }
 }
 
 // Units that no role has to process: neither pages nor output rows.
@@ -386,7 +497,7 @@ struct Cursor {
 };
 
 template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
-__global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
+__global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
     paged_partial_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v,
                             const __grid_constant__ CUtensorMap tmap_q, const PartialParams p) {
@@ -423,6 +534,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   constexpr bool kDualPV = dual_pv(G, D, KV8);
   constexpr int kWarpMmaPV2 = warp_pv2(G, D, KV8);
   constexpr int kEpiWarps = pv2_from_epilogue(G, D, KV8) ? 3 : 4;  // epilogue group
+  constexpr bool kScaleWarp = scale_warp(G, BSC);
   constexpr int kEpiThreads = 32 * kEpiWarps;
   constexpr int kGA = (G + 1) / 2 > 0 ? (G + 1) / 2 : 1;  // columns of group 0 (group 1: G - kGA)
   constexpr int kLd = kGA > 4 ? 8 : 4;      // TMEM columns a softmax thread loads per operand
@@ -463,6 +575,14 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   const uint32_t cl_bar = bar0 + 8u * (4 * kStages + 20 + 2 * kUnitRing);
   // block scales: the scales of the chunk's pages are in ring entry s
   auto sc_full = [&](int s) { return bar0 + 8u * (4 * kStages + 21 + 2 * kUnitRing + s); };
+  const uint32_t dir_bar = sc_full(kScRing);  // the sequence directory is built
+  // BSC with more units than CTAs: sequences from dir_b0 on (the first one none of
+  // whose units is a CTA's first) are taken longest first. Every CTA's first
+  // unit is its own index still, so that its loads wait for nothing.
+  const int units_per_seq = p.Hkv * p.num_splits;
+  const int dir_b0 = BSC ? ((int)gridDim.x + units_per_seq - 1) / units_per_seq : 0;
+  const int dir_B = BSC ? p.num_units / units_per_seq : 0;
+  const bool use_dir = BSC && p.num_units > (int)gridDim.x && dir_B <= kDirMax;
   volatile int* uring = reinterpret_cast<volatile int*>(base + kOffURing);
 
   const int warp = threadIdx.x >> 5;
@@ -486,6 +606,96 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
     uint64_t wlim;
     bool counted;
     bool first;  // the next unit is this CTA's static first unit
+    // BSC: the next unit is claimed from the counter when the current one
+    // starts, and decoded, published and its first table window requested a
+    // few chunks later, so that a unit boundary waits for none of these.
+    uint32_t dir_bar = 0;
+    const volatile uint16_t* dir_order = nullptr;  // null: no directory
+    int dir_first = 0, per_seq = 1;          // first unit in directory order; units a sequence
+    int pend = 0, r_u = -1, win = 0, nxt = 0;
+    Unit r_U;
+    bool claimed = false, resolved = false, ended = false;
+    __device__ __forceinline__ void claim() {
+      if (claimed || ended) return;
+      claimed = true;
+      // (pend is not touched until resolve(): the warp does not wait for the counter here)
+      if (p->num_units > (int)gridDim.x && lane == 0) pend = atomicAdd(p->sched, 1);
+    }
+    // The claimed unit (or the first one after it with chunks to work on), published;
+    // its first table window is requested.
+    __device__ __forceinline__ void resolve() {
+      if (resolved || ended) return;
+      claim();
+      resolved = true;
+      while (true) {
+        int u = p->num_units;
+        if (u > (int)gridDim.x) u = (int)gridDim.x + __shfl_sync(kFull, pend, 0);
+        claimed = false;
+        int pub = -1;
+        if (u < p->num_units) {
+          bool ok = true;
+          if (dir_order != nullptr) ok = mbar_wait(dir_bar, 0, wlim);
+          if (!__all_sync(kFull, ok)) {
+            *failed = true;
+            ended = true;
+            r_u = -1;
+            done();
+            return;
+          }
+          if (dir_order != nullptr && u >= dir_first) {
+            const int v = u - dir_first, i = v / per_seq;
+            u = dir_order[i] * per_seq + (v - i * per_seq);
+          }
+          r_U = load_unit<BS>(*p, u);
+          if (!unit_has_work(r_U)) {
+            claim();
+            continue;
+          }
+          pub = u;
+          if (r_U.n_chunks == 0) {
+            // an empty context: zeros, written here and not passed on. The current
+            // unit's pages may not all be requested yet, so at most one entry of the
+            // ring may be taken ahead of it (its slot was read, or will be, by roles
+            // that need no page still to be requested).
+            const int64_t row = (int64_t)r_U.b * p->Hq + r_U.h * G;
+            for (int i = lane; i < G * D; i += 32) {
+              if (p->out_f32) static_cast<float*>(p->out)[row * D + i] = 0.f;
+              else static_cast<TNat*>(p->out)[row * D + i] = to_out<TNat>(0.f);
+            }
+            claim();
+            continue;
+          }
+        }
+        r_u = publish(pub, r_U) ? pub : -1;
+        if (r_u < 0) {
+          ended = true;
+          done();
+        } else {
+          const int32_t* table = p->block_table + (int64_t)r_U.b * p->max_blocks + r_U.p0;
+          win = r_U.p0 + lane < r_U.p1 ? __ldg(table + lane) : 0;
+          nxt = r_U.p0 + 32 + lane < r_U.p1 ? __ldg(table + 32 + lane) : 0;
+        }
+        return;
+      }
+    }
+    // Unit `pub` (-1: the end) into the ring; false after a timed-out wait.
+    __device__ __forceinline__ bool publish(int pub, const Unit& U) {
+      const int slot = k % kUnitRing;
+      bool ok = true;
+      if (k >= kUnitRing) ok = mbar_wait(empty0 + 8u * slot, ((k / kUnitRing) - 1) & 1, wlim);
+      if (!__all_sync(kFull, ok)) {
+        *failed = true;
+        done();
+        return false;
+      }
+      if (lane == 0) {
+        unit_put(ring + slot * kUnitInts, pub, U);
+        mbar_arrive(full0 + 8u * slot);
+      }
+      __syncwarp();
+      ++k;
+      return true;
+    }
     // This CTA takes no more units: count it done exactly once (also after a
     // timed-out wait), so the CTA that finishes last resets the counters and
     // the next call starts from zero.
@@ -512,34 +722,41 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         U = load_unit<BS>(*p, (int)blockIdx.x);
         if (unit_has_work(U)) return (int)blockIdx.x;
       }
-      while (true) {
-        int u = 0;
-        if (lane == 0) u = (int)gridDim.x + atomicAdd(p->sched, 1);
-        u = __shfl_sync(kFull, u, 0);
-        const int pub = u < p->num_units ? u : -1;
-        if (pub >= 0) {
-          U = load_unit<BS>(*p, pub);
-          if (!unit_has_work(U)) continue;  // nothing to do for this unit
+      if constexpr (BSC) {
+        resolve();
+        resolved = false;
+        U = r_U;
+        return r_u;
+      } else {
+        while (true) {
+          int u = 0;
+          if (lane == 0) u = (int)gridDim.x + atomicAdd(p->sched, 1);
+          u = __shfl_sync(kFull, u, 0);
+          const int pub = u < p->num_units ? u : -1;
+          if (pub >= 0) {
+            U = load_unit<BS>(*p, pub);
+            if (!unit_has_work(U)) continue;  // nothing to do for this unit
+          }
+          const int slot = k % kUnitRing;
+          bool ok = true;
+          if (k >= kUnitRing) ok = mbar_wait(empty0 + 8u * slot, ((k / kUnitRing) - 1) & 1, wlim);
+          if (!__all_sync(kFull, ok)) {
+            *failed = true;
+            done();
+            return -1;
+          }
+          if (lane == 0) {
+            unit_put(ring + slot * kUnitInts, pub, U);
+            mbar_arrive(full0 + 8u * slot);
+          }
+          __syncwarp();
+          ++k;
+          if (pub < 0) {
+            done();
+            return -1;
+          }
+          return pub;
         }
-        const int slot = k % kUnitRing;
-        bool ok = true;
-        if (k >= kUnitRing) ok = mbar_wait(empty0 + 8u * slot, ((k / kUnitRing) - 1) & 1, wlim);
-        if (!__all_sync(kFull, ok)) {
-          *failed = true;
-          done();
-          return -1;
-        }
-        if (lane == 0) {
-          unit_put(ring + slot * kUnitInts, pub, U);
-          mbar_arrive(full0 + 8u * slot);
-        }
-        __syncwarp();
-        ++k;
-        if (pub < 0) {
-          done();
-          return -1;
-        }
-        return pub;
       }
     }
   };
@@ -579,7 +796,8 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   if (threadIdx.x == 0) {
     for (int s2 = 0; s2 < kUnitRing; ++s2) {
       mbar_init(uring_full(s2), 1);
-      mbar_init(uring_empty(s2), kUnitConsumers + (kDual ? 2 : 0) + (kDualPV ? 1 : 0));
+      mbar_init(uring_empty(s2),
+                kUnitConsumers + (kDual ? 2 : 0) + (kDualPV ? 1 : 0) + (kScaleWarp ? 1 : 0));
     }
     for (int s2 = 0; s2 < 2; ++s2) {
       mbar_init(ep_full(s2), 4 * kGroups);
@@ -591,7 +809,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         mbar_init(empty_bar(r, s), 1);
       }
     for (int b2 = 0; b2 < 2; ++b2) {
-      mbar_init(s_full(b2), 1);
+      mbar_init(s_full(b2), BSC ? 2 : 1);  // S itself (and its tokens' scales)
       mbar_init(s_free(b2), 4 * kGroups);
       mbar_init(p_full(b2), 4 * kGroups);
       mbar_init(o_full(b2), 1);
@@ -604,6 +822,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
     }
     if (p.cluster > 1) mbar_init(cl_bar, (uint32_t)(p.cluster - 1));
     for (int s = 0; s < kScRing; ++s) mbar_init(sc_full(s), 32);
+    if constexpr (BSC) mbar_init(dir_bar, 1);
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
@@ -635,8 +854,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
   static_assert(2 * (kSCols + kOCols) <= (int)kTmemCols, "TMEM columns");
   // BSC, a K producer warp: lane i requests the K and V scale of page i of chunk
   // c (block bl; one outside the cache gets 0, as its page reads zeros) into
-  // the chunk's ring entry. Asynchronous: nothing waits for them but the
-  // softmax, on sc_full.
+  // the chunk's ring entry. Asynchronous: only the scale warp waits for them, on sc_full.
   auto load_scales = [&](int c, int npg, int bl, int h) {
     if constexpr (BSC) {
       const int e = c % kScRing;
@@ -648,6 +866,115 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         cp_async_4(dst + kMaxPps * 4u, p.v_scale + i, in);
       }
       cp_async_arrive(sc_full(e));
+    }
+  };
+
+  // FP8 K/V, one warp (the QK^T warp; BSC: the scale warp), the unit's Q in buffer qb:
+  auto q_terms_to_fp8 = [&](int qb) {
+    // The unit's q rows (16-bit tile from TMA) become QT fp8 terms,
+    // q * sigma = hi + lo (+ lo2), with a power-of-two sigma per row that puts
+    // the row's largest |q| in [128, 256): the fp8 QK^T then sees q
+    // exactly except for elements below 2^-10 of the row maximum.
+    // Not done in the K producer, so the TMA rings never wait for a unit's
+    // Q. A unit's first QK^T waits for it: with library frexp / ldexp,
+    // shuffled maxima and one conversion an element it took 1.5 us at G = 4
+    // and 3.3 us at G = 8.
+    const uint8_t* qt = base + kOffQ + qb * kOpBytes;
+    uint8_t* q8 = base + kOffQ8 + qb * L::kQ8Bytes;
+    float* qs = reinterpret_cast<float*>(base + kOffQs) + qb * kGE;
+    const int d0 = 4 * lane;  // lanes past D read the tile's zero half
+    // in passes over four rows: their loads, maxima and conversions overlap, which a
+    // row's stores between them would forbid
+    constexpr int kRows = 4;
+#pragma unroll
+    for (int g1 = 0; g1 < G; g1 += kRows) {
+      float x[kRows][4];
+      uint32_t mx[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (g1 + r >= G) break;
+        const uint2 w = *reinterpret_cast<const uint2*>(qt + op_offset(g1 + r, d0));
+        if constexpr (FP16) {
+          const float2 lo2 = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+          const float2 hi2 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+          x[r][0] = lo2.x;
+          x[r][1] = lo2.y;
+          x[r][2] = hi2.x;
+          x[r][3] = hi2.y;
+        } else {
+          x[r][0] = __uint_as_float(w.x << 16);
+          x[r][1] = __uint_as_float(w.x & 0xffff0000u);
+          x[r][2] = __uint_as_float(w.y << 16);
+          x[r][3] = __uint_as_float(w.y & 0xffff0000u);
+        }
+        // |x| as bits orders like |x|
+        mx[r] = max(max(__float_as_uint(x[r][0]) & 0x7fffffffu, __float_as_uint(x[r][1]) & 0x7fffffffu),
+                    max(__float_as_uint(x[r][2]) & 0x7fffffffu, __float_as_uint(x[r][3]) & 0x7fffffffu));
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (g1 + r < G) mx[r] = __reduce_max_sync(kFull, mx[r]);
+      uint32_t ta[kRows][3], tb[kRows][3];
+      float inv[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (g1 + r >= G) break;
+        // sigma = 2^(134 - E) for the largest one's biased exponent E, its reciprocal
+        // exact; a row with an infinity or NaN becomes NaN throughout
+        const uint32_t E = mx[r] >> 23, sf = min(253u, 261u - E);
+        const float sig = E == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(sf << 23);
+        inv[r] = __uint_as_float((254u - sf) << 23);
+        split_e4m3x3(x[r][0] * sig, x[r][1] * sig, ta[r]);
+        split_e4m3x3(x[r][2] * sig, x[r][3] * sig, tb[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (g1 + r >= G) break;
+        if (d0 < D) {
+#pragma unroll
+          for (int k = 0; k < QT; ++k)
+            *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(k * kN + g1 + r, d0)) =
+                ta[r][k] | (tb[r][k] << 16);
+        }
+        if (lane == 0) qs[g1 + r] = inv[r];
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q8_full(qb));  // the row scales, for the softmax
+  };
+
+  // BSC, one warp (the scale warp, else the QK^T warp): chunk c's scales for the
+  // softmax. k_t = ks k8_t and v_t = vs v8_t with the scales of token t's block. ks
+  // multiplies the logit. vs is taken into the weight: with s'_t = s_t +
+  // log2(vs), P'_t = 2^(s'_t - m') is what multiplies the raw V bytes, its largest
+  // value is 1 as the fp8 split wants whichever block holds the large values,
+  // and the weight 2^(s_t - m') = P'_t / vs goes into the sum. The running
+  // maximum m' of s' stands where that of s does everywhere (accumulators, sums
+  // and log-sum-exp are relative to it). A scale below kMinBlockScale (a block of
+  // zeros) enters s' as that and multiplies P' by the rest. Lane i turns page
+  // i's scales into (ks, log2 vs, 1 / vs, the split factor of P'); the second arrival
+  // on the chunk's s_full says that they are there.
+  // Not in the softmax, whose steps set the pace (58.8 us against 58.0 in the
+  // QK^T warp for B = 4, L = 32768 at 32/8 heads).
+  auto chunk_scales = [&](int c) {
+    if constexpr (BSC) {
+      const int e = c % kScRing;
+      bool ok = mbar_wait(sc_full(e), (c / kScRing) & 1, wlim);
+      if (kScaleWarp && ok && c >= 2) ok = mbar_wait(s_free(c & 1), ((c - 2) >> 1) & 1, wlim);
+      if (!__all_sync(kFull, ok)) failed = true;
+      if (failed) return;
+      if (lane < PPS) {  // lanes past the chunk's pages: stale, not read
+        const float* sc = reinterpret_cast<const float*>(base + L::kOffSc) + e * 2 * kMaxPps;
+        const float vs = sc[kMaxPps + lane], vse = fmaxf(vs, kMinBlockScale);
+        // 2^lvs and ivs are vs and 1 / vs to about 2^-22; their product is 1 to an ulp or
+        // two, so the sum takes the weight that the V bytes are multiplied with
+        const float lvs = __log2f(vse), ivs = exp2f(-lvs);
+        reinterpret_cast<float4*>(base + L::kOffTs)[(c & 1) * kMaxPps + lane] = make_float4(
+            sc[lane], lvs, ivs, vs < kMinBlockScale ? kP8Scale * (vs * ivs) : kP8Scale);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_full(c & 1));
     }
   };
 
@@ -663,6 +990,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
     }
     FetchSource fetch{&p, uring, uring_full(0), uring_empty(0), lane, 0, &failed, wlim, false,
                       true};
+    if (use_dir) {
+      fetch.dir_bar = dir_bar;
+      fetch.dir_order = reinterpret_cast<const volatile uint16_t*>(base + L::kOffDirOrd);
+      fetch.dir_first = dir_b0 * units_per_seq;
+      fetch.per_seq = units_per_seq;
+    }
     RingSource ring = ring_source();
     Cursor<BS, FetchSource> cur_k;
     Cursor<BS, RingSource> cur_v;
@@ -681,9 +1014,16 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
       const int32_t* table = p.block_table + (int64_t)U.b * p.max_blocks;
       if (cu_i == 0) {
         win_base = U.p0;
-        if (cu_j == 0 && cu_u == (int)blockIdx.x) win_blk = first_win;
-        else win_blk = (U.p0 + lane < U.p1) ? __ldg(table + U.p0 + lane) : 0;
-        nxt_blk = (U.p0 + 32 + lane < U.p1) ? __ldg(table + U.p0 + 32 + lane) : 0;
+        const bool is_first = cu_j == 0 && cu_u == (int)blockIdx.x;
+        if (BSC && r == 0 && !is_first) {
+          win_blk = fetch.win;
+          nxt_blk = fetch.nxt;
+        } else {
+          if (is_first) win_blk = first_win;
+          else win_blk = (U.p0 + lane < U.p1) ? __ldg(table + U.p0 + lane) : 0;
+          nxt_blk = (U.p0 + 32 + lane < U.p1) ? __ldg(table + U.p0 + 32 + lane) : 0;
+        }
+        if (BSC && r == 0) fetch.claim();
         if (r == 0) {
           // this unit's G query rows -> Q operand buffer j & 1
           const int qb = cu_j & 1;
@@ -739,6 +1079,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         if (BSC && r == 0) load_scales(c, npg, bl, U.h);
       }
       __syncwarp();
+      if (BSC && r == 0 && cu_i == min(kResolveChunk, U.n_chunks - 1)) fetch.resolve();
       if (r == 0) cur_k.advance(p, fetch); else cur_v.advance(p, ring);
     }
     if constexpr (BSC) cp_async_wait_all();  // none in flight at exit, whatever failed
@@ -761,6 +1102,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
     }
     FetchSource fetch{&p, uring, uring_full(0), uring_empty(0), lane, 0, &failed, wlim, false,
                       true};
+    if (use_dir) {
+      fetch.dir_bar = dir_bar;
+      fetch.dir_order = reinterpret_cast<const volatile uint16_t*>(base + L::kOffDirOrd);
+      fetch.dir_first = dir_b0 * units_per_seq;
+      fetch.per_seq = units_per_seq;
+    }
     RingSource ring = ring_source();
     Cursor<BS, FetchSource> cur_k;
     Cursor<BS, RingSource> cur_v;
@@ -777,9 +1124,16 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
       const int32_t* table = p.block_table + (int64_t)U.b * p.max_blocks;
       if (cu_i == 0) {
         win_base = U.p0;
-        if (cu_j == 0 && cu_u == (int)blockIdx.x) win_blk = first_win;
-        else win_blk = (U.p0 + lane < U.p1) ? __ldg(table + U.p0 + lane) : 0;
-        nxt_blk = (U.p0 + 32 + lane < U.p1) ? __ldg(table + U.p0 + 32 + lane) : 0;
+        const bool is_first = cu_j == 0 && cu_u == (int)blockIdx.x;
+        if (BSC && fetcher && !is_first) {
+          win_blk = fetch.win;
+          nxt_blk = fetch.nxt;
+        } else {
+          if (is_first) win_blk = first_win;
+          else win_blk = (U.p0 + lane < U.p1) ? __ldg(table + U.p0 + lane) : 0;
+          nxt_blk = (U.p0 + 32 + lane < U.p1) ? __ldg(table + U.p0 + 32 + lane) : 0;
+        }
+        if (BSC && fetcher) fetch.claim();
         if (fetcher) {
           // this unit's G query rows -> Q operand buffer j & 1
           const int qb = cu_j & 1;
@@ -838,6 +1192,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         }
         __syncwarp();
       }
+      if (BSC && fetcher && cu_i == min(kResolveChunk, U.n_chunks - 1)) fetch.resolve();
       if (fetcher) cur_k.advance(p, fetch); else cur_v.advance(p, ring);
     }
     if constexpr (BSC) cp_async_wait_all();  // none in flight at exit, whatever failed
@@ -857,69 +1212,23 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
       if (ok && cur.i == 0) ok = mbar_wait(q_full(qb), (cur.j >> 1) & 1, wlim);
       if (!__all_sync(kFull, ok)) failed = true;
       if (failed) return;
-      if constexpr (KV8) {
-        if (cur.i == 0) {
-          // The unit's q rows (16-bit tile from TMA) become two fp8 terms,
-          // q * sigma = hi + lo, with a power-of-two sigma per row that puts
-          // the row's largest |q| in [128, 256): the fp8 QK^T then sees q
-          // exactly except for elements below 2^-10 of the row maximum.
-          // Done here, not in the K producer, so the TMA rings never wait for
-          // a unit's Q.
-          const uint8_t* qt = base + kOffQ + qb * kOpBytes;
-          uint8_t* q8 = base + kOffQ8 + qb * L::kQ8Bytes;
-          float* qs = reinterpret_cast<float*>(base + kOffQs) + qb * kGE;
-          const int d0 = 4 * lane;  // lanes past D read the tile's zero half
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const uint2 w = *reinterpret_cast<const uint2*>(qt + op_offset(g, d0));
-            float x[4];
-            if constexpr (FP16) {
-              const __half2 lo2 = *reinterpret_cast<const __half2*>(&w.x);
-              const __half2 hi2 = *reinterpret_cast<const __half2*>(&w.y);
-              x[0] = __low2float(lo2);
-              x[1] = __high2float(lo2);
-              x[2] = __low2float(hi2);
-              x[3] = __high2float(hi2);
-            } else {
-              x[0] = __uint_as_float(w.x << 16);
-              x[1] = __uint_as_float(w.x & 0xffff0000u);
-              x[2] = __uint_as_float(w.y << 16);
-              x[3] = __uint_as_float(w.y & 0xffff0000u);
-            }
-            float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-            int e = 0;
-            if (mx > 0.f) frexpf(mx, &e);
-            const float sig = ldexpf(1.f, 8 - e);
-            uint32_t hw = 0, lw = 0, lw2 = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float y = x[i] * sig;
-              const uint8_t hb = to_e4m3(y);
-              const float r = y - e4m3_to_float(hb);
-              const uint8_t lb = to_e4m3(r);
-              hw |= (uint32_t)hb << (8 * i);
-              lw |= (uint32_t)lb << (8 * i);
-              if constexpr (QT == 3) lw2 |= (uint32_t)to_e4m3(r - e4m3_to_float(lb)) << (8 * i);
-            }
-            if (d0 < D) {
-              *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(g, d0)) = hw;
-              *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(kN + g, d0)) = lw;
-              if constexpr (QT == 3)
-                *reinterpret_cast<uint32_t*>(q8 + op8q_offset<D>(2 * kN + g, d0)) = lw2;
-            }
-            if (lane == 0) qs[g] = 1.f / sig;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q8_full(qb));  // the row scales, for the softmax
+      if constexpr (kScaleWarp) {
+        if (cur.i == 0) {  // the scale warp's fp8 terms
+          ok = mbar_wait(q8_full(qb), (cur.j >> 1) & 1, wlim);
+          if (!__all_sync(kFull, ok)) failed = true;
+          if (failed) return;
         }
+      } else if constexpr (KV8) {
+        if (cur.i == 0) q_terms_to_fp8(qb);
       }
       ok = mbar_wait(full_bar(0, slot), (c / kStages) & 1, wlim);
       if (ok && c >= 2) ok = mbar_wait(s_free(c & 1), ((c - 2) >> 1) & 1, wlim);
       if (!__all_sync(kFull, ok)) failed = true;
       if (failed) return;
+      if constexpr (BSC && !kScaleWarp) {
+        chunk_scales(c);
+        if (failed) return;
+      }
       tc_fence_after();
       if (lane == 0) {
         const uint32_t kb = base_u32 + kOffK + slot * kSlotBytes;
@@ -1170,28 +1479,11 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
           tld(tS(c & 1) + lane_base + (uint32_t)g0, s);
           if constexpr (KV8) tld(tS(c & 1) + lane_base + (uint32_t)(kN + g0), s2);
           if constexpr (QT == 3) tld(tS(c & 1) + lane_base + (uint32_t)(2 * kN + g0), s3);
-          // BSC: k_t = ks k8_t and v_t = vs v8_t with the scales of token t's
-          // block. ks multiplies the logit. vs is taken into the weight: with
-          // s'_t = s_t + log2(vs), P'_t = 2^(s'_t - m') is what multiplies the raw
-          // V bytes, its largest value is 1 as the fp8 split wants, and the
-          // weight 2^(s_t - m') = P'_t / vs goes into the sum. A unit's maximum
-          // m' then stands where m does everywhere below (accumulators, sums and
-          // log-sum-exp are all relative to it). A scale below kMinBlockScale
-          // (a block of zeros) enters s' as that and multiplies P' by the rest.
-          float kst = 1.f, lvs = 0.f, ivs = 1.f, p8 = kP8Scale;
-          if constexpr (BSC) {
-            const int e = c % kScRing;
-            ok = !failed && mbar_wait(sc_full(e), (c / kScRing) & 1, wlim);
-            if (!__all_sync(kFull, ok)) failed = true;
-            const float* sc = reinterpret_cast<const float*>(base + L::kOffSc) + e * 2 * kMaxPps;
-            const int pi = (t < n_valid ? t : 0) / BS;  // entries past the chunk's pages are stale
-            kst = sc[pi];
-            const float vst = sc[kMaxPps + pi];
-            const float vse = fmaxf(vst, kMinBlockScale);
-            lvs = log2f(vse);
-            ivs = 1.f / vse;
-            if (vst < kMinBlockScale) p8 = kP8Scale * (vst * ivs);
-          }
+          // (ks, log2 vs, 1 / vs, split factor) of the token's page
+          float4 ts = make_float4(1.f, 0.f, 1.f, kP8Scale);
+          if constexpr (BSC)
+            ts = reinterpret_cast<const float4*>(
+                base + L::kOffTs)[(c & 1) * kMaxPps + (t < n_valid ? t : 0) / BS];
           tmem_ld_wait();
           if constexpr (KV8) {
 #pragma unroll
@@ -1202,15 +1494,19 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
           if (lane == 0) mbar_arrive(s_free(c & 1));
 #pragma unroll
           for (int j = 0; j < kGA; ++j) {
-            if constexpr (BSC) s[j] = (t < n_valid) ? fmaf(s[j] * kst, qsc[j], lvs) : -INFINITY;
+            if constexpr (BSC) s[j] = (t < n_valid) ? fmaf(s[j] * ts.x, qsc[j], ts.y) : -INFINITY;
             else s[j] = (t < n_valid) ? s[j] * qsc[j] : -INFINITY;
           }
           float* rb = red + (c & 1) * 32;
 #pragma unroll
           for (int j = 0; j < kGA; ++j) {
             float mx = s[j];
+            if constexpr (BSC) {
+              mx = warp_max(mx);
+            } else {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+              for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+            }
             if (lane == 0) rb[wq * 8 + j] = mx;
           }
           named_bar_sync(bar, 128);
@@ -1228,16 +1524,33 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
             alpha[j] = exp2f(m_run[j] - mn);
             m_run[j] = mn;
             prs[j] = exp2f(s[j] - mn);
-            l_th[j] = l_th[j] * alpha[j] + (BSC ? prs[j] * ivs : prs[j]);
+            l_th[j] = l_th[j] * alpha[j] + (BSC ? prs[j] * ts.z : prs[j]);
+          }
+          if constexpr (BSC) {
+            // 256 p = t0 + t1 + t2, two heads at a time: p's 11-bit fp16 rounding (2^-12)
+            // is what three 4-bit terms hold, and the differences are exact in fp16
+#pragma unroll
+            for (int j = 0; j < kGA; j += 2) {
+              uint32_t t3[3];
+              split_e4m3x3(prs[j] * ts.w, j + 1 < kGA ? prs[j + 1 < kGA ? j + 1 : j] * ts.w : 0.f, t3);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (j + k < kGA && j + k < ng) {
+                  const uint32_t off = op8_offset(g0 + j + k, t);
+#pragma unroll
+                  for (int q = 0; q < 3; ++q) pb[q * kOpHalf + off] = (uint8_t)(t3[q] >> (8 * k));
+                }
+              }
+            }
           }
 #pragma unroll
-          for (int j = 0; j < kGA; ++j) {
+          for (int j = 0; j < (BSC ? 0 : kGA); ++j) {
             const float pr = prs[j];
             if (j < ng) {  // rows of padding heads stay zero
               const int g = g0 + j;
               if constexpr (KV8) {
                 // p * 256 = t0 + t1 + t2 in fp8 (about 12 significant bits)
-                const float x = pr * p8;
+                const float x = pr * kP8Scale;
                 const uint8_t b0 = to_e4m3(x);
                 const float r0 = x - e4m3_to_float(b0);
                 const uint8_t b1 = to_e4m3(r0);
@@ -1310,9 +1623,33 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8), 1)
         if (lane == 0) mbar_arrive(ep_full(es));
       }
     }
+  } else if (kScaleWarp && warp == warp_scale(D)) {
+    // ------------------------- block scales and queries -------------------------
+    RingSource ring = ring_source();
+    Cursor<BS, RingSource> cur;
+    cur.start(p, ring);
+    while (!failed && cur.valid()) {
+      if (cur.i == 0) {
+        const bool ok = mbar_wait(q_full(cur.j & 1), (cur.j >> 1) & 1, wlim);
+        if (!__all_sync(kFull, ok)) failed = true;
+        if (failed) break;
+        q_terms_to_fp8(cur.j & 1);
+      }
+      chunk_scales(cur.c);
+      cur.advance(p, ring);
+    }
   } else {
     // ------------------------------ epilogue ------------------------------
     const int t = threadIdx.x - kWarpEpi0 * 32;  // output dim
+    if constexpr (BSC) {
+      if (use_dir && warp == kWarpEpi0 && !p.stall_units) {
+        build_directory<BS>(p, dir_b0, dir_B,
+                            reinterpret_cast<volatile uint16_t*>(base + L::kOffDirOrd),
+                            reinterpret_cast<volatile int*>(base + L::kOffDirHist), lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dir_bar);
+      }
+    }
     volatile int* flag = reinterpret_cast<volatile int*>(base + kOffEpiFlag);
     for (int je = 0;; ++je) {
       const int es = je % kEpiSlots;
@@ -1471,7 +1808,7 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const CUten
   // waits for that grid before reading any input.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(tc_threads(G, D, KV8));
+  cfg.blockDim = dim3(tc_threads(G, D, KV8, BSC));
   cfg.dynamicSmemBytes = Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -1500,7 +1837,7 @@ template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 int max_clusters_one(int cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster * 64u);
-  cfg.blockDim = dim3(tc_threads(G, D, KV8));
+  cfg.blockDim = dim3(tc_threads(G, D, KV8, BSC));
   cfg.dynamicSmemBytes = Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1534,7 +1871,7 @@ template <int G, int D, int BS, bool FP16, bool KV8, bool BSC>
 int occupancy_one() {
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-          &n, paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>, tc_threads(G, D, KV8),
+          &n, paged_partial_tc_kernel<G, D, BS, FP16, KV8, BSC>, tc_threads(G, D, KV8, BSC),
           Layout<KV8, D, G, BSC, q_terms(FP16, BSC)>::kSmemBytes) != cudaSuccess)
     return 1;
   return n > 0 ? n : 1;

@@ -158,6 +158,18 @@ def test_long_contexts_and_cluster_merge():
     every_way(Problem(7, 8, 2, 64, 32, [30001], "fp16"), splits=(0, 16, 64))
 
 
+@pytest.mark.parametrize("B,D,G,Hkv", [(300, 64, 4, 1), (1000, 64, 2, 1), (1024, 64, 8, 1), (1100, 64, 4, 1),
+                                       (60, 128, 8, 8)])
+def test_many_ragged_sequences(B, D, G, Hkv):
+    """More units than CTAs, with and without a directory of the sequences (up to 1024): empty
+    contexts, single tokens, a few long ones anywhere in the batch."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 60, B)
+    lens[rng.integers(0, B, B // 10)] = 0
+    lens[rng.integers(0, B, 9)] = rng.integers(300, 5000, 9)
+    every_way(Problem(B, G, Hkv, D, 16, lens), splits=(0, 1, 7))
+
+
 def test_extreme_block_scales():
     """V scales 2^40 apart, zeros, blocks whose V or K is nothing but zeros, and subnormal scales:
     the probabilities do not suffer from where the large values sit."""
