@@ -22,6 +22,7 @@ ABI_VERSION = 2
 _STATUS_NAMES = {0: "PDA_OK", -1: "PDA_EINVAL", -2: "PDA_EUNSUPPORTED", -3: "PDA_ENOMEM",
                  -4: "PDA_ECUDA", -5: "PDA_EALIAS", -6: "PDA_EDEVICE"}
 _DT = {torch.bfloat16: PDA_BF16, torch.float16: PDA_FP16, torch.float32: PDA_F32}
+_DT16 = {torch.bfloat16: PDA_BF16, torch.float16: PDA_FP16}
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpaged_decode_attn.so")
@@ -199,6 +200,7 @@ class PagedDecodeAttention:
         self.device = int(device)
         self.dtype = dtype
         self.kv_fp8 = bool(kv_fp8)
+        self._geometry = (num_q_heads, num_kv_heads, block_size, head_dim)
         self.config = make_config(num_q_heads, num_kv_heads, head_dim, block_size, dtype,
                                   max_batch, max_blocks_per_seq, max_splits, self.device,
                                   self.kv_fp8)
@@ -232,6 +234,14 @@ class PagedDecodeAttention:
         and v_cache are torch.float8_e4m3fn (or uint8) tensors; k_scale and
         v_scale are fp32 device tensors of Hkv (per kv head) or 1 values, or,
         for a block-scaled cache (append_kv_fp8), both [num_blocks, Hkv]."""
+        # two dimensions and more values than heads: block scales (with one block they are
+        # the heads' scales)
+        if self.kv_fp8 and any([t is not None and t.dim() == 2 and
+                                t.numel() not in (1, self.config.num_kv_heads)
+                                for t in (k_scale, v_scale)]):
+            return self._run_block_scaled(q, k_cache, v_cache, block_table, context_lens, scale,
+                                          out, num_splits, max_context_len_hint, out_dtype,
+                                          stream, k_scale, v_scale)
         c = self.config
         B = q.shape[0]
         if scale is None:
@@ -248,23 +258,6 @@ class PagedDecodeAttention:
         else:
             kp = _dev_ptr(k_cache, "k_cache", self.dtype)
             vp = _dev_ptr(v_cache, "v_cache", self.dtype)
-        if self.kv_fp8 and any(t is not None and t.dim() == 2 for t in (k_scale, v_scale)):
-            want = (k_cache.shape[0], c.num_kv_heads)
-            if k_scale is None or v_scale is None or k_scale.shape != want or v_scale.shape != want:
-                raise ValueError("block scales: k_scale and v_scale must both be [num_blocks, Hkv]")
-            _same_device(q.device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
-                         v_scale=v_scale, block_table=block_table, context_lens=context_lens,
-                         out=out)
-            _check(self.lib, self.lib.paged_decode_attn_run_block_scaled(
-                self.handle, _dev_ptr(q, "q", self.dtype), kp, vp,
-                _dev_ptr(k_scale, "k_scale", torch.float32),
-                _dev_ptr(v_scale, "v_scale", torch.float32),
-                _dev_ptr(block_table, "block_table", torch.int32),
-                _dev_ptr(context_lens, "context_lens", torch.int32), B, block_table.shape[1],
-                k_cache.shape[0], float(scale), _dev_ptr(out, "out", out_dtype),
-                _stream_on(stream, self.device), int(num_splits), int(max_context_len_hint),
-                _DT[out_dtype]))
-            return out
         per_head = 0
         for t in (k_scale, v_scale):
             if t is not None:
@@ -284,6 +277,41 @@ class PagedDecodeAttention:
                 per_head, _dev_ptr(out, "out", out_dtype), _stream_ptr(stream),
                 int(num_splits), int(max_context_len_hint), _DT[out_dtype])
         _check(self.lib, self.lib.paged_decode_attn_run_scaled(*args))
+        return out
+
+    def _run_block_scaled(self, q, k_cache, v_cache, block_table, context_lens, scale, out,
+                          num_splits, max_context_len_hint, out_dtype, stream, k_scale, v_scale):
+        dt, dev = self.dtype, self.device
+        Hq, Hkv, bs, D = self._geometry
+        if k_scale is None or v_scale is None:
+            raise ValueError("block scales: k_scale and v_scale must both be [num_blocks, Hkv]")
+        if _fp8_device(k_cache, v_cache, k_scale, v_scale) != dev:
+            raise ValueError(f"the cache must be on cuda:{dev}, the handle's device")
+        if k_cache.shape[1:] != (bs, Hkv, D):
+            raise ValueError("caches must be [num_blocks, block_size, Hkv, D] with the handle's sizes")
+        shape = q.shape
+        if len(shape) != 3 or shape[1:] != (Hq, D):
+            raise ValueError("q must be [batch, Hq, D] with the handle's sizes")
+        B = shape[0]
+        if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
+            raise ValueError("block_table must be [batch, max_blocks] and context_lens [batch]")
+        if out_dtype is None:
+            out_dtype = dt
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        elif out.shape != shape:
+            raise ValueError("out must have q's shape")
+        p = _pointers(dev, (("q", q, dt), ("k_cache", k_cache, None), ("v_cache", v_cache, None),
+                            ("k_scale", k_scale, torch.float32),
+                            ("v_scale", v_scale, torch.float32),
+                            ("block_table", block_table, torch.int32),
+                            ("context_lens", context_lens, torch.int32), ("out", out, out_dtype)))
+        status = self.lib.paged_decode_attn_run_block_scaled(
+            self.handle, p[0], p[1], p[2], p[3], p[4], p[5], p[6], B, block_table.shape[1],
+            k_cache.shape[0], 1.0 / math.sqrt(D) if scale is None else float(scale), p[7],
+            _stream_on(stream, dev), int(num_splits), int(max_context_len_hint), _DT[out_dtype])
+        if status:
+            _check(self.lib, status)
         return out
 
     def run_raw(self, q_ptr: int, k_ptr: int, v_ptr: int, table_ptr: int, lens_ptr: int,
@@ -482,53 +510,93 @@ def remap_table(block_table, lens, block_size: int, new_id, err=None, stream=Non
 
 
 # --------------------------- block-scaled FP8 caches ---------------------------
+# A decode step makes these calls once a layer, and a small one is bound by the
+# host: the checks of a call run over its tensors once, without helpers per tensor.
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _refuse(name: str, t: torch.Tensor, device: int, dtype) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _pointers(device: int, named) -> list[int]:
+    """Pointers of (name, tensor, dtype or None) on one device, each checked."""
+    out = []
+    for name, t, dtype in named:
+        if t.get_device() != device or not t.is_contiguous() or (
+                dtype is not None and t.dtype != dtype):
+            _refuse(name, t, device, dtype)
+        out.append(t.data_ptr())
+    return out
+
+
+def _rows16(name: str, t: torch.Tensor, device: int, dtype) -> tuple[int, int]:
+    """Pointer and token stride of [rows, heads, D] with the heads contiguous in a row."""
+    if t.get_device() != device or t.dtype != dtype:
+        _refuse(name, t, device, dtype)
+    T, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
+        raise ValueError(f"{name}: heads must be contiguous within a token")
+    return t.data_ptr(), (s0 if T > 1 else H * D)
 
 
 def _stream_on(stream, device: int) -> int:
     """`stream`, or torch's current stream of `device` (which need not be the current one)."""
-    return _stream_ptr(torch.cuda.current_stream(device) if stream is None else stream)
+    if stream is None:
+        return _raw_stream(device)
+    return _stream_ptr(stream)
 
 
-def _fp8_cache(k_cache, v_cache, k_scale, v_scale):
-    """Pointers of a block-scaled FP8 cache: [num_blocks, block_size, Hkv, D] E4M3 bytes and
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _fp8_device(k_cache, v_cache, k_scale, v_scale) -> int:
+    """Device of a block-scaled FP8 cache: [num_blocks, block_size, Hkv, D] E4M3 bytes and
     [num_blocks, Hkv] fp32 scales."""
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_blocks, block_size, Hkv, D] alike")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise ValueError(f"{name} must be float8_e4m3fn or uint8")
-    if k_scale.shape != (shape[0], shape[2]) or v_scale.shape != (shape[0], shape[2]):
+    if k_cache.dtype not in _FP8 or v_cache.dtype not in _FP8:
+        raise ValueError("k_cache and v_cache must be float8_e4m3fn or uint8")
+    want = (shape[0], shape[2])
+    if k_scale.shape != want or v_scale.shape != want:
         raise ValueError("k_scale and v_scale must be [num_blocks, Hkv]")
-    return (_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-            _dev_ptr(k_scale, "k_scale", torch.float32),
-            _dev_ptr(v_scale, "v_scale", torch.float32))
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA tensor")
+    return k_cache.get_device()
 
 
-def _append_args(k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, cu_rows,
-                 err, stream):
+def _append_args(device, k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+                 cu_rows, err, stream):
     """Checks shared by the two appends; the cache and sequence arguments of the C calls."""
-    ptrs = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
     nb, bs, Hkv, D = k_cache.shape
     if k.shape != v.shape or k.shape[1:] != (Hkv, D):
         raise ValueError("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_blocks]")
-    B = block_table.shape[0]
+    B, width = block_table.shape
     if context_lens.shape != (B,) or cu_rows.shape != (B + 1,):
         raise ValueError("context_lens must be [batch] and cu_rows [batch + 1]")
-    _same_device(k_cache.device, k=k, v=v, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                 block_table=block_table, context_lens=context_lens, cu_rows=cu_rows, err=err)
-    dev = _device_of(k_cache)
-    return ptrs + (nb, bs, _dev_ptr(block_table, "block_table", torch.int32),
-                   block_table.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
-                   _dev_ptr(cu_rows, "cu_rows", torch.int64), B, _opt_err(err),
-                   dev, _stream_on(stream, dev))
+    named = [("k_cache", k_cache, None), ("v_cache", v_cache, None),
+             ("k_scale", k_scale, torch.float32), ("v_scale", v_scale, torch.float32),
+             ("block_table", block_table, torch.int32),
+             ("context_lens", context_lens, torch.int32), ("cu_rows", cu_rows, torch.int64)]
+    if err is not None:
+        if err.numel() < 2:
+            raise ValueError("err must hold two int32 values")
+        named.append(("err", err, torch.int32))
+    ptr = _pointers(device, named)
+    return (ptr[0], ptr[1], ptr[2], ptr[3], nb, bs, ptr[4], width, ptr[5], ptr[6], B,
+            ptr[7] if err is not None else None, device, _stream_on(stream, device))
 
 
 def append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -542,16 +610,22 @@ def append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     [num_blocks, block_size, Hkv, D] float8_e4m3fn or uint8, scales
     [num_blocks, Hkv] fp32, block_table [batch, max_blocks] int32. Sequence b's
     last tokens, up to context_lens[b] (int32, the new ones included), are the
-    rows cu_rows[b] .. cu_rows[b + 1] - 1 (cu_rows: int64, [batch + 1])."""
-    lib = load_library()
-    kp, ks = _token_rows(k, "k", k.dtype)
-    vp, vs = _token_rows(v, "v", k.dtype)
-    if k.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("k and v must be bfloat16 or float16")
-    args = _append_args(k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+    rows cu_rows[b] .. cu_rows[b + 1] - 1 (cu_rows: int64, [batch + 1]). A block
+    is written for one sequence: one shared with another sequence is copied
+    first (copy_blocks and, for the scales, ``scale[dst] = scale[src]``)."""
+    lib = _lib or load_library()
+    dt = k.dtype
+    if dt not in _DT16 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must be bfloat16 or float16 [rows, heads, head_dim]")
+    dev = _fp8_device(k_cache, v_cache, k_scale, v_scale)
+    kp, ks = _rows16("k", k, dev, dt)
+    vp, vs = _rows16("v", v, dev, dt)
+    args = _append_args(dev, k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
                         cu_rows, err, stream)
     T, Hkv, D = k.shape
-    _check(lib, lib.paged_decode_attn_append_kv_fp8(kp, ks, vp, vs, T, Hkv, D, _DT[k.dtype], *args))
+    status = lib.paged_decode_attn_append_kv_fp8(kp, ks, vp, vs, T, Hkv, D, _DT16[dt], *args)
+    if status:
+        _check(lib, status)
 
 
 def rope_append_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -563,37 +637,40 @@ def rope_append_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                        stream=None) -> torch.Tensor:
     """RoPE on q and k, then append_kv_fp8 of the rotated k and of v, in one
     launch. positions [rows] int32, cos_sin_cache [max_position, rot_dim] fp32
-    (cosines then sines), neox as in rope_kv_write. Returns q_out (a new
-    tensor, or ``q_out``; pass ``q_out=q`` to rotate in place); its rows that
-    belong to no sequence are not written."""
-    lib = load_library()
+    (cosines then sines; angles scaled for long contexts are the table's
+    matter), neox as in rope_kv_write. Returns q_out (a new tensor, or
+    ``q_out``; pass ``q_out=q`` to rotate in place); its rows that belong to no
+    sequence are not written."""
+    lib = _lib or load_library()
     dt = q.dtype
-    if dt not in (torch.bfloat16, torch.float16):
-        raise ValueError("q, k and v must be bfloat16 or float16")
-    qp, qs = _token_rows(q, "q", dt)
-    kp, ks = _token_rows(k, "k", dt)
-    vp, vs = _token_rows(v, "v", dt)
+    if dt not in _DT16 or q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be bfloat16 or float16 [rows, heads, head_dim]")
     T, Hq, D = q.shape
     if k.shape[0] != T or k.shape[2] != D:
         raise ValueError("k and v must have q's rows and head_dim")
+    dev = _fp8_device(k_cache, v_cache, k_scale, v_scale)
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-    if q_out.shape != q.shape:
+    elif q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
-    qop, qos = _token_rows(q_out, "q_out", dt)
     if cos_sin_cache.dim() != 2:
         raise ValueError("cos_sin_cache must be [max_position, rot_dim]")
     if positions.shape != (T,):
         raise ValueError("positions must be [rows]")
-    args = _append_args(k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+    qp, qs = _rows16("q", q, dev, dt)
+    kp, ks = _rows16("k", k, dev, dt)
+    vp, vs = _rows16("v", v, dev, dt)
+    qop, qos = (qp, qs) if q_out is q else _rows16("q_out", q_out, dev, dt)
+    args = _append_args(dev, k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
                         cu_rows, err, stream)
-    _same_device(k_cache.device, q=q, q_out=q_out, positions=positions,
-                 cos_sin_cache=cos_sin_cache)
+    pos, cs = _pointers(dev, (("positions", positions, torch.int32),
+                              ("cos_sin_cache", cos_sin_cache, torch.float32)))
     max_pos, rot_dim = cos_sin_cache.shape
-    _check(lib, lib.paged_decode_attn_rope_append_kv_fp8(
-        qp, qs, kp, ks, vp, vs, _dev_ptr(positions, "positions", torch.int32),
-        _dev_ptr(cos_sin_cache, "cos_sin_cache", torch.float32), max_pos, rot_dim,
-        int(bool(neox)), T, Hq, k.shape[1], D, _DT[dt], qop, qos, *args))
+    status = lib.paged_decode_attn_rope_append_kv_fp8(
+        qp, qs, kp, ks, vp, vs, pos, cs, max_pos, rot_dim, 1 if neox else 0, T, Hq, k.shape[1], D,
+        _DT16[dt], qop, qos, *args)
+    if status:
+        _check(lib, status)
     return q_out
 
 
@@ -605,14 +682,14 @@ def gather_kv_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_rows
     of ``dtype`` (or k_out's): sequence b from row cu_rows[b] (int64; default:
     exclusive prefix sums of lens, computed on the host from lens). Returns
     (k_out, v_out)."""
-    lib = load_library()
-    ptrs = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    lib = _lib or load_library()
+    dev = _fp8_device(k_cache, v_cache, k_scale, v_scale)
     nb, bs, Hkv, D = k_cache.shape
     if (k_out is None) != (v_out is None):
         raise ValueError("pass both k_out and v_out, or neither")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_blocks]")
-    B = block_table.shape[0]
+    B, width = block_table.shape
     if cu_rows is None or max_len is None or k_out is None:
         lens_h = lens.cpu().to(torch.int64)
         total = int(lens_h.sum())
@@ -627,18 +704,23 @@ def gather_kv_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_rows
             v_out = torch.empty((total, Hkv, D), dtype=dtype, device=k_cache.device)
     if lens.shape != (B,) or cu_rows.shape != (B,):
         raise ValueError("lens and cu_rows must be [batch]")
-    if k_out.shape[1:] != (Hkv, D) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+    shape, dt = k_out.shape, k_out.dtype
+    if len(shape) != 3 or shape[1:] != (Hkv, D) or v_out.shape != shape or v_out.dtype != dt:
         raise ValueError("k_out and v_out must be [rows, Hkv, D] alike")
-    if k_out.dtype not in _DT:
+    if dt not in _DT:
         raise ValueError("k_out and v_out must be bfloat16, float16 or float32")
-    _same_device(k_cache.device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                 block_table=block_table, lens=lens, cu_rows=cu_rows, k_out=k_out, v_out=v_out,
-                 err=err)
-    dev = _device_of(k_cache)
-    _check(lib, lib.paged_decode_attn_gather_kv_fp8(
-        *ptrs, nb, bs, Hkv, D, _dev_ptr(block_table, "block_table", torch.int32),
-        block_table.shape[1], _dev_ptr(lens, "lens", torch.int32),
-        _dev_ptr(cu_rows, "cu_rows", torch.int64), B, int(max_len), _dev_ptr(k_out, "k_out"),
-        _dev_ptr(v_out, "v_out"), k_out.shape[0], _DT[k_out.dtype], _opt_err(err),
-        dev, _stream_on(stream, dev)))
+    named = [("k_cache", k_cache, None), ("v_cache", v_cache, None),
+             ("k_scale", k_scale, torch.float32), ("v_scale", v_scale, torch.float32),
+             ("block_table", block_table, torch.int32), ("lens", lens, torch.int32),
+             ("cu_rows", cu_rows, torch.int64), ("k_out", k_out, None), ("v_out", v_out, None)]
+    if err is not None:
+        if err.numel() < 2:
+            raise ValueError("err must hold two int32 values")
+        named.append(("err", err, torch.int32))
+    p = _pointers(dev, named)
+    status = lib.paged_decode_attn_gather_kv_fp8(
+        p[0], p[1], p[2], p[3], nb, bs, Hkv, D, p[4], width, p[5], p[6], B, int(max_len), p[7],
+        p[8], shape[0], _DT[dt], p[9] if err is not None else None, dev, _stream_on(stream, dev))
+    if status:
+        _check(lib, status)
     return k_out, v_out

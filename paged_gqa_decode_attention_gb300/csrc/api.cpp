@@ -148,6 +148,50 @@ void plan_splits(const pda_config& c, int kernel, int num_sms, int ctas_per_sm, 
   *chunk_out = chunk;
 }
 
+// The split count of a block-scaled FP8 call, whose kernel takes the units beyond
+// one a CTA longest sequence first. In token-equivalents of one CTA's time: a unit
+// costs its tokens in whole 128-token chunks plus 512, a merged split 32, a split
+// that a shorter sequence does not have (the counter still visits it) 240. The
+// host knows the longest context only, so a batch is weighed twice: as if
+// every sequence had it, and as if the lengths were spread out (a quarter of it on
+// average), where many splits keep one long sequence from setting the time.
+// Measured on GB300 against the 16-bit rule's pick: 64 sequences of 100 to
+// 16384 tokens at 14/2 heads, D 64, S = 7 41 us (S = 1: 99), 13 of 1 to 9001 at 28/4
+// heads 24 (24), one of 777 at 14/2 heads S = 7 9.9 (S = 49: 15.6), 4 x 32768 at 32/8
+// heads S = 9 56 (S = 4: 54), 128 of 32 to 4096 at 64/8 heads S = 1 69 (S = 2: 81).
+void plan_block_scaled(const pda_config& c, int num_sms, int batch, int max_blocks, int hint,
+                       int* S_out, int* chunk_out) {
+  constexpr int64_t kUnit = 512, kMerge = 32, kVisit = 240, kChunk = 128;
+  const int bs = c.block_size;
+  int64_t max_len = (int64_t)max_blocks * bs;
+  if (hint > 0 && hint < max_len) max_len = hint;
+  const int max_pages = max_len > 0 ? ceil_div(max_len, bs) : 1;
+  const int cap = c.max_splits < max_pages ? c.max_splits : max_pages;
+  const int64_t base = (int64_t)batch * c.num_kv_heads, sms = num_sms > 0 ? num_sms : 1;
+  int64_t best = INT64_MAX;
+  *S_out = 1;
+  *chunk_out = max_pages;
+  for (int s = 1; s <= cap; ++s) {
+    const int pages = ceil_div(max_pages, s);
+    if (ceil_div(max_pages, pages) != s) continue;  // identical to a smaller split count
+    const int64_t tokens = ((int64_t)pages * bs + kChunk - 1) / kChunk * kChunk;
+    const int64_t merge = s > 1 ? kMerge * s : 0;
+    int64_t cost = ((base * s + sms - 1) / sms) * (tokens + kUnit) + merge;
+    if (batch > 1) {
+      const int64_t units4 = s > 2 ? s + 2 : 4;  // four times the splits of an average sequence
+      const int64_t spread = base * max_len / 4 / sms + base * units4 * kUnit / 4 / sms +
+                             base * (4 * s - units4 > 0 ? 4 * s - units4 : 0) * kVisit / 4 / sms +
+                             tokens / 2;
+      cost += (spread > tokens + kUnit ? spread : tokens + kUnit) + merge;
+    }
+    if (cost < best) {
+      best = cost;
+      *S_out = s;
+      *chunk_out = pages;
+    }
+  }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -298,7 +342,8 @@ int64_t call_max_len(const pda_config& c, int max_blocks, int hint) {
 // CTAs and, for the tensor-core kernel, whether the launch is one wave of
 // clusters (one per (sequence, kv head), the splits merging through
 // distributed shared memory) when every pair fits.
-LaunchShape launch_shape(const pda_handle_s* h, int batch, int max_blocks, int hint, int forced) {
+LaunchShape launch_shape(const pda_handle_s* h, int batch, int max_blocks, int hint, int forced,
+                         bool block_scales = false) {
   const pda_config& c = h->cfg;
   LaunchShape r{1, 1, 0, 0, 0, h->kernel, h->ctas_per_sm};
   if (h->small_cc &&
@@ -307,8 +352,11 @@ LaunchShape launch_shape(const pda_handle_s* h, int batch, int max_blocks, int h
     r.kernel = pda::kPartialCudaCore;
     r.ctas_per_sm = h->cc_ctas_per_sm;
   }
-  plan_splits(c, r.kernel, h->num_sms, r.ctas_per_sm, batch, max_blocks, hint, forced,
-              &r.splits, &r.chunk_pages);
+  if (block_scales && forced <= 0)
+    plan_block_scaled(c, h->num_sms, batch, max_blocks, hint, &r.splits, &r.chunk_pages);
+  else
+    plan_splits(c, r.kernel, h->num_sms, r.ctas_per_sm, batch, max_blocks, hint, forced,
+                &r.splits, &r.chunk_pages);
   r.units = (int64_t)r.splits * c.num_kv_heads * batch;
   if (r.kernel == pda::kPartialTensorCore) {
     const int64_t max_ctas = (int64_t)h->num_sms * r.ctas_per_sm;
@@ -397,7 +445,7 @@ int run_any(pda_handle h, const void* q, const void* k_cache, const void* v_cach
   }
 
   const LaunchShape shape =
-      launch_shape(h, batch, max_blocks, max_context_len_hint, num_splits);
+      launch_shape(h, batch, max_blocks, max_context_len_hint, num_splits, block_scales);
   const int S = shape.splits, chunk = shape.chunk_pages;
   const int64_t units = shape.units;
   if (units > INT_MAX) return fail(PDA_EINVAL, "splits * num_kv_heads * batch exceeds 2^31");

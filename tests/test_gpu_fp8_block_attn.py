@@ -219,6 +219,19 @@ def test_equal_scales_match_the_per_head_call():
     check(b, want, "head scales")
 
 
+def test_scales_of_one_block_and_of_heads_in_two_dimensions():
+    """A cache of one block, and per-head scales passed as [1, Hkv], both mean the heads' scales."""
+    p = Problem(16, 4, 8, 128, 16, [13], "bf16", extra_blocks=0)
+    assert p.ks.shape == (1, 8)
+    every_way(p, splits=(0,))
+    p = Problem(17, 4, 8, 128, 16, [300, 20], "bf16")
+    p.ks[:], p.vs[:] = p.ks[p.table[0, 0]], p.vs[p.table[0, 0]]
+    p.upload()
+    with p.attn() as attn:
+        one = {n: t[int(p.table[0, 0])][None].contiguous() for n, t in p.scales.items()}
+        check(attn.run(*p.dev, **one), p.want())
+
+
 def test_captured_and_replayed_with_a_cache_that_moves_on():
     p = Problem(13, 4, 2, 128, 16, [100, 200], "bf16").upload()
     with p.attn() as attn:
@@ -267,6 +280,10 @@ def test_refusals():
             attn.run(*p.dev, k_scale=ks.cpu(), v_scale=vs)
         with pytest.raises(ValueError):
             attn.run(*p.dev, k_scale=ks.half(), v_scale=vs)
+        with pytest.raises(ValueError):
+            attn.run(p.dev[0][:, :4].contiguous(), *p.dev[1:], k_scale=ks, v_scale=vs)
+        with pytest.raises(ValueError):
+            attn.run(*p.dev[:4], torch.cat([p.dev[4], p.dev[4]]), p.dev[5], k_scale=ks, v_scale=vs)
         q, kc, vc, table, lens, scale = p.dev
         out = torch.empty_like(q)
         args = lambda k, v, h: (h, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), k, v, table.data_ptr(),
