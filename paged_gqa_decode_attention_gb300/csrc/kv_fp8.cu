@@ -14,7 +14,7 @@
 //
 // A block that a call appends to behind tokens it holds keeps
 // s' = max(s, needed by the new rows); where s' > s its earlier values become
-// rn_e4m3(y * s / s'). One warp (two for 64-token blocks of 128 dims) owns the
+// rn_e4m3(y * s / s'). One warp (two or four where it has over 256 vectors) owns the
 // tile of one (block, K or V, head): nothing is exchanged between blocks of
 // threads, no atomics, the result does not depend on any order.
 //
@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kAppendWarps = 8;
 constexpr int kAppendThreads = 32 * kAppendWarps;
+constexpr int kQPairs = 4;  // vector pairs of a q row in flight per lane
 constexpr int kMinScaleExp = -60;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -78,70 +79,85 @@ __device__ __forceinline__ void record(int* err, int code, int detail) {
 // touched block and the last slot also the one after it. The unit count
 // floor(T / block_size) + B needs no device value.
 //
-// Returns the sequence of unit u (-1: none): a 32-way search for the last b
-// with base(b) <= u, one round of loads per factor of 32 of the batch.
-__device__ __forceinline__ int unit_sequence(const int64_t* cu, int B, int block_size, int64_t u,
-                                             int lane) {
-  int lo = 0, n = B;
+// unit_sequence: the sequence of unit u (b = -1: none), its rows and its length: a
+// 32-way search for the last b with base(b) <= u, one round of loads per factor
+// of 32 of the batch; the last round's lanes have loaded what is known of their
+// sequences along with it.
+struct UnitSeq {
+  int b, len;
+  int64_t r_lo, r_hi;
+};
+__device__ __forceinline__ UnitSeq unit_sequence(const AppendParams& p, int64_t u, int lane) {
+  int lo = 0, n = p.B;
+  UnitSeq r;
   while (true) {
     const int step = (n + 31) >> 5;
     const int i = lane * step;
+    int64_t c0 = 0, c1 = 0;
+    int len = 0;
     bool le = false;
-    if (i < n) le = __ldg(cu + lo + i) / block_size + (lo + i) <= u;
+    if (i < n) {
+      c0 = __ldg(p.cu + lo + i);
+      if (step == 1) {
+        c1 = __ldg(p.cu + lo + i + 1);
+        len = __ldg(p.lens + lo + i);
+      }
+      le = c0 / p.block_size + (lo + i) <= u;
+    }
     const int cnt = __popc(__ballot_sync(kAll, le));
-    if (cnt == 0) return -1;
-    lo += (cnt - 1) * step;
-    if (step == 1) return lo;
+    r.b = cnt == 0 ? -1 : lo + (cnt - 1) * step;
+    if (cnt == 0 || step == 1) {
+      const int src = cnt == 0 ? 0 : cnt - 1;
+      r.r_lo = __shfl_sync(kAll, c0, src);
+      r.r_hi = __shfl_sync(kAll, c1, src);
+      r.len = __shfl_sync(kAll, len, src);
+      return r;
+    }
     n = min(step, n - (cnt - 1) * step);
+    lo = r.b;
   }
 }
 
-// The vector of 8 elements at column `col` of a head row, rotated: pairs
-// (j, j + half) need the vector `half` columns away, which another lane of the
-// same row group holds; interleaved pairs lie inside the vector.
-template <typename F, bool kNeox>
-__device__ __forceinline__ uint4 rotate_vec(uint4 x, const float* cs, int col, int half, int lane) {
-  uint4 y = x;
-  if constexpr (kNeox) {
-    const int rot = 2 * half;
-    const int hop = col < half ? (half >> 3) : (col < rot ? -(half >> 3) : 0);
-    uint4 o;
-    o.x = __shfl_sync(kAll, x.x, lane + hop);
-    o.y = __shfl_sync(kAll, x.y, lane + hop);
-    o.z = __shfl_sync(kAll, x.z, lane + hop);
-    o.w = __shfl_sync(kAll, x.w, lane + hop);
-    if (hop != 0 && cs != nullptr) {
-      // lower half: x cos - o sin; upper half: x cos + o sin
-      const int j = col < half ? col : col - half;
-      const float sg = col < half ? -1.f : 1.f;
-      const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + j));
-      const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + j + 4));
-      const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half + j));
-      const float4 s1 = __ldg(reinterpret_cast<const float4*>(cs + half + j + 4));
-      y.x = rounded_dot2_x2<F>(F::lo_f(x.x), c0.x, sg * F::lo_f(o.x), s0.x,
-                               F::hi_f(x.x), c0.y, sg * F::hi_f(o.x), s0.y);
-      y.y = rounded_dot2_x2<F>(F::lo_f(x.y), c0.z, sg * F::lo_f(o.y), s0.z,
-                               F::hi_f(x.y), c0.w, sg * F::hi_f(o.y), s0.w);
-      y.z = rounded_dot2_x2<F>(F::lo_f(x.z), c1.x, sg * F::lo_f(o.z), s1.x,
-                               F::hi_f(x.z), c1.y, sg * F::hi_f(o.z), s1.y);
-      y.w = rounded_dot2_x2<F>(F::lo_f(x.w), c1.z, sg * F::lo_f(o.w), s1.z,
-                               F::hi_f(x.w), c1.w, sg * F::hi_f(o.w), s1.w);
-    }
-  } else {
-    if (col < 2 * half && cs != nullptr) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (col >> 1)));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + (col >> 1)));
-      auto pair = [](uint32_t w, float cc, float ss) {
-        const float a = F::lo_f(w), b = F::hi_f(w);
-        return rounded_dot2_x2<F>(a, cc, -b, ss, b, cc, a, ss);
-      };
-      y.x = pair(x.x, c.x, s.x);
-      y.y = pair(x.y, c.y, s.y);
-      y.z = pair(x.z, c.z, s.z);
-      y.w = pair(x.w, c.w, s.w);
+// Rotates the pair of vectors (A, B) that hold both elements of 8 rotated pairs:
+// c and s are their cosines and sines. Halves: pair i is (element i of A, element
+// i of B); adjacent pairs: the two halves of word i of A, then of B.
+template <typename F, bool kHalves>
+__device__ __forceinline__ void rotate_pair(uint4& A, uint4& B, const float (&c)[8],
+                                            const float (&s)[8]) {
+  uint32_t* a = &A.x;
+  uint32_t* b = &B.x;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if constexpr (kHalves) {
+      const float a0 = F::lo_f(a[w]), a1 = F::hi_f(a[w]), b0 = F::lo_f(b[w]), b1 = F::hi_f(b[w]);
+      a[w] = rounded_dot2_x2<F, true>(a0, c[2 * w], -b0, s[2 * w], a1, c[2 * w + 1], -b1, s[2 * w + 1]);
+      b[w] = rounded_dot2_x2<F, true>(b0, c[2 * w], a0, s[2 * w], b1, c[2 * w + 1], a1, s[2 * w + 1]);
+    } else {
+      float x = F::lo_f(a[w]), y = F::hi_f(a[w]);
+      a[w] = rounded_dot2_x2<F, true>(x, c[w], -y, s[w], y, c[w], x, s[w]);
+      x = F::lo_f(b[w]);
+      y = F::hi_f(b[w]);
+      b[w] = rounded_dot2_x2<F, true>(x, c[4 + w], -y, s[4 + w], y, c[4 + w], x, s[4 + w]);
     }
   }
-  return y;
+}
+
+// 8 cosines and sines from angle 8u on of a table row (rot / 2 cosines, then sines).
+__device__ __forceinline__ void load_angles(const float* cs, int u, int half, float (&c)[8],
+                                            float (&s)[8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(cs + 8 * u) + k);
+    const float4 y = __ldg(reinterpret_cast<const float4*>(cs + half + 8 * u) + k);
+    c[4 * k] = x.x;
+    c[4 * k + 1] = x.y;
+    c[4 * k + 2] = x.z;
+    c[4 * k + 3] = x.w;
+    s[4 * k] = y.x;
+    s[4 * k + 1] = y.y;
+    s[4 * k + 2] = y.z;
+    s[4 * k + 3] = y.w;
+  }
 }
 
 template <typename F>
@@ -214,12 +230,23 @@ enum Rope { kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2 };
 // CTAs below p.kv_ctas: a unit's tiles, W warps per tile; the others (rope):
 // one q row per warp.
 template <typename F, int D, int NV, int W, int kRope>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  constexpr int kCols = D / 8;           // vectors of a head row (8 or 16)
-  constexpr int kRowsPerStep = 32 / kCols;
+__global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) append_kernel(const AppendParams p) {
+  // A lane's two vectors of a row are the A and B of one rotation item (8 pairs), or
+  // any two where nothing rotates; kItems lanes cover a row.
+  constexpr int kItems = D / 16;
+  constexpr int kRowsPerStep = 32 / kItems;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = (lane & (kCols - 1)) * 8;
+  const int u16 = lane & (kItems - 1), sub = lane / kItems;
   const int half = p.rot_dim >> 1;
+  const bool rotates = kRope != kRopeNone && 16 * u16 < p.rot_dim;
+  int colA = 8 * u16, colB = 8 * u16 + D / 2;
+  if constexpr (kRope == kRopeHalves) {
+    colA = rotates ? 8 * u16 : 16 * u16;
+    colB = rotates ? 8 * u16 + half : 16 * u16 + 8;
+  } else if constexpr (kRope == kRopePairs) {
+    colA = 16 * u16;
+    colB = 16 * u16 + 8;
+  }
 
   if (kRope != kRopeNone && blockIdx.x >= p.kv_ctas) {
     const int64_t r = ((int64_t)blockIdx.x - p.kv_ctas) * kAppendWarps + warp;
@@ -230,22 +257,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (lane == 0) record(p.err, kErrPosition, (int)r);
       return;
     }
-    const float* cs = p.cos_sin + (int64_t)pos * p.rot_dim;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + r * p.q_stride);
-    uint4* dst = reinterpret_cast<uint4*>(p.q_out + r * p.qo_stride);
-    const int n = p.Hq * kCols;
-    for (int i0 = 0; i0 < n; i0 += 32 * 4) {
-      uint4 x[4];
+    float c[8], s[8];
+    if (rotates) load_angles(p.cos_sin + (int64_t)pos * p.rot_dim, u16, half, c, s);
+    const uint16_t* src = p.q + r * p.q_stride;
+    uint16_t* dst = p.q_out + r * p.qo_stride;
+    for (int h0 = 0; h0 < p.Hq; h0 += kQPairs * kRowsPerStep) {
+      uint4 A[kQPairs], B[kQPairs];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int idx = i0 + i * 32 + lane;
-        x[i] = idx < n ? src[idx] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kQPairs; ++i) {
+        const int h = h0 + i * kRowsPerStep + sub;
+        if (h < p.Hq) {
+          A[i] = *reinterpret_cast<const uint4*>(src + h * D + colA);
+          B[i] = *reinterpret_cast<const uint4*>(src + h * D + colB);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int idx = i0 + i * 32 + lane;
-        const uint4 y = rotate_vec<F, kRope == kRopeHalves>(x[i], cs, col, half, lane);
-        if (idx < n) dst[idx] = y;
+      for (int i = 0; i < kQPairs; ++i) {
+        const int h = h0 + i * kRowsPerStep + sub;
+        if (h < p.Hq) {
+          if (rotates) rotate_pair<F, kRope == kRopeHalves>(A[i], B[i], c, s);
+          *reinterpret_cast<uint4*>(dst + h * D + colA) = A[i];
+          *reinterpret_cast<uint4*>(dst + h * D + colB) = B[i];
+        }
       }
     }
     return;
@@ -254,11 +287,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __shared__ uint32_t s_max[kAppendWarps];
   const int64_t u = blockIdx.x / p.groups;
   const int grp = blockIdx.x - (int)(u * p.groups);
-  const int b = unit_sequence(p.cu, p.B, p.block_size, u, lane);
+  const UnitSeq seq = unit_sequence(p, u, lane);
+  const int b = seq.b, len = seq.len;
   if (b < 0) return;
-  const int64_t r_lo = __ldg(p.cu + b), r_hi = __ldg(p.cu + b + 1);
-  const int len = __ldg(p.lens + b);
-  const int64_t n = r_hi - r_lo;
+  const int64_t r_lo = seq.r_lo, r_hi = seq.r_hi, n = r_hi - r_lo;
   const int bs = p.block_size;
   const int64_t base = r_lo / bs + b, slots = r_hi / bs + b + 1 - base;
   const int64_t j = u - base;
@@ -280,41 +312,46 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   float* scales = is_v ? p.v_scale : p.k_scale;
 
   for (int page = start / bs + (int)j; page <= last_page; ++page) {
-    const int blk = __ldg(p.table + (int64_t)b * p.max_blocks + page);
-    const bool blk_ok = blk >= 0 && blk < p.num_blocks;
-    if (!blk_ok && threadIdx.x == 0) record(p.err, kErrBlockId, b);
     const int t_lo = max(start, page * bs), t_hi = min(len, (page + 1) * bs);
     const int off = t_lo - page * bs, nr = t_hi - t_lo;
     const int64_t row0 = r_lo + (t_lo - start);
+    // the rows and the block id are requested together
+    const int blk = __ldg(p.table + (int64_t)b * p.max_blocks + page);
+    uint4 x[NV];        // NV / 2 rows' A and B
+    bool live[NV / 2];  // the row is written
+    auto row_of = [&](int i) { return (i * W + wsub) * kRowsPerStep + sub; };
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      live[i] = has_tile && row_of(i) < nr;
+      x[2 * i] = x[2 * i + 1] = make_uint4(0, 0, 0, 0);
+      if (live[i]) {
+        const uint16_t* src = x_rows + (row0 + row_of(i)) * x_stride + h * D;
+        x[2 * i] = __ldg(reinterpret_cast<const uint4*>(src + colA));
+        x[2 * i + 1] = __ldg(reinterpret_cast<const uint4*>(src + colB));
+      }
+    }
+    const bool blk_ok = blk >= 0 && blk < p.num_blocks;
+    if (!blk_ok && threadIdx.x == 0) record(p.err, kErrBlockId, b);
     const bool active = has_tile && blk_ok;
     const int64_t sidx = (int64_t)(blk_ok ? blk : 0) * p.Hkv + (has_tile ? h : 0);
     float old = 0.f;
     if (active && off > 0) old = scales[sidx];
-    uint4 x[NV];
-    bool live[NV];  // the row is written
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int row = (i * W + wsub) * kRowsPerStep + lane / kCols;
-      live[i] = active && row < nr;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (live[i])
-        x[i] = __ldg(reinterpret_cast<const uint4*>(x_rows + (row0 + row) * x_stride + h * D + col));
-    }
     if constexpr (kRope != kRopeNone) {
+      int pos[NV / 2];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int row = (i * W + wsub) * kRowsPerStep + lane / kCols;
-        const float* cs = nullptr;
+      for (int i = 0; i < NV / 2; ++i) pos[i] = live[i] ? __ldg(p.positions + row0 + row_of(i)) : 0;
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) {
         if (live[i]) {
-          const int pos = __ldg(p.positions + row0 + row);
-          live[i] = pos >= 0 && pos < p.max_position;
-          cs = p.cos_sin + (int64_t)pos * p.rot_dim;
-          if (!live[i]) {
-            x[i] = make_uint4(0, 0, 0, 0);
-            cs = nullptr;
+          if (pos[i] < 0 || pos[i] >= p.max_position) {  // writes nothing (q's CTA reports it)
+            live[i] = false;
+            x[2 * i] = x[2 * i + 1] = make_uint4(0, 0, 0, 0);
+          } else if (rotates && !is_v) {
+            float c[8], s[8];
+            load_angles(p.cos_sin + (int64_t)pos[i] * p.rot_dim, u16, half, c, s);
+            rotate_pair<F, kRope == kRopeHalves>(x[2 * i], x[2 * i + 1], c, s);
           }
         }
-        if (!is_v) x[i] = rotate_vec<F, kRope == kRopeHalves>(x[i], cs, col, half, lane);
       }
     }
     // largest magnitude of the tile
@@ -367,13 +404,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       const bool pow2 = is_normal_power_of_two(s);
       const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+      for (int i = 0; i < NV / 2; ++i) {
         if (live[i]) {
-          const int row = (i * W + wsub) * kRowsPerStep + lane / kCols;
-          uint2 y;
-          if (pow2 && !nonfinite) y = quantise<F, true, false>(x[i], s, inv);
-          else y = quantise<F, false, true>(x[i], s, inv);
-          *reinterpret_cast<uint2*>(tile_base + (off + row) * row_bytes + col) = y;
+          uint8_t* dst = tile_base + (off + row_of(i)) * row_bytes;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint2 y;
+            if (pow2 && !nonfinite) y = quantise<F, true, false>(x[2 * i + k], s, inv);
+            else y = quantise<F, false, true>(x[2 * i + k], s, inv);
+            *reinterpret_cast<uint2*>(dst + (k == 0 ? colA : colB)) = y;
+          }
         }
       }
     }
@@ -535,16 +575,17 @@ void launch_append(const AppendParams& p, int rope, unsigned grid, cudaStream_t 
 
 template <typename F>
 void launch_append_geometry(const AppendParams& p, int D, int rope, unsigned grid, cudaStream_t s) {
-  // NV * W * 256 = block_size * D / 8 vectors of a tile
+  // NV * W * 32 = block_size * D / 8 vectors of a tile: at most 8 a lane, so that
+  // four CTAs fit an SM and their chains of loads overlap
   const int tile = p.block_size * D;
   if (D == 64) {
     if (tile == 1024) launch_append<F, 64, 4, 1>(p, rope, grid, s);
     else if (tile == 2048) launch_append<F, 64, 8, 1>(p, rope, grid, s);
-    else launch_append<F, 64, 16, 1>(p, rope, grid, s);
+    else launch_append<F, 64, 8, 2>(p, rope, grid, s);
   } else {
     if (tile == 2048) launch_append<F, 128, 8, 1>(p, rope, grid, s);
-    else if (tile == 4096) launch_append<F, 128, 16, 1>(p, rope, grid, s);
-    else launch_append<F, 128, 16, 2>(p, rope, grid, s);
+    else if (tile == 4096) launch_append<F, 128, 8, 2>(p, rope, grid, s);
+    else launch_append<F, 128, 8, 4>(p, rope, grid, s);
   }
 }
 
@@ -609,7 +650,7 @@ int append_impl(AppendParams p, int D, int dtype, int rope, int device, void* st
   if (rope != kRopeNone && !q_in_place && overlaps(outs[5], rq))
     return fail(PDA_EALIAS, "q_out overlaps q (only the exact in-place form is allowed)");
 
-  const int W = (p.block_size * D == 8192) ? 2 : 1;  // warps per tile
+  const int W = std::max(1, p.block_size * D / 2048);  // warps per tile
   const int tiles = kAppendWarps / W;
   p.groups = (2 * p.Hkv + tiles - 1) / tiles;
   p.kv_ctas = (p.T / p.block_size + p.B) * p.groups;

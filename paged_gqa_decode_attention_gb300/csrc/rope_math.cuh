@@ -52,7 +52,17 @@ __device__ __forceinline__ float round_to_odd_float(double d) {
 // both are recomputed in double and rounded through a round-to-odd float.
 // The bound is kept tight (per output) because a warp takes the slow path
 // whenever one of its lanes does.
+// kCold: the double-precision path is a call, not inlined code, for kernels that
+// unroll many of these and would not fit the instruction caches otherwise.
 template <typename F>
+__device__ __noinline__ uint32_t rounded_dot2_x2_exact(float a0, float b0, float c0, float d0,
+                                                       float a1, float b1, float c1, float d1) {
+  const double e0 = __dadd_rn(__dmul_rn((double)a0, (double)b0), __dmul_rn((double)c0, (double)d0));
+  const double e1 = __dadd_rn(__dmul_rn((double)a1, (double)b1), __dmul_rn((double)c1, (double)d1));
+  return F::pack2(round_to_odd_float(e0), round_to_odd_float(e1));
+}
+
+template <typename F, bool kCold = false>
 __device__ __forceinline__ uint32_t rounded_dot2_x2(float a0, float b0, float c0, float d0,
                                                     float a1, float b1, float c1, float d1) {
   const float p0 = __fmul_rn(c0, d0), p1 = __fmul_rn(c1, d1);
@@ -62,6 +72,7 @@ __device__ __forceinline__ uint32_t rounded_dot2_x2(float a0, float b0, float c0
   const uint32_t lo = F::pack2(__fsub_rd(r0, m0), __fsub_rd(r1, m1));
   const uint32_t hi = F::pack2(__fadd_ru(r0, m0), __fadd_ru(r1, m1));
   if (lo == hi) return lo;
+  if constexpr (kCold) return rounded_dot2_x2_exact<F>(a0, b0, c0, d0, a1, b1, c1, d1);
   const double e0 = __dadd_rn(__dmul_rn((double)a0, (double)b0), __dmul_rn((double)c0, (double)d0));
   const double e1 = __dadd_rn(__dmul_rn((double)a1, (double)b1), __dmul_rn((double)c1, (double)d1));
   return F::pack2(round_to_odd_float(e0), round_to_odd_float(e1));
