@@ -236,9 +236,8 @@ class PagedDecodeAttention:
         for a block-scaled cache (append_kv_fp8), both [num_blocks, Hkv]."""
         # two dimensions and more values than heads: block scales (with one block they are
         # the heads' scales)
-        if self.kv_fp8 and any([t is not None and t.dim() == 2 and
-                                t.numel() not in (1, self.config.num_kv_heads)
-                                for t in (k_scale, v_scale)]):
+        if self.kv_fp8 and (_is_block_scale(k_scale, self._geometry[1]) or
+                            _is_block_scale(v_scale, self._geometry[1])):
             return self._run_block_scaled(q, k_cache, v_cache, block_table, context_lens, scale,
                                           out, num_splits, max_context_len_hint, out_dtype,
                                           stream, k_scale, v_scale)
@@ -285,21 +284,19 @@ class PagedDecodeAttention:
         Hq, Hkv, bs, D = self._geometry
         if k_scale is None or v_scale is None:
             raise ValueError("block scales: k_scale and v_scale must both be [num_blocks, Hkv]")
-        if _fp8_device(k_cache, v_cache, k_scale, v_scale) != dev:
-            raise ValueError(f"the cache must be on cuda:{dev}, the handle's device")
-        if k_cache.shape[1:] != (bs, Hkv, D):
+        nb, c_bs, c_hkv, c_d = _fp8_shape(k_cache, v_cache, k_scale, v_scale)
+        if c_bs != bs or c_hkv != Hkv or c_d != D:
             raise ValueError("caches must be [num_blocks, block_size, Hkv, D] with the handle's sizes")
-        shape = q.shape
-        if len(shape) != 3 or shape[1:] != (Hq, D):
+        B = len(q)
+        if q.dim() != 3 or q.numel() != B * Hq * D or q.shape[1] != Hq:
             raise ValueError("q must be [batch, Hq, D] with the handle's sizes")
-        B = shape[0]
-        if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
+        if block_table.dim() != 2 or len(block_table) != B or context_lens.shape != (B,):
             raise ValueError("block_table must be [batch, max_blocks] and context_lens [batch]")
         if out_dtype is None:
             out_dtype = dt
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=q.device)
-        elif out.shape != shape:
+            out = torch.empty_like(q, dtype=out_dtype)
+        elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
         p = _pointers(dev, (("q", q, dt), ("k_cache", k_cache, None), ("v_cache", v_cache, None),
                             ("k_scale", k_scale, torch.float32),
@@ -307,9 +304,10 @@ class PagedDecodeAttention:
                             ("block_table", block_table, torch.int32),
                             ("context_lens", context_lens, torch.int32), ("out", out, out_dtype)))
         status = self.lib.paged_decode_attn_run_block_scaled(
-            self.handle, p[0], p[1], p[2], p[3], p[4], p[5], p[6], B, block_table.shape[1],
-            k_cache.shape[0], 1.0 / math.sqrt(D) if scale is None else float(scale), p[7],
-            _stream_on(stream, dev), int(num_splits), int(max_context_len_hint), _DT[out_dtype])
+            self.handle, *p[:7], B, block_table.shape[1], nb,
+            D ** -0.5 if scale is None else scale, p[7],
+            _raw_stream(dev) if stream is None else _stream_ptr(stream), num_splits,
+            max_context_len_hint, _DT[out_dtype])
         if status:
             _check(self.lib, status)
         return out
@@ -531,10 +529,15 @@ def _pointers(device: int, named) -> list[int]:
     out = []
     for name, t, dtype in named:
         if t.get_device() != device or not t.is_contiguous() or (
-                dtype is not None and t.dtype != dtype):
+                dtype is not None and t.dtype is not dtype):
             _refuse(name, t, device, dtype)
         out.append(t.data_ptr())
     return out
+
+
+def _is_block_scale(t, num_kv_heads: int) -> bool:
+    """Two dimensions and more values than heads (with one block they are the heads' scales)."""
+    return t is not None and t.dim() == 2 and t.numel() not in (1, num_kv_heads)
 
 
 def _rows16(name: str, t: torch.Tensor, device: int, dtype) -> tuple[int, int]:
@@ -548,20 +551,14 @@ def _rows16(name: str, t: torch.Tensor, device: int, dtype) -> tuple[int, int]:
     return t.data_ptr(), (s0 if T > 1 else H * D)
 
 
-def _stream_on(stream, device: int) -> int:
-    """`stream`, or torch's current stream of `device` (which need not be the current one)."""
-    if stream is None:
-        return _raw_stream(device)
-    return _stream_ptr(stream)
-
-
+# torch's current stream of a device, which need not be the current one
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _fp8_device(k_cache, v_cache, k_scale, v_scale) -> int:
-    """Device of a block-scaled FP8 cache: [num_blocks, block_size, Hkv, D] E4M3 bytes and
-    [num_blocks, Hkv] fp32 scales."""
+def _fp8_shape(k_cache, v_cache, k_scale, v_scale):
+    """(num_blocks, block_size, Hkv, D) of a block-scaled FP8 cache: [num_blocks, block_size,
+    Hkv, D] E4M3 bytes and [num_blocks, Hkv] fp32 scales."""
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_blocks, block_size, Hkv, D] alike")
@@ -570,16 +567,22 @@ def _fp8_device(k_cache, v_cache, k_scale, v_scale) -> int:
     want = (shape[0], shape[2])
     if k_scale.shape != want or v_scale.shape != want:
         raise ValueError("k_scale and v_scale must be [num_blocks, Hkv]")
-    if not k_cache.is_cuda:
+    return shape
+
+
+def _cuda_device(t: torch.Tensor) -> int:
+    device = t.get_device()
+    if device < 0:
         raise ValueError("k_cache must be a CUDA tensor")
-    return k_cache.get_device()
+    return device
 
 
 def _append_args(device, k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
                  cu_rows, err, stream):
     """Checks shared by the two appends; the cache and sequence arguments of the C calls."""
-    nb, bs, Hkv, D = k_cache.shape
-    if k.shape != v.shape or k.shape[1:] != (Hkv, D):
+    nb, bs, Hkv, D = _fp8_shape(k_cache, v_cache, k_scale, v_scale)
+    rows = k.shape
+    if v.shape != rows or rows[1] != Hkv or rows[2] != D:
         raise ValueError("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_blocks]")
@@ -595,8 +598,9 @@ def _append_args(device, k, v, k_cache, v_cache, k_scale, v_scale, block_table, 
             raise ValueError("err must hold two int32 values")
         named.append(("err", err, torch.int32))
     ptr = _pointers(device, named)
-    return (ptr[0], ptr[1], ptr[2], ptr[3], nb, bs, ptr[4], width, ptr[5], ptr[6], B,
-            ptr[7] if err is not None else None, device, _stream_on(stream, device))
+    return (*ptr[:4], nb, bs, ptr[4], width, ptr[5], ptr[6], B,
+            ptr[7] if err is not None else None, device,
+            _raw_stream(device) if stream is None else _stream_ptr(stream))
 
 
 def append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -617,7 +621,7 @@ def append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     dt = k.dtype
     if dt not in _DT16 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("k and v must be bfloat16 or float16 [rows, heads, head_dim]")
-    dev = _fp8_device(k_cache, v_cache, k_scale, v_scale)
+    dev = _cuda_device(k_cache)
     kp, ks = _rows16("k", k, dev, dt)
     vp, vs = _rows16("v", v, dev, dt)
     args = _append_args(dev, k, v, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
@@ -648,7 +652,7 @@ def rope_append_kv_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     T, Hq, D = q.shape
     if k.shape[0] != T or k.shape[2] != D:
         raise ValueError("k and v must have q's rows and head_dim")
-    dev = _fp8_device(k_cache, v_cache, k_scale, v_scale)
+    dev = _cuda_device(k_cache)
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
     elif q_out.shape != q.shape:
@@ -683,8 +687,8 @@ def gather_kv_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_rows
     exclusive prefix sums of lens, computed on the host from lens). Returns
     (k_out, v_out)."""
     lib = _lib or load_library()
-    dev = _fp8_device(k_cache, v_cache, k_scale, v_scale)
-    nb, bs, Hkv, D = k_cache.shape
+    nb, bs, Hkv, D = _fp8_shape(k_cache, v_cache, k_scale, v_scale)
+    dev = _cuda_device(k_cache)
     if (k_out is None) != (v_out is None):
         raise ValueError("pass both k_out and v_out, or neither")
     if block_table.dim() != 2:
@@ -720,7 +724,8 @@ def gather_kv_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_rows
     p = _pointers(dev, named)
     status = lib.paged_decode_attn_gather_kv_fp8(
         p[0], p[1], p[2], p[3], nb, bs, Hkv, D, p[4], width, p[5], p[6], B, int(max_len), p[7],
-        p[8], shape[0], _DT[dt], p[9] if err is not None else None, dev, _stream_on(stream, dev))
+        p[8], shape[0], _DT[dt], p[9] if err is not None else None, dev,
+        _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if status:
         _check(lib, status)
     return k_out, v_out
