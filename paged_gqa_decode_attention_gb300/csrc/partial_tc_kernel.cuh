@@ -1507,7 +1507,8 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
 #pragma unroll
               for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
             }
-            if (lane == 0) rb[wq * 8 + j] = mx;
+            // BSC: a head's four maxima side by side, one load each
+            if (lane == 0) rb[BSC ? j * 4 + wq : wq * 8 + j] = mx;
           }
           named_bar_sync(bar, 128);
           // every softmax thread has read the row scales of this unit's Q buffer
@@ -1519,11 +1520,17 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
           // knows, so interleaved they would serialise the columns.
 #pragma unroll
           for (int j = 0; j < kGA; ++j) {
-            const float mx = fmaxf(fmaxf(rb[j], rb[8 + j]), fmaxf(rb[16 + j], rb[24 + j]));
+            float mx;
+            if constexpr (BSC) {
+              const float4 m4 = reinterpret_cast<const float4*>(rb)[j];
+              mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+            } else {
+              mx = fmaxf(fmaxf(rb[j], rb[8 + j]), fmaxf(rb[16 + j], rb[24 + j]));
+            }
             const float mn = fmaxf(m_run[j], mx);  // finite: every chunk holds a valid token
-            alpha[j] = exp2f(m_run[j] - mn);
+            alpha[j] = BSC ? ex2_ftz(m_run[j] - mn) : exp2f(m_run[j] - mn);
             m_run[j] = mn;
-            prs[j] = exp2f(s[j] - mn);
+            prs[j] = BSC ? ex2_ftz(s[j] - mn) : exp2f(s[j] - mn);
             l_th[j] = l_th[j] * alpha[j] + (BSC ? prs[j] * ts.z : prs[j]);
           }
           if constexpr (BSC) {
