@@ -83,10 +83,19 @@ __device__ __forceinline__ void record(int* err, int code, int detail) {
 // 32-way search for the last b with base(b) <= u, one round of loads per factor
 // of 32 of the batch; the last round's lanes have loaded what is known of their
 // sequences along with it.
+// (A division by a block size that the compiler does not know would cost more
+// than the rows.)
+template <int BS>
+__device__ __forceinline__ int64_t block_index(int64_t x) {
+  static_assert((BS & (BS - 1)) == 0, "a power of two");
+  return x >> (BS == 16 ? 4 : BS == 32 ? 5 : 6);
+}
+
 struct UnitSeq {
   int b, len;
   int64_t r_lo, r_hi;
 };
+template <int BS>
 __device__ __forceinline__ UnitSeq unit_sequence(const AppendParams& p, int64_t u, int lane) {
   int lo = 0, n = p.B;
   UnitSeq r;
@@ -102,7 +111,7 @@ __device__ __forceinline__ UnitSeq unit_sequence(const AppendParams& p, int64_t 
         c1 = __ldg(p.cu + lo + i + 1);
         len = __ldg(p.lens + lo + i);
       }
-      le = c0 / p.block_size + (lo + i) <= u;
+      le = block_index<BS>(c0) + (lo + i) <= u;
     }
     const int cnt = __popc(__ballot_sync(kAll, le));
     r.b = cnt == 0 ? -1 : lo + (cnt - 1) * step;
@@ -189,9 +198,8 @@ __device__ __forceinline__ float block_scale(float a) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ bool is_normal_power_of_two(float s) {
-  const uint32_t u = __float_as_uint(s);
-  return (u & 0x7fffffu) == 0 && u >= (1u << 23) && u <= (253u << 23);
+__device__ __forceinline__ bool is_power_of_two(float s) {  // a normal one
+  return (__float_as_uint(s) & 0x7fffffu) == 0;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -213,16 +221,54 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&x)[4]) {
 
 // One vector of 8 16-bit elements over the scale s, as 8 E4M3 bytes. E4M3 has
 // no infinity: a non-finite element is stored as NaN.
-template <typename F, bool kPow2, bool kNonFinite>
-__device__ __forceinline__ uint2 quantise(uint4 x, float s, float inv) {
-  auto q = [&](float a) {
-    if (kNonFinite && isinf(a)) return __uint_as_float(0x7fc00000u);
-    return kPow2 ? a * inv : __fdiv_rn(a, s);
-  };
+template <typename F>
+__device__ __forceinline__ uint2 quantise_any(uint4 x, float s) {
+  auto q = [&](float a) { return isinf(a) ? __uint_as_float(0x7fc00000u) : __fdiv_rn(a, s); };
   uint2 y;
   y.x = e4m3x4(q(F::lo_f(x.x)), q(F::hi_f(x.x)), q(F::lo_f(x.y)), q(F::hi_f(x.y)));
   y.y = e4m3x4(q(F::lo_f(x.z)), q(F::hi_f(x.z)), q(F::lo_f(x.w)), q(F::hi_f(x.w)));
   return y;
+}
+
+// The same for finite elements and a power of two s whose reciprocal fits the
+// 16-bit type (twice, for fp16: inv is its square root or near it), in 16-bit
+// arithmetic. A product is exact except among the type's subnormals, and there it
+// is nowhere near the E4M3 rounding borders (multiples of 2^-10; an fp16 product
+// between 2^-11 and 2^-9 has its last bit at 2^-21 or above).
+__device__ __forceinline__ uint2 quantise_pow2(uint4 x, uint32_t inv_a, uint32_t, Bf16) {
+  const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&inv_a);
+  auto q = [&](uint32_t w) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), f);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  };
+  const uint32_t a = q(x.x), b = q(x.y), c = q(x.z), d = q(x.w);
+  return make_uint2(e4m3x4(Bf16::lo_f(a), Bf16::hi_f(a), Bf16::lo_f(b), Bf16::hi_f(b)),
+                    e4m3x4(Bf16::lo_f(c), Bf16::hi_f(c), Bf16::lo_f(d), Bf16::hi_f(d)));
+}
+__device__ __forceinline__ uint2 quantise_pow2(uint4 x, uint32_t inv_a, uint32_t inv_b, Fp16) {
+  const __half2 f = *reinterpret_cast<const __half2*>(&inv_a);
+  const __half2 g = *reinterpret_cast<const __half2*>(&inv_b);
+  auto q = [&](uint32_t w) {
+    const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w), f), g);
+    return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(y), __NV_SATFINITE, __NV_E4M3);
+  };
+  return make_uint2(q(x.x) | (q(x.y) << 16), q(x.z) | (q(x.w) << 16));
+}
+
+// Whether 1 / 2^e can be applied so, and the factors (pairs of the 16-bit type).
+__device__ __forceinline__ bool pow2_factors(int e, uint32_t& a, uint32_t& b, Bf16) {
+  a = (uint32_t)(127 - e) << 7;  // |e| <= 120
+  a |= a << 16;
+  b = 0;
+  return e >= -120 && e <= 120;
+}
+__device__ __forceinline__ bool pow2_factors(int e, uint32_t& a, uint32_t& b, Fp16) {
+  const int ea = -e / 2, eb = -e - ea;
+  a = (uint32_t)(15 + ea) << 10;
+  b = (uint32_t)(15 + eb) << 10;
+  a |= a << 16;
+  b |= b << 16;
+  return e >= -28 && e <= 28;
 }
 
 enum Rope { kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2 };
@@ -234,6 +280,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
   // A lane's two vectors of a row are the A and B of one rotation item (8 pairs), or
   // any two where nothing rotates; kItems lanes cover a row.
   constexpr int kItems = D / 16;
+  constexpr int BS = NV * W * 256 / D;  // block size
   constexpr int kRowsPerStep = 32 / kItems;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u16 = lane & (kItems - 1), sub = lane / kItems;
@@ -285,14 +332,13 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
   }
 
   __shared__ uint32_t s_max[kAppendWarps];
-  const int64_t u = blockIdx.x / p.groups;
-  const int grp = blockIdx.x - (int)(u * p.groups);
-  const UnitSeq seq = unit_sequence(p, u, lane);
+  const int u = (int)blockIdx.x / p.groups, grp = (int)blockIdx.x - u * p.groups;
+  const UnitSeq seq = unit_sequence<BS>(p, u, lane);
   const int b = seq.b, len = seq.len;
   if (b < 0) return;
   const int64_t r_lo = seq.r_lo, r_hi = seq.r_hi, n = r_hi - r_lo;
-  const int bs = p.block_size;
-  const int64_t base = r_lo / bs + b, slots = r_hi / bs + b + 1 - base;
+  constexpr int bs = BS;
+  const int64_t base = block_index<BS>(r_lo) + b, slots = block_index<BS>(r_hi) + b + 1 - base;
   const int64_t j = u - base;
   if (n == 0 || j >= slots) return;
   if (r_lo < 0 || n < 0 || r_hi > p.T || n > len || (int64_t)len > (int64_t)p.max_blocks * bs) {
@@ -300,7 +346,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
     return;
   }
   const int start = len - (int)n;
-  const int last_page = (len - 1) / bs;
+  const int last_page = (int)((unsigned)(len - 1) / bs);
   const int tile = grp * (kAppendWarps / W) + warp / W;
   const int wsub = warp % W;
   const bool has_tile = tile < 2 * p.Hkv;
@@ -311,7 +357,7 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
   uint8_t* cache = is_v ? p.v_cache : p.k_cache;
   float* scales = is_v ? p.v_scale : p.k_scale;
 
-  for (int page = start / bs + (int)j; page <= last_page; ++page) {
+  for (int page = (int)((unsigned)start / bs) + (int)j; page <= last_page; ++page) {
     const int t_lo = max(start, page * bs), t_hi = min(len, (page + 1) * bs);
     const int off = t_lo - page * bs, nr = t_hi - t_lo;
     const int64_t row0 = r_lo + (t_lo - start);
@@ -401,8 +447,9 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
         }
       }
       if (wsub == 0 && lane == 0) scales[sidx] = s;
-      const bool pow2 = is_normal_power_of_two(s);
-      const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+      uint32_t fa, fb;
+      const bool quick = pow2_factors((int)(__float_as_uint(s) >> 23) - 127, fa, fb, F()) &&
+                         is_power_of_two(s) && !nonfinite;
 #pragma unroll
       for (int i = 0; i < NV / 2; ++i) {
         if (live[i]) {
@@ -410,8 +457,8 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint2 y;
-            if (pow2 && !nonfinite) y = quantise<F, true, false>(x[2 * i + k], s, inv);
-            else y = quantise<F, false, true>(x[2 * i + k], s, inv);
+            if (quick) y = quantise_pow2(x[2 * i + k], fa, fb, F());
+            else y = quantise_any<F>(x[2 * i + k], s);
             *reinterpret_cast<uint2*>(dst + (k == 0 ? colA : colB)) = y;
           }
         }
@@ -458,15 +505,18 @@ struct GatherParams {
   uint4* v_out;
   int* err;
   int64_t num_blocks, out_rows;
-  int block_size, max_blocks, max_len, Hkv, D;
+  int block_size, max_blocks, max_len, Hkv;
+  uint32_t div_mul;  // ceil(2^32 / Hkv); 0 for Hkv = 1
 };
 
 constexpr int kGatherThreads = 256;
 constexpr int kGatherVec = 4;  // vectors in flight per thread
 
 // grid (pages, sequences, 2): one block's tokens of K (z = 0) or V. A block's
-// rows are contiguous in the cache and in the output.
-template <typename T>
+// rows are contiguous in the cache and in the output. x / Hkv is a multiplication
+// (p.div_mul, exact for the x = token * Hkv + head of a block: ceil(2^32 / Hkv) * x
+// is below the next multiple of 2^32 while x * Hkv < 2^32).
+template <typename T, int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const GatherParams p) {
   constexpr int E = Pack<T>::n;  // elements of an output vector
   const int b = blockIdx.y, page = blockIdx.x;
@@ -485,12 +535,12 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Gather
     return;
   }
   const bool is_v = blockIdx.z != 0;
-  const int64_t row_elems = (int64_t)p.Hkv * p.D;
+  const int64_t row_elems = (int64_t)p.Hkv * D;
   const uint8_t* src = (is_v ? p.v : p.k) + (int64_t)blk * p.block_size * row_elems;
   uint4* dst = (is_v ? p.v_out : p.k_out) + row0 * row_elems / E;
   const float* sc = (is_v ? p.v_scale : p.k_scale) + (int64_t)blk * p.Hkv;
   const int n = nr * (int)row_elems / E;
-  const int per_head = p.D / E;
+  constexpr int per_head = D / E;
   for (int i0 = threadIdx.x; i0 < n; i0 += kGatherThreads * kGatherVec) {
     uint2 w[kGatherVec];
     float s[kGatherVec];
@@ -500,7 +550,9 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const Gather
       if (i < n) {
         if constexpr (E == 8) w[t] = __ldg(reinterpret_cast<const uint2*>(src) + i);
         else w[t].x = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
-        s[t] = __ldg(sc + (i / per_head) % p.Hkv);
+        const uint32_t row_head = (uint32_t)i / per_head;
+        const uint32_t row = p.Hkv == 1 ? row_head : __umulhi(row_head, p.div_mul);
+        s[t] = __ldg(sc + (row_head - row * (uint32_t)p.Hkv));
       }
     }
 #pragma unroll
@@ -750,8 +802,7 @@ extern "C" int paged_decode_attn_gather_kv_fp8(
     return fail(PDA_EINVAL, "out_dtype must be PDA_BF16, PDA_FP16 or PDA_F32");
   const int st = pda::check_cache(num_kv_heads, head_dim, block_size, num_blocks);
   if (st != PDA_OK) return st;
-  if ((int64_t)num_kv_heads * head_dim * block_size > INT_MAX)
-    return fail(PDA_EINVAL, "a block holds more than 2^31 values");
+  if (num_kv_heads > 8191) return fail(PDA_EUNSUPPORTED, "more than 8191 kv heads");
   if (batch == 0 || max_len == 0) return PDA_OK;
   if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !lens || !cu_rows ||
       (out_rows > 0 && (!k_out || !v_out)))
@@ -796,13 +847,18 @@ extern "C" int paged_decode_attn_gather_kv_fp8(
   p.max_blocks = max_blocks;
   p.max_len = max_len;
   p.Hkv = num_kv_heads;
-  p.D = head_dim;
+  p.div_mul = num_kv_heads > 1 ? (uint32_t)(((1ull << 32) + num_kv_heads - 1) / num_kv_heads) : 0u;
   pda::Dev guard(device);
   if (guard.err != cudaSuccess) return fail(PDA_ECUDA, "cudaSetDevice failed");
   const dim3 grid((unsigned)((max_len + block_size - 1) / block_size), (unsigned)batch, 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (out_dtype == PDA_BF16) pda::gather_fp8_kernel<pda::Bf16><<<grid, pda::kGatherThreads, 0, s>>>(p);
-  else if (out_dtype == PDA_FP16) pda::gather_fp8_kernel<pda::Fp16><<<grid, pda::kGatherThreads, 0, s>>>(p);
-  else pda::gather_fp8_kernel<float><<<grid, pda::kGatherThreads, 0, s>>>(p);
+  auto launch = [&](auto t) {
+    using T = decltype(t);
+    if (head_dim == 64) pda::gather_fp8_kernel<T, 64><<<grid, pda::kGatherThreads, 0, s>>>(p);
+    else pda::gather_fp8_kernel<T, 128><<<grid, pda::kGatherThreads, 0, s>>>(p);
+  };
+  if (out_dtype == PDA_BF16) launch(pda::Bf16());
+  else if (out_dtype == PDA_FP16) launch(pda::Fp16());
+  else launch(float());
   return pda::launched("gather launch");
 }

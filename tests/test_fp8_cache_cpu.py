@@ -126,6 +126,7 @@ def gather_args(**kw):
     (dict(lens=None), pda.PDA_EINVAL), (dict(vo=9 * A + 8), pda.PDA_EINVAL), (dict(cu=7 * A + 4), pda.PDA_EINVAL),
     (dict(vo=8 * A), pda.PDA_EALIAS), (dict(ko=A), pda.PDA_EALIAS), (dict(ko=5 * A), pda.PDA_EALIAS),
     (dict(dev=-1), pda.PDA_EINVAL), (dict(B=0), pda.PDA_OK), (dict(maxlen=0), pda.PDA_OK),
+    (dict(Hkv=8192), pda.PDA_EUNSUPPORTED), (dict(Hkv=0), pda.PDA_EINVAL), (dict(nb=0), pda.PDA_EINVAL),
 ])
 def test_gather_refusals_before_cuda(lib, kw, status):
     assert lib.paged_decode_attn_gather_kv_fp8(*gather_args(**kw)) == status

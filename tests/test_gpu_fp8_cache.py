@@ -165,6 +165,38 @@ def test_append_special_values(dt):
     cache.check(dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_append_every_scale_exponent(dt):
+    """One block per power of two between the type's extremes: scales from the smallest (2^-60, or
+    what the type's subnormals ask for) to the largest, behind old scales that are larger too."""
+    gen = torch.Generator().manual_seed(13)
+    Hkv, D, bs = 1, 64, 16
+    lo, hi = (-133, 127) if dt == "bf16" else (-24, 15)
+    exps = list(range(lo, hi + 1))
+    B = len(exps)
+    unit = torch.rand(B, bs, 2 * Hkv, D, generator=gen, dtype=torch.float64) * 2 - 1
+    # every block spans its scale's whole range down to far below E4M3's smallest step
+    small = torch.exp2(-torch.randint(0, 24, unit.shape, generator=gen).double())
+    x = (unit * small * torch.exp2(torch.tensor(exps).double())[:, None, None, None]).to(DT[dt])
+    x = x.reshape(B * bs, 2 * Hkv, D)
+    cache = Cache(11, B, bs, Hkv, D)
+    table = np.arange(B, dtype=np.int32)[:, None]
+    lens, cu = np.full(B, bs), bs * np.arange(B + 1)
+    def both(rows, lens, cu):
+        ref.append(rows[:, :Hkv].double().numpy(), cache.k, cache.ks, table, lens, cu)
+        ref.append(rows[:, Hkv:].double().numpy(), cache.v, cache.vs, table, lens, cu)
+        d = rows.to(DEV)
+        append_kv_fp8(d[:, :Hkv], d[:, Hkv:], *cache.dev, dev(table), dev(lens, torch.int32),
+                      dev(cu, torch.int64))
+        cache.check(f"{dt} {lens[0]}")
+
+    both(x, lens, cu)
+    # a second token behind a first one whose scale is 2^7 times larger
+    first = x.reshape(B, bs, 2 * Hkv, D)[:, 0].double() * 128
+    both(first.clamp(-torch.finfo(DT[dt]).max, torch.finfo(DT[dt]).max).to(DT[dt]), np.full(B, 1), np.arange(B + 1))
+    both(x.reshape(B, bs, 2 * Hkv, D)[:, 1].contiguous(), np.full(B, 2), np.arange(B + 1))
+
+
 def test_append_behind_foreign_scales():
     """Blocks written by another quantiser: scales that are no powers of two, zero, negative, NaN,
     infinite, subnormal."""
