@@ -33,6 +33,7 @@
 
 #include "paged_decode_attn.h"
 #include "pda_internal.h"
+#include "ptx.cuh"
 #include "rope_math.cuh"
 #include "row_sets.h"
 
@@ -277,6 +278,8 @@ enum Rope { kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2 };
 // one q row per warp.
 template <typename F, int D, int NV, int W, int kRope>
 __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) append_kernel(const AppendParams p) {
+  griddep_launch_dependents();  // the next grid may be set up; it waits for this one's end
+  griddep_wait();
   // A lane's two vectors of a row are the A and B of one rotation item (8 pairs), or
   // any two where nothing rotates; kItems lanes cover a row.
   constexpr int kItems = D / 16;
@@ -519,6 +522,8 @@ constexpr int kGatherVec = 4;  // vectors in flight per thread
 template <typename T, int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_fp8_kernel(const GatherParams p) {
   constexpr int E = Pack<T>::n;  // elements of an output vector
+  griddep_launch_dependents();
+  griddep_wait();
   const int b = blockIdx.y, page = blockIdx.x;
   int L = __ldg(p.lens + b);
   if (L > p.max_len || L < 0) {
@@ -595,8 +600,7 @@ struct Dev {
   }
 };
 
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+int launched(const char* what, cudaError_t e) {
   if (e != cudaSuccess) return fail(PDA_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
   return PDA_OK;
 }
@@ -618,27 +622,44 @@ int check_cache(int num_kv_heads, int head_dim, int block_size, int64_t num_bloc
   return PDA_OK;
 }
 
+// Launches with programmatic dependent launch, as the decode kernels: set-up overlaps
+// the end of the previous grid in the stream (off with PDA_PDL=0).
+template <typename P>
+cudaError_t launch(void (*kernel)(const P), dim3 grid, int threads, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <typename F, int D, int NV, int W>
-void launch_append(const AppendParams& p, int rope, unsigned grid, cudaStream_t s) {
-  if (rope == kRopeNone) append_kernel<F, D, NV, W, kRopeNone><<<grid, kAppendThreads, 0, s>>>(p);
-  else if (rope == kRopeHalves) append_kernel<F, D, NV, W, kRopeHalves><<<grid, kAppendThreads, 0, s>>>(p);
-  else append_kernel<F, D, NV, W, kRopePairs><<<grid, kAppendThreads, 0, s>>>(p);
+cudaError_t launch_append(const AppendParams& p, int rope, unsigned grid, cudaStream_t s) {
+  return launch(rope == kRopeNone     ? append_kernel<F, D, NV, W, kRopeNone>
+                : rope == kRopeHalves ? append_kernel<F, D, NV, W, kRopeHalves>
+                                      : append_kernel<F, D, NV, W, kRopePairs>,
+                dim3(grid), kAppendThreads, s, p);
 }
 
 template <typename F>
-void launch_append_geometry(const AppendParams& p, int D, int rope, unsigned grid, cudaStream_t s) {
+cudaError_t launch_append_geometry(const AppendParams& p, int D, int rope, unsigned grid,
+                                   cudaStream_t s) {
   // NV * W * 32 = block_size * D / 8 vectors of a tile: at most 8 a lane, so that
   // four CTAs fit an SM and their chains of loads overlap
   const int tile = p.block_size * D;
   if (D == 64) {
-    if (tile == 1024) launch_append<F, 64, 4, 1>(p, rope, grid, s);
-    else if (tile == 2048) launch_append<F, 64, 8, 1>(p, rope, grid, s);
-    else launch_append<F, 64, 8, 2>(p, rope, grid, s);
-  } else {
-    if (tile == 2048) launch_append<F, 128, 8, 1>(p, rope, grid, s);
-    else if (tile == 4096) launch_append<F, 128, 8, 2>(p, rope, grid, s);
-    else launch_append<F, 128, 8, 4>(p, rope, grid, s);
+    if (tile == 1024) return launch_append<F, 64, 4, 1>(p, rope, grid, s);
+    if (tile == 2048) return launch_append<F, 64, 8, 1>(p, rope, grid, s);
+    return launch_append<F, 64, 8, 2>(p, rope, grid, s);
   }
+  if (tile == 2048) return launch_append<F, 128, 8, 1>(p, rope, grid, s);
+  if (tile == 4096) return launch_append<F, 128, 8, 2>(p, rope, grid, s);
+  return launch_append<F, 128, 8, 4>(p, rope, grid, s);
 }
 
 // Both append entry points; rope == kRopeNone: no q, no positions.
@@ -711,9 +732,9 @@ int append_impl(AppendParams p, int D, int dtype, int rope, int device, void* st
   Dev guard(device);
   if (guard.err != cudaSuccess) return fail(PDA_ECUDA, "cudaSetDevice failed");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == PDA_BF16) launch_append_geometry<Bf16>(p, D, rope, (unsigned)grid, s);
-  else launch_append_geometry<Fp16>(p, D, rope, (unsigned)grid, s);
-  return launched("append launch");
+  return launched("append launch",
+                  dtype == PDA_BF16 ? launch_append_geometry<Bf16>(p, D, rope, (unsigned)grid, s)
+                                    : launch_append_geometry<Fp16>(p, D, rope, (unsigned)grid, s));
 }
 
 }  // namespace
@@ -852,13 +873,12 @@ extern "C" int paged_decode_attn_gather_kv_fp8(
   if (guard.err != cudaSuccess) return fail(PDA_ECUDA, "cudaSetDevice failed");
   const dim3 grid((unsigned)((max_len + block_size - 1) / block_size), (unsigned)batch, 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto launch = [&](auto t) {
+  auto gather = [&](auto t) {
     using T = decltype(t);
-    if (head_dim == 64) pda::gather_fp8_kernel<T, 64><<<grid, pda::kGatherThreads, 0, s>>>(p);
-    else pda::gather_fp8_kernel<T, 128><<<grid, pda::kGatherThreads, 0, s>>>(p);
+    return pda::launch(head_dim == 64 ? pda::gather_fp8_kernel<T, 64> : pda::gather_fp8_kernel<T, 128>,
+                       grid, pda::kGatherThreads, s, p);
   };
-  if (out_dtype == PDA_BF16) launch(pda::Bf16());
-  else if (out_dtype == PDA_FP16) launch(pda::Fp16());
-  else launch(float());
-  return pda::launched("gather launch");
+  return pda::launched("gather launch", out_dtype == PDA_BF16   ? gather(pda::Bf16())
+                                        : out_dtype == PDA_FP16 ? gather(pda::Fp16())
+                                                                : gather(float()));
 }
