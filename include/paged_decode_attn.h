@@ -358,7 +358,9 @@ int paged_decode_attn_remap_table(int32_t* block_table, int batch, int max_block
  * positive and finite counts as 0, and the values as zeros). So the blocks
  * that a call writes must belong to one sequence each: copy a block shared
  * with another sequence (paged_decode_attn_copy_blocks, and its scales)
- * before appending to it.
+ * before appending to it. (Scale rows of Hkv * 4 bytes can be copied by
+ * paged_decode_attn_copy_blocks as blocks of their own when Hkv is a multiple
+ * of 4.)
  *
  * head_dim 64 or 128, block_size 16, 32 or 64. Pointers and strides 16-byte
  * aligned (index arrays and scales: their element size). `err` (optional
@@ -412,7 +414,10 @@ int paged_decode_attn_gather_kv_fp8(const void* k_cache, const void* v_cache,
  * blk = block_table[b, t / block_size]. k_scale and v_scale are [num_blocks,
  * Hkv] fp32, finite and >= 0, whatever wrote them (powers of two or not); a
  * block id outside [0, num_blocks) reads zeros. The largest and the smallest
- * nonzero V scale that a sequence uses may lie a factor of 2^100 apart. */
+ * nonzero V scale that a sequence uses may lie a factor of 2^100 apart.
+ * num_splits 0: a rule of this call's own (a batch's lengths may be spread out,
+ * chunks of 128 tokens are whole); paged_decode_attn_plan and
+ * paged_decode_attn_launch_shape describe the other run calls. */
 int paged_decode_attn_run_block_scaled(pda_handle handle, const void* q, const void* k_cache,
                                        const void* v_cache, const float* k_scale,
                                        const float* v_scale, const int32_t* block_table,

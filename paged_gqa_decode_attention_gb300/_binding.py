@@ -373,6 +373,8 @@ def _token_rows(t: torch.Tensor, name: str, dtype) -> tuple[int, int]:
     T, H, D = t.shape
     if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{name}: heads must be contiguous within a token")
+    if T > 1 and t.stride(0) < H * D:
+        raise ValueError(f"{name}: tokens must not overlap (a broadcast view)")
     return t.data_ptr(), (t.stride(0) if T > 1 else H * D)
 
 
@@ -548,6 +550,8 @@ def _rows16(name: str, t: torch.Tensor, device: int, dtype) -> tuple[int, int]:
     s0, s1, s2 = t.stride()
     if s2 != 1 or (H > 1 and s1 != D):
         raise ValueError(f"{name}: heads must be contiguous within a token")
+    if T > 1 and s0 < H * D:
+        raise ValueError(f"{name}: tokens must not overlap (a broadcast view)")
     return t.data_ptr(), (s0 if T > 1 else H * D)
 
 

@@ -258,6 +258,23 @@ def test_captured_and_replayed_with_a_cache_that_moves_on():
             check(out, p.want(), f"replay {step}")
 
 
+def test_two_handles_on_two_streams_and_an_empty_batch():
+    ps = [Problem(18 + i, 4, 2, 128, 16, [900 + i, 33, 400], "bf16").upload() for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    attns = [p.attn() for p in ps]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs = [a.run(*p.dev, **p.scales, stream=s) for a, p, s in zip(attns, ps, streams)]
+    torch.cuda.synchronize()
+    for p, out in zip(ps, outs):
+        check(out, p.want())
+    q, kc, vc, table, lens, scale = ps[0].dev
+    assert attns[0].run(q[:0], kc, vc, table[:0], lens[:0], scale, **ps[0].scales).shape == (0, 8, 128)
+    for a in attns:
+        a.close()
+
+
 def test_timed_out_wait_is_reported_and_the_next_run_is_exact(monkeypatch):
     monkeypatch.setenv("PDA_TEST_STALL_RUNS", "1")
     p = Problem(14, 4, 2, 128, 16, [700, 90], "bf16").upload()

@@ -456,6 +456,53 @@ def test_gather_into_given_rows():
 
 # ------------------------------------ as used ------------------------------------
 
+def test_nothing_to_do_and_broadcast_rows():
+    """No sequences, no rows, sequences without new rows: the cache stays as it is. Rows that
+    overlap (a broadcast view) are refused."""
+    cache = Cache(14, 6, 16, 2, 64)
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    one = torch.ones(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    i64 = lambda *x: torch.tensor(x, dtype=torch.int64, device=DEV)
+    none = torch.zeros(0, 2, dtype=torch.int32, device=DEV)
+    append_kv_fp8(k, k, *cache.dev, none, i32()[:0], i64(0))
+    append_kv_fp8(one, one, *cache.dev, none, i32()[:0], i64(0))
+    append_kv_fp8(k, k, *cache.dev, i32(0, 1).view(2, 1), i32(7, 16), i64(0, 0, 0))
+    append_kv_fp8(one, one, *cache.dev, i32(0, 1).view(2, 1), i32(7, 16), i64(0, 0, 0))
+    append_kv_fp8(one, one, *cache.dev, i32(0, 1).view(2, 1), i32(7, 16), i64(1, 1, 1))
+    cache.check()
+    got = gather_kv_fp8(*cache.dev, none, i32()[:0])
+    assert got[0].shape == (0, 2, 64)
+    got = gather_kv_fp8(*cache.dev, i32(0, 1).view(2, 1), i32(0, 0))
+    assert got[0].shape == (0, 2, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        append_kv_fp8(one.expand(3, 2, 64), one.expand(3, 2, 64), *cache.dev, i32(0).view(1, 1), i32(3), i64(0, 3))
+    with pytest.raises(ValueError):
+        append_kv_fp8(one.transpose(1, 2), one.transpose(1, 2), *cache.dev, i32(0).view(1, 1), i32(1), i64(0, 1))
+    cache.check()
+
+
+def test_two_streams_append_to_their_own_sequences():
+    """Calls on two streams at once, each for sequences of its own, in one cache."""
+    gen = torch.Generator().manual_seed(15)
+    Hkv, D, bs, n = 8, 128, 16, 2000
+    cache = Cache(15, 2 * 125 + 1, bs, Hkv, D)
+    order = np.random.default_rng(15).permutation(250).astype(np.int32)
+    x = rows_of(gen, 2 * n, 2 * Hkv, D, "bf16")
+    parts = []
+    for i in range(2):
+        rows, table = x[i * n:(i + 1) * n], order[i * 125:(i + 1) * 125][None]
+        ref.append(rows[:, :Hkv].double().numpy(), cache.k, cache.ks, table, [n], [0, n])
+        ref.append(rows[:, Hkv:].double().numpy(), cache.v, cache.vs, table, [n], [0, n])
+        parts.append((rows.to(DEV), dev(table), dev(np.array([n]), torch.int32), dev(np.array([0, n]), torch.int64)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):  # the same rows again: blocks that start anew hold the same
+        for (rows, table, lens, cu), s in zip(parts, streams):
+            append_kv_fp8(rows[:, :Hkv], rows[:, Hkv:], *cache.dev, table, lens, cu, stream=s)
+    cache.check()
+
+
 def test_calls_are_captured_and_replayed_on_another_stream():
     """A decode step's append in a CUDA graph on a side stream: every replay appends the next
     token from the tensors it was captured with."""
