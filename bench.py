@@ -49,13 +49,13 @@ NOMINAL_HBM_GBS = 8000.0  # GB300 HBM3e, nominal (~8 TB/s)
 _CSRC = os.path.join(ROOT, "paged_gqa_decode_attention_gb300", "csrc")
 TC_KERNEL_SOURCES = ("partial_tc_kernel.cuh", "ptx.cuh", "split_merge.cuh", "pda_internal.h",
                      "partial_tc_bf16_d128.cu", "partial_launch.cu")
-ROPE_KERNEL_SOURCES = ("rope_kv_write.cu", "ptx.cuh", "pda_internal.h")
+ROPE_KERNEL_SOURCES = ("rope_kv_write.cu", "rope_math.cuh", "ptx.cuh", "pda_internal.h")
 NCU_TRAFFIC = {
     # workload: (bytes per launch, kernel sources, their SHA-256 at capture)
-    "long_b4_l32768": (540_981_760, TC_KERNEL_SOURCES,
-                       "9d54b0a72658dbd1b0ed990de896a3e78228f88ebff1598f7b029366fd744473"),
-    "rope_prefill_t32768": (768_234_496, ROPE_KERNEL_SOURCES,
-                            "fa980a506c38f4a633447bab730832813569500c8a40c5ee3795b4ff6925ceb9"),
+    "long_b4_l32768": (540_340_480, TC_KERNEL_SOURCES,
+                       "60448575f5577a694659d0f55a1993256b433be3e7512a5ab6693fcc0bba9b8c"),
+    "rope_prefill_t32768": (768_333_312, ROPE_KERNEL_SOURCES,
+                            "6a2054a4bd717ffb53685e1958f28f2c3092a8b29e38ee2358654ebfefccbf74"),
 }
 
 

@@ -18,9 +18,15 @@
 // tile of one (block, K or V, head): nothing is exchanged between blocks of
 // threads, no atomics, the result does not depend on any order.
 //
-// Bound by memory traffic: a row costs 2 bytes read and 1 written per value.
-// A tile's rows are held in registers between the maximum and the rounding
-// (NV 16-byte vectors a lane), so each is read once.
+// Bound by memory traffic: a row costs 2 bytes read and 1 written per value. A
+// tile's rows are held in registers between the maximum and the rounding (NV
+// 16-byte vectors a lane, at most 8: with 16 only two CTAs fit an SM and their
+// chains of loads did not overlap, 51 us against 40), so each is read once.
+// Measured on GB300 (back to back, copy rate 6784.5 GB/s): 41984 fp16 rows of 8
+// heads, D 128, blocks of 32: 40.0 us, 6450 GB/s; 256 single bf16 tokens 4.2 us.
+// With rotation the exact rounding's instructions bound it: 21631 bf16 rows at
+// 32/8 heads 99.6 us, 4940 GB/s (57% of issue slots, no row read twice).
+// Read-back of 24058 tokens to bf16: 24.8 us, 5950 GB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

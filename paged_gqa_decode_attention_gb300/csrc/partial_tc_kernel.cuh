@@ -75,6 +75,15 @@
 //     normalises it, stores the output or the split partial, and runs the
 //     split ticket and merge, while the softmax warps go on with the next
 //     unit (the unit boundary does not stall the pipeline).
+// Block-scaled FP8 K/V (BSC; k_scale and v_scale per block and kv head) differ in
+// this: the K producer requests the scales of each chunk's pages, a scale warp
+// (G <= 4; else the QK^T warp) makes of them what the softmax applies per token
+// (chunk_scales) and, at G <= 4, the fp8 q terms; the V scale is part of the
+// weights; fp16 queries take three fp8 terms; the next unit is claimed while the
+// current one runs, and units beyond one a CTA are taken longest sequence first.
+// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 54.6 us (0.73
+// of the 269 MB's time at the copy rate), 128 x 32-4096 at 64/8 heads 68.6 us (0.53),
+// 8 x 32768 at 32/8 heads 94.9 us (0.84), 128/8 heads 8 x 16384 84.8 us.
 // Every wait is bounded; a timed-out CTA records error code 3, stops issuing
 // work, still passes every barrier, counts itself done with the work counter
 // (so the counters are reset for the next call) and frees its TMEM.
