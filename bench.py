@@ -52,10 +52,10 @@ TC_KERNEL_SOURCES = ("partial_tc_kernel.cuh", "ptx.cuh", "split_merge.cuh", "pda
 ROPE_KERNEL_SOURCES = ("rope_kv_write.cu", "rope_math.cuh", "ptx.cuh", "pda_internal.h")
 NCU_TRAFFIC = {
     # workload: (bytes per launch, kernel sources, their SHA-256 at capture)
-    "long_b4_l32768": (540_340_480, TC_KERNEL_SOURCES,
-                       "60448575f5577a694659d0f55a1993256b433be3e7512a5ab6693fcc0bba9b8c"),
-    "rope_prefill_t32768": (768_333_312, ROPE_KERNEL_SOURCES,
-                            "6a2054a4bd717ffb53685e1958f28f2c3092a8b29e38ee2358654ebfefccbf74"),
+    "long_b4_l32768": (540_070_400, TC_KERNEL_SOURCES,
+                       "ce16d04ed3e6246ab278183dac82db6dfb857c072c7bc3441c384a2be8683b3b"),
+    "rope_prefill_t32768": (768_278_272, ROPE_KERNEL_SOURCES,
+                            "4fbbc0ed42893172acf68d4475cc7222f44220320fb80eb911cd4f91664f68e1"),
 }
 
 

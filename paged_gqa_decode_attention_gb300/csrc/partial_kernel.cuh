@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, partial_ctas_per_sm_hint(kPartialCud
     for (int c = 0; c < n_chunks; ++c) {
       const int slot = c % kStages;
       if (c >= kStages) {
-        const bool ok = mbar_wait(empty_bar(slot), ((c / kStages) - 1) & 1);
+        const bool ok = mbar_wait_inline(empty_bar(slot), ((c / kStages) - 1) & 1);
         if (!__all_sync(kFull, ok)) {
           failed = true;
           break;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, partial_ctas_per_sm_hint(kPartialCud
 
     for (int c = 0; c < n_chunks; ++c) {
       const int slot = c % kStages;
-      const bool ok = mbar_wait(full_bar(slot), (c / kStages) & 1);
+      const bool ok = mbar_wait_inline(full_bar(slot), (c / kStages) & 1);
       if (!__all_sync(kFull, ok)) {
         failed = true;
         break;

@@ -81,9 +81,9 @@
 // (chunk_scales) and, at G <= 4, the fp8 q terms; the V scale is part of the
 // weights; fp16 queries take three fp8 terms; the next unit is claimed while the
 // current one runs, and units beyond one a CTA are taken longest sequence first.
-// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 54.6 us (0.73
-// of the 269 MB's time at the copy rate), 128 x 32-4096 at 64/8 heads 68.6 us (0.53),
-// 8 x 32768 at 32/8 heads 94.9 us (0.84), 128/8 heads 8 x 16384 84.8 us.
+// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 54.7 us (0.73
+// of the 269 MB's time at the copy rate), 128 x 32-4096 at 64/8 heads 64.8 us (0.57),
+// 8 x 32768 at 32/8 heads 93.9 us (0.84), 128/8 heads 8 x 16384 79.5 us.
 // Every wait is bounded; a timed-out CTA records error code 3, stops issuing
 // work, still passes every barrier, counts itself done with the work counter
 // (so the counters are reset for the next call) and frees its TMEM.
@@ -892,10 +892,11 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
     uint8_t* q8 = base + kOffQ8 + qb * L::kQ8Bytes;
     float* qs = reinterpret_cast<float*>(base + kOffQs) + qb * kGE;
     const int d0 = 4 * lane;  // lanes past D read the tile's zero half
-    // in passes over four rows: their loads, maxima and conversions overlap, which a
-    // row's stores between them would forbid
-    constexpr int kRows = 4;
-#pragma unroll
+    // in passes over two rows, whose loads, maxima and conversions overlap; a loop,
+    // since this code runs once a unit and its size counts (64/8 heads, 128 sequences:
+    // four rows unrolled 68.7 us, this 66.1)
+    constexpr int kRows = 2;
+#pragma unroll 1
     for (int g1 = 0; g1 < G; g1 += kRows) {
       float x[kRows][4];
       uint32_t mx[kRows];
