@@ -366,7 +366,8 @@ int paged_decode_attn_remap_table(int32_t* block_table, int batch, int max_block
  * aligned (index arrays and scales: their element size). `err` (optional
  * device int[2]) receives the first problem found: code 1 (cu_rows not
  * ascending within num_rows, or a context length below n_b or above
- * max_blocks * block_size; the sequence is skipped) or 2 (a block id outside
+ * max_blocks * block_size or 2^31 - 1 - block_size; the sequence is not
+ * appended) or 2 (a block id outside
  * [0, num_blocks); the block is skipped), and the sequence. Outputs must not
  * overlap inputs or each other (PDA_EALIAS). Asynchronous on `stream`;
  * allocates nothing; graph-capturable. */
@@ -383,7 +384,8 @@ int paged_decode_attn_append_kv_fp8(const void* k, int64_t k_token_stride, const
  * rot_dim, neox_style; exactly rounded to dtype), the rotated q rows go to
  * q_out (q_out == q with equal strides rotates in place) and the rotated k
  * rows, as dtype values, and the v rows are quantised and appended as above.
- * Rows that belong to no sequence are neither read nor written. A row with a
+ * Rows before cu_rows[0] or from cu_rows[batch] on are neither read nor
+ * written (the q rows of a sequence that is not appended are rotated). A row with a
  * position outside [0, max_position) writes nothing (code 4 and the row). */
 int paged_decode_attn_rope_append_kv_fp8(
     const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,

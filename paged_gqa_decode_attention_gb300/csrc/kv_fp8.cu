@@ -283,7 +283,8 @@ enum Rope { kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2 };
 // CTAs below p.kv_ctas: a unit's tiles, W warps per tile; the others (rope):
 // one q row per warp.
 template <typename F, int D, int NV, int W, int kRope>
-__global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3)
+    append_kernel(const AppendParams p) {
   griddep_launch_dependents();  // the next grid may be set up; it waits for this one's end
   griddep_wait();
   // A lane's two vectors of a row are the A and B of one rotation item (8 pairs), or
@@ -350,7 +351,8 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3) ap
   const int64_t base = block_index<BS>(r_lo) + b, slots = block_index<BS>(r_hi) + b + 1 - base;
   const int64_t j = u - base;
   if (n == 0 || j >= slots) return;
-  if (r_lo < 0 || n < 0 || r_hi > p.T || n > len || (int64_t)len > (int64_t)p.max_blocks * bs) {
+  if (r_lo < 0 || n < 0 || r_hi > p.T || n > len || len > INT_MAX - bs ||
+      (int64_t)len > (int64_t)p.max_blocks * bs) {
     if (threadIdx.x == 0) record(p.err, kErrContextLen, b);
     return;
   }

@@ -81,9 +81,9 @@
 // (chunk_scales) and, at G <= 4, the fp8 q terms; the V scale is part of the
 // weights; fp16 queries take three fp8 terms; the next unit is claimed while the
 // current one runs, and units beyond one a CTA are taken longest sequence first.
-// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 54.7 us (0.73
-// of the 269 MB's time at the copy rate), 128 x 32-4096 at 64/8 heads 64.8 us (0.57),
-// 8 x 32768 at 32/8 heads 93.9 us (0.84), 128/8 heads 8 x 16384 79.5 us.
+// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 52.9 us (0.75
+// of the 269 MB's time at the copy rate), 128 x 32-4096 at 64/8 heads 63.8 us (0.57),
+// 8 x 32768 at 32/8 heads 90.7 us (0.87), 128/8 heads 8 x 16384 80 us.
 // Every wait is bounded; a timed-out CTA records error code 3, stops issuing
 // work, still passes every barrier, counts itself done with the work counter
 // (so the counters are reset for the next call) and frees its TMEM.
@@ -180,7 +180,6 @@ constexpr float kMinBlockScale = 0x1p-60f;
 // that every CTA builds of a batch of up to kDirMax sequences.
 constexpr int kDirMax = 1024;
 constexpr int kDirBuckets = 64;
-constexpr int kResolveChunk = 3;  // chunk of a unit at which the next one is looked up
 // fp8 terms of Q: two hold a bf16 exactly; the block-scaled kernel takes three
 // for fp16.
 __host__ __device__ constexpr int q_terms(bool fp16, bool bsc) { return fp16 && bsc ? 3 : 2; }
@@ -407,8 +406,9 @@ __device__ __forceinline__ int length_bucket(int n_chunks) {
 // first, ascending inside a bucket. Every CTA computes the same
 // order (a counting sort in a fixed sequence of steps, no atomics), so that a
 // position in it means the same unit to all.
+// A call: it runs once, and its code inlined would only crowd the loops.
 template <int BS>
-__device__ __forceinline__ void build_directory(const PartialParams& p, int b0, int B,
+__device__ __noinline__ void build_directory(const PartialParams& p, int b0, int B,
                                                 volatile uint16_t* order, volatile int* hist,
                                                 int lane) {
   for (int i = lane; i < kDirBuckets; i += 32) hist[i] = 0;
@@ -616,75 +616,58 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
     bool counted;
     bool first;  // the next unit is this CTA's static first unit
     // BSC: the next unit is claimed from the counter when the current one
-    // starts, and decoded, published and its first table window requested a
-    // few chunks later, so that a unit boundary waits for none of these.
+    // starts, so that a unit boundary does not wait for the counter. (Looking it
+    // up and requesting its table window early as well measured 1% slower.)
     uint32_t dir_bar = 0;
     const volatile uint16_t* dir_order = nullptr;  // null: no directory
     int dir_first = 0, per_seq = 1;          // first unit in directory order; units a sequence
-    int pend = 0, r_u = -1, win = 0, nxt = 0;
-    Unit r_U;
-    bool claimed = false, resolved = false, ended = false;
+    int pend = 0, win = 0, nxt = 0;
+    bool claimed = false;
     __device__ __forceinline__ void claim() {
-      if (claimed || ended) return;
+      if (claimed) return;
       claimed = true;
-      // (pend is not touched until resolve(): the warp does not wait for the counter here)
+      // (pend is not touched until next_claimed(): the warp does not wait for it here)
       if (p->num_units > (int)gridDim.x && lane == 0) pend = atomicAdd(p->sched, 1);
     }
     // The claimed unit (or the first one after it with chunks to work on), published;
-    // its first table window is requested.
-    __device__ __forceinline__ void resolve() {
-      if (resolved || ended) return;
-      claim();
-      resolved = true;
+    // its first table window is requested. -1 at the end.
+    __device__ __forceinline__ int next_claimed(Unit& U) {
       while (true) {
+        claim();
         int u = p->num_units;
         if (u > (int)gridDim.x) u = (int)gridDim.x + __shfl_sync(kFull, pend, 0);
         claimed = false;
-        int pub = -1;
-        if (u < p->num_units) {
-          bool ok = true;
-          if (dir_order != nullptr) ok = mbar_wait(dir_bar, 0, wlim);
-          if (!__all_sync(kFull, ok)) {
-            *failed = true;
-            ended = true;
-            r_u = -1;
-            done();
-            return;
-          }
-          if (dir_order != nullptr && u >= dir_first) {
-            const int v = u - dir_first, i = v / per_seq;
-            u = dir_order[i] * per_seq + (v - i * per_seq);
-          }
-          r_U = load_unit<BS>(*p, u);
-          if (!unit_has_work(r_U)) {
-            claim();
-            continue;
-          }
-          pub = u;
-          if (r_U.n_chunks == 0) {
-            // an empty context: zeros, written here and not passed on. The current
-            // unit's pages may not all be requested yet, so at most one entry of the
-            // ring may be taken ahead of it (its slot was read, or will be, by roles
-            // that need no page still to be requested).
-            const int64_t row = (int64_t)r_U.b * p->Hq + r_U.h * G;
-            for (int i = lane; i < G * D; i += 32) {
-              if (p->out_f32) static_cast<float*>(p->out)[row * D + i] = 0.f;
-              else static_cast<TNat*>(p->out)[row * D + i] = to_out<TNat>(0.f);
-            }
-            claim();
-            continue;
-          }
-        }
-        r_u = publish(pub, r_U) ? pub : -1;
-        if (r_u < 0) {
-          ended = true;
+        if (u >= p->num_units) {
+          publish(-1, U);
           done();
-        } else {
-          const int32_t* table = p->block_table + (int64_t)r_U.b * p->max_blocks + r_U.p0;
-          win = r_U.p0 + lane < r_U.p1 ? __ldg(table + lane) : 0;
-          nxt = r_U.p0 + 32 + lane < r_U.p1 ? __ldg(table + 32 + lane) : 0;
+          return -1;
         }
-        return;
+        bool ok = true;
+        if (dir_order != nullptr) ok = mbar_wait(dir_bar, 0, wlim);
+        if (!__all_sync(kFull, ok)) {
+          *failed = true;
+          done();
+          return -1;
+        }
+        if (dir_order != nullptr && u >= dir_first) {
+          const int v = u - dir_first, i = v / per_seq;
+          u = dir_order[i] * per_seq + (v - i * per_seq);
+        }
+        U = load_unit<BS>(*p, u);
+        if (!unit_has_work(U)) continue;
+        if (U.n_chunks == 0) {  // an empty context: zeros, written here and not passed on
+          const int64_t row = (int64_t)U.b * p->Hq + U.h * G;
+          for (int i = lane; i < G * D; i += 32) {
+            if (p->out_f32) static_cast<float*>(p->out)[row * D + i] = 0.f;
+            else static_cast<TNat*>(p->out)[row * D + i] = to_out<TNat>(0.f);
+          }
+          continue;
+        }
+        if (!publish(u, U)) return -1;
+        const int32_t* table = p->block_table + (int64_t)U.b * p->max_blocks + U.p0;
+        win = U.p0 + lane < U.p1 ? __ldg(table + lane) : 0;
+        nxt = U.p0 + 32 + lane < U.p1 ? __ldg(table + 32 + lane) : 0;
+        return u;
       }
     }
     // Unit `pub` (-1: the end) into the ring; false after a timed-out wait.
@@ -732,10 +715,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
         if (unit_has_work(U)) return (int)blockIdx.x;
       }
       if constexpr (BSC) {
-        resolve();
-        resolved = false;
-        U = r_U;
-        return r_u;
+        return next_claimed(U);
       } else {
         while (true) {
           int u = 0;
@@ -1089,7 +1069,6 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
         if (BSC && r == 0) load_scales(c, npg, bl, U.h);
       }
       __syncwarp();
-      if (BSC && r == 0 && cu_i == min(kResolveChunk, U.n_chunks - 1)) fetch.resolve();
       if (r == 0) cur_k.advance(p, fetch); else cur_v.advance(p, ring);
     }
     if constexpr (BSC) cp_async_wait_all();  // none in flight at exit, whatever failed
@@ -1202,7 +1181,6 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
         }
         __syncwarp();
       }
-      if (BSC && fetcher && cu_i == min(kResolveChunk, U.n_chunks - 1)) fetch.resolve();
       if (fetcher) cur_k.advance(p, fetch); else cur_v.advance(p, ring);
     }
     if constexpr (BSC) cp_async_wait_all();  // none in flight at exit, whatever failed
