@@ -9,7 +9,7 @@ import torch
 import fp8_cache_ref as ref
 import oracle
 from paged_gqa_decode_attention_gb300 import (append_kv_fp8, copy_blocks, gather_kv_fp8,
-                                              rope_append_kv_fp8, workloads)
+                                              rope_append_kv_fp8, rope_kv_write, workloads)
 
 pytestmark = pytest.mark.gpu
 
@@ -479,6 +479,10 @@ def test_nothing_to_do_and_broadcast_rows():
         append_kv_fp8(one.expand(3, 2, 64), one.expand(3, 2, 64), *cache.dev, i32(0).view(1, 1), i32(3), i64(0, 3))
     with pytest.raises(ValueError):
         append_kv_fp8(one.transpose(1, 2), one.transpose(1, 2), *cache.dev, i32(0).view(1, 1), i32(1), i64(0, 1))
+    wide = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        rope_kv_write(one.expand(3, 2, 64), one.expand(3, 2, 64), one.expand(3, 2, 64), i32(0, 1, 2), i64(0, 1, 2),
+                      torch.zeros(4, 64, device=DEV), wide, wide.clone())
     cache.check()
 
 
