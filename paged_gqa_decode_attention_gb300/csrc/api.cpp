@@ -150,19 +150,19 @@ void plan_splits(const pda_config& c, int kernel, int num_sms, int ctas_per_sm, 
 
 // The split count of a block-scaled FP8 call, whose kernel takes the units beyond
 // one a CTA longest sequence first. In token-equivalents of one CTA's time: a unit
-// costs its tokens in whole 128-token chunks plus 512, a merged split 32, a split
+// costs its tokens in whole 128-token chunks plus 256, a merged split 32, a split
 // that a shorter sequence does not have (the counter still visits it) 240. The
 // host knows the longest context only, so a batch is weighed twice: as if
 // every sequence had it, and as if the lengths were spread out (a quarter of it on
 // average), where many splits keep one long sequence from setting the time.
 // Measured on GB300 (sweeps of S), the pick against the 16-bit rule's pick and the
 // best: 64 sequences of 100 to 16384 tokens at 14/2 heads, D 64, S = 7 41 us (S = 1 95,
-// S = 8 40), 13 of 1 to 9001 at 28/4 heads S = 5 23.6 (S = 7 21.0), one of 777 at 14/2
+// S = 8 40), 13 of 1 to 9001 at 28/4 heads S = 5 23.1 (S = 7 21.0), one of 777 at 14/2
 // heads S = 7 10.1 (S = 49 15.6), 4 x 32768 at 32/8 heads S = 9 54 (S = 4 51), 8 x 32768
 // S = 7 92 (the best), 128 of 32 to 4096 at 64/8 heads S = 1 64 (the best; S = 2 69).
 void plan_block_scaled(const pda_config& c, int num_sms, int batch, int max_blocks, int hint,
                        int* S_out, int* chunk_out) {
-  constexpr int64_t kUnit = 512, kMerge = 32, kVisit = 240, kChunk = 128;
+  constexpr int64_t kUnit = 256, kMerge = 32, kVisit = 240, kChunk = 128;
   const int bs = c.block_size;
   int64_t max_len = (int64_t)max_blocks * bs;
   if (hint > 0 && hint < max_len) max_len = hint;
