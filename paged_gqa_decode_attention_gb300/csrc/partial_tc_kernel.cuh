@@ -307,8 +307,10 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t b) {
   return __half2float(__half(h));
 }
 
-// Two values (|x| <= 448) as three E4M3 terms each, t[0] + t[1] + t[2] = x to fp16's
-// precision: byte 0 of a term belongs to a, byte 1 to b.
+// Two values (|x| <= 448) as three E4M3 terms each, byte 0 of a term for a, byte 1 for
+// b: t[0] + t[1] + t[2] is x rounded to fp16, to 2^-12 |x| or 2^-10, whichever is larger
+// (the terms share one exponent range). For Q, whose rows are scaled to [128, 256): an
+// element is off by at most 2^-17 of its row's largest.
 __device__ __forceinline__ void split_e4m3x3(float a, float b, uint32_t (&t)[3]) {
   uint32_t x;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(b), "f"(a));
@@ -324,6 +326,34 @@ __device__ __forceinline__ void split_e4m3x3(float a, float b, uint32_t (&t)[3])
       r = __hsub2(r, *reinterpret_cast<const __half2*>(&h));
     }
   }
+}
+
+// Two weights x = 256 p in [0, 256] as three E4M3 terms each (bytes as above),
+//   x = t[0] + t[1] / 32 + t[2] / 1024,
+// each term with a range of its own: their products land in accumulators of their
+// own, which fold() weighs. What a term leaves of x is at most 8, and 8 of 256 after the
+// scaling by 32, so 32 x residual stays within [-256, 256]. The first residual is
+// exact in fp32 and then rounded to fp16 (2^-11 of at most x / 16), the second exact in
+// fp16. In all the terms are x to 2^-13 x, or, where the last one is subnormal, 2^-20
+// (2^-28 in p): the tens of thousands of tokens behind one dominant one are small
+// weights each, and with one range for all three terms (2^-18 in p) they left the
+// weighted sum but not the denominator: 32768 tokens that hold 5% of the weight came
+// out off by 4.5e-2 of their values.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t (&t)[3]) {
+  uint16_t e;
+  uint32_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(b), "f"(a));
+  t[0] = e;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(e));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"((b - f.y) * 32.f), "f"((a - f.x) * 32.f));
+  const __half2 r = *reinterpret_cast<const __half2*>(&h);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(h));
+  t[1] = e;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(e));
+  const __half2 r2 = __hmul2(__hsub2(r, *reinterpret_cast<const __half2*>(&h)), __float2half2_rn(32.f));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<const uint32_t*>(&r2)));
+  t[2] = e;
 }
 
 // One work unit: (split, kv head, sequence) and its page / token / chunk range.
@@ -1358,7 +1388,10 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
         if constexpr (KV8) tld(tO(c & 1) + lane_base + (uint32_t)(2 * kN + g0), o3);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < kLd; ++j) o[j] += KV8 ? o2[j] + o3[j] : o2[j];
+        for (int j = 0; j < kLd; ++j) {
+          if constexpr (BSC) o[j] = fmaf(o3[j], 0x1p-10f, fmaf(o2[j], 0x1p-5f, o[j]));  // split_weights
+          else o[j] += KV8 ? o2[j] + o3[j] : o2[j];
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free(c & 1));
@@ -1522,12 +1555,11 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
             l_th[j] = l_th[j] * alpha[j] + (BSC ? prs[j] * ts.z : prs[j]);
           }
           if constexpr (BSC) {
-            // 256 p = t0 + t1 + t2, two heads at a time: p's 11-bit fp16 rounding (2^-12)
-            // is what three 4-bit terms hold, and the differences are exact in fp16
+            // two heads at a time
 #pragma unroll
             for (int j = 0; j < kGA; j += 2) {
               uint32_t t3[3];
-              split_e4m3x3(prs[j] * ts.w, j + 1 < kGA ? prs[j + 1 < kGA ? j + 1 : j] * ts.w : 0.f, t3);
+              split_weights(prs[j] * ts.w, j + 1 < kGA ? prs[j + 1 < kGA ? j + 1 : j] * ts.w : 0.f, t3);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 if (j + k < kGA && j + k < ng) {
