@@ -298,15 +298,6 @@ __device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo) {
   if constexpr (kRow == 64) return sdesc_sw64(saddr, lbo, 512); else return sdesc_sw128(saddr, lbo, 1024);
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float x) {
-  return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
-  __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
-  return __half2float(__half(h));
-}
-
 // Two values (|x| <= 448) as three E4M3 terms each, byte 0 of a term for a, byte 1 for
 // b: t[0] + t[1] + t[2] is x rounded to fp16, to 2^-12 |x| or 2^-10, whichever is larger
 // (the terms share one exponent range). For Q, whose rows are scaled to [128, 256): an
@@ -1389,8 +1380,8 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < kLd; ++j) {
-          if constexpr (BSC) o[j] = fmaf(o3[j], 0x1p-10f, fmaf(o2[j], 0x1p-5f, o[j]));  // split_weights
-          else o[j] += KV8 ? o2[j] + o3[j] : o2[j];
+          if constexpr (KV8) o[j] = fmaf(o3[j], 0x1p-10f, fmaf(o2[j], 0x1p-5f, o[j]));  // split_weights
+          else o[j] += o2[j];
         }
         tc_fence_before();
         __syncwarp();
@@ -1554,8 +1545,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
             prs[j] = BSC ? ex2_ftz(s[j] - mn) : exp2f(s[j] - mn);
             l_th[j] = l_th[j] * alpha[j] + (BSC ? prs[j] * ts.z : prs[j]);
           }
-          if constexpr (BSC) {
-            // two heads at a time
+          if constexpr (KV8) {  // two heads at a time; rows of padding heads stay zero
 #pragma unroll
             for (int j = 0; j < kGA; j += 2) {
               uint32_t t3[3];
@@ -1571,27 +1561,14 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
             }
           }
 #pragma unroll
-          for (int j = 0; j < (BSC ? 0 : kGA); ++j) {
+          for (int j = 0; j < (KV8 ? 0 : kGA); ++j) {
             const float pr = prs[j];
             if (j < ng) {  // rows of padding heads stay zero
               const int g = g0 + j;
-              if constexpr (KV8) {
-                // p * 256 = t0 + t1 + t2 in fp8 (about 12 significant bits)
-                const float x = pr * kP8Scale;
-                const uint8_t b0 = to_e4m3(x);
-                const float r0 = x - e4m3_to_float(b0);
-                const uint8_t b1 = to_e4m3(r0);
-                const uint8_t b2 = to_e4m3(r0 - e4m3_to_float(b1));
-                const uint32_t off = op8_offset(g, t);
-                pb[off] = b0;
-                pb[kOpHalf + off] = b1;
-                pb[2 * kOpHalf + off] = b2;
-              } else {
-                const typename H::T hi = H::from(pr);
-                const typename H::T lo = H::from(pr - H::to(hi));
-                *reinterpret_cast<typename H::T*>(pb + op32_offset(g, t)) = hi;
-                *reinterpret_cast<typename H::T*>(pb + op32_offset(kN + g, t)) = lo;
-              }
+              const typename H::T hi = H::from(pr);
+              const typename H::T lo = H::from(pr - H::to(hi));
+              *reinterpret_cast<typename H::T*>(pb + op32_offset(g, t)) = hi;
+              *reinterpret_cast<typename H::T*>(pb + op32_offset(kN + g, t)) = lo;
             }
           }
           if (grp == 0 && n_valid < kT) {

@@ -8,8 +8,9 @@ off by at most max(2^-13 P', 2^-28). The sums: a thread adds up to L / 128 weigh
 and the accumulators take L / 128 folds of 128-token products, each addition off by
 2^-24 of the running value; at L = 131072 that is 2^-14 for either. A logit is off by
 at most delta = scale * (Q sum |q_i k_i| + 2^-17 max |q| sum |k_i|) + 2^-20 (|s| + 64)
-with Q = 2 D 2^-24, plus 2^-12 for fp16 queries, which moves a weight by at most
-exp(2 delta). So
+with Q = 2 D 2^-24, plus 2^-12 for fp16 queries of more than bf16's 8 bits (three E4M3
+terms; the two terms that the per-head call takes hold 8), which moves a weight by at
+most exp(2 delta). So
   |out - exact| <= (2^-12 + 4 delta) sum w |v| + 2^-28 max(w vs) sum_t |v8_t| + half a
 step of the output type,
 which stays below the flat 2e-3 of fp32 output in every case here.
@@ -36,14 +37,15 @@ class Tail:
     token holds about that share of the weight. The other tokens' logits deviate by 0.5; values
     have mean 1 and deviation 1, the dominant token's are 0."""
 
-    def __init__(self, G, Hkv, D, bs, L, dt):
+    def __init__(self, G, Hkv, D, bs, L, dt, q_bits8=False):
         rng = np.random.default_rng(L + 17 * G + D)
         pages = L // bs
         assert pages * bs == L
         nb, B = pages - 1 + len(SHARES), len(SHARES)
         self.G, self.Hkv, self.D, self.bs, self.L, self.dt = G, Hkv, D, bs, L, dt
+        self.q_terms = 3 if dt == "fp16" and not q_bits8 else 2
         q = np.abs(rng.standard_normal((1, G * Hkv, D))) + 0.5
-        self.q = torch.from_numpy(np.repeat(q, B, 0)).to(DT[dt])
+        self.q = torch.from_numpy(np.repeat(q, B, 0)).to(torch.bfloat16 if q_bits8 else DT[dt]).to(DT[dt])
         self.scale = float(np.float32(D ** -0.5))
         # logits: a byte value of 1 in every dimension is worth `unit`; 448 of them the largest gap
         total, norm = q.sum(-1).mean(), np.sqrt((q ** 2).sum(-1)).mean()
@@ -66,10 +68,10 @@ class Tail:
         self.k8, self.v8, self.nb = k8, v8, nb
 
     def want(self, ks, vs):
-        """(exact, tolerance) for per-head scales ks, vs [Hkv]; all that the sequences share once."""
+        """(exact, tolerance) for per-head scales ks, vs [Hkv]."""
         B, Hq, D = self.q.shape
         out, tol = np.zeros(self.q.shape), np.zeros(self.q.shape)
-        Q = 2 * D * 2.0 ** -24 + (2.0 ** -12 if self.dt == "fp16" else 0.0)
+        Q = 2 * D * 2.0 ** -24 + (2.0 ** -12 if self.q_terms == 3 else 0.0)
         for h in range(self.Hkv):
             for b in range(B):
                 k = ref.decode(self.k8[self.table[b], :, h]).reshape(self.L, D)
@@ -125,6 +127,20 @@ def test_block_scaled_long_tail_behind_a_dominant_token(G, Hkv, D, bs, L, dt):
     want = t.want(ks, vs)
     scales = dict(k_scale=torch.from_numpy(np.tile(ks, (t.nb, 1))).to(DEV),
                   v_scale=torch.from_numpy(np.tile(vs, (t.nb, 1))).to(DEV))
+    args = t.args()
+    with t.attn() as attn:
+        for s in (1, 0, 3):
+            check(attn.run(*args, **scales, num_splits=s, out_dtype=torch.float32), want, f"splits {s}")
+        check(attn.run(*args, **scales, num_splits=1), want, dt)
+        assert attn.check_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("G,Hkv,D,bs,L,dt", CASES)
+def test_per_head_scales_long_tail_behind_a_dominant_token(G, Hkv, D, bs, L, dt):
+    t = Tail(G, Hkv, D, bs, L, dt, q_bits8=True)
+    ks, vs = np.full(Hkv, t.ks, np.float32), np.full(Hkv, 1 / 64, np.float32)
+    want = t.want(ks, vs)
+    scales = dict(k_scale=torch.from_numpy(ks).to(DEV), v_scale=torch.from_numpy(vs).to(DEV))
     args = t.args()
     with t.attn() as attn:
         for s in (1, 0, 3):
