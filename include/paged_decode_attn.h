@@ -368,7 +368,9 @@ int paged_decode_attn_remap_table(int32_t* block_table, int batch, int max_block
  * ascending within num_rows, or a context length below n_b or above
  * max_blocks * block_size or 2^31 - 1 - block_size; the sequence is not
  * appended) or 2 (a block id outside
- * [0, num_blocks); the block is skipped), and the sequence. Outputs must not
+ * [0, num_blocks); the block is skipped), and the sequence. Where cu_rows descends
+ * anywhere, some blocks of the other sequences may be skipped too; each block of
+ * theirs is written in full or left as it was. Outputs must not
  * overlap inputs or each other (PDA_EALIAS). Asynchronous on `stream`;
  * allocates nothing; graph-capturable. */
 int paged_decode_attn_append_kv_fp8(const void* k, int64_t k_token_stride, const void* v,

@@ -89,7 +89,9 @@ __device__ __forceinline__ void record(int* err, int code, int detail) {
 // unit_sequence: the sequence of unit u (b = -1: none), its rows and its length: a
 // 32-way search for the last b with base(b) <= u, one round of loads per factor
 // of 32 of the batch; the last round's lanes have loaded what is known of their
-// sequences along with it.
+// sequences along with it. Where cu does not ascend it gives some sequence or none,
+// and the caller checks that u is one of that sequence's slots: then u still stands
+// for one block of one sequence, and no other unit for the same one.
 // (A division by a block size that the compiler does not know would cost more
 // than the rows.)
 template <int BS>
@@ -343,15 +345,25 @@ __global__ void __launch_bounds__(kAppendThreads, kRope == kRopeNone ? 4 : 3)
 
   __shared__ uint32_t s_max[kAppendWarps];
   const int u = (int)blockIdx.x / p.groups, grp = (int)blockIdx.x - u * p.groups;
+  // Unit u also reports sequence u's rows where they descend or leave the input: the
+  // search need not find such a sequence. (Requested before the search, so that
+  // nothing waits for them; there are at least B units.)
+  const bool reports = grp == 0 && threadIdx.x == 0 && u < p.B && p.err != nullptr;
+  int64_t own_lo = 0, own_hi = 0;
+  if (reports) {
+    own_lo = __ldg(p.cu + u);
+    own_hi = __ldg(p.cu + u + 1);
+  }
   const UnitSeq seq = unit_sequence<BS>(p, u, lane);
+  if (reports && (own_lo < 0 || own_hi < own_lo || own_hi > p.T)) record(p.err, kErrContextLen, u);
   const int b = seq.b, len = seq.len;
   if (b < 0) return;
   const int64_t r_lo = seq.r_lo, r_hi = seq.r_hi, n = r_hi - r_lo;
   constexpr int bs = BS;
   const int64_t base = block_index<BS>(r_lo) + b, slots = block_index<BS>(r_hi) + b + 1 - base;
   const int64_t j = u - base;
-  if (n == 0 || j >= slots) return;
-  if (r_lo < 0 || n < 0 || r_hi > p.T || n > len || len > INT_MAX - bs ||
+  if (n <= 0 || j < 0 || j >= slots || r_lo < 0 || r_hi > p.T) return;  // (reported above)
+  if (n > len || len > INT_MAX - bs ||
       (int64_t)len > (int64_t)p.max_blocks * bs) {
     if (threadIdx.x == 0) record(p.err, kErrContextLen, b);
     return;
