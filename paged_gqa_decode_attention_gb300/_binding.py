@@ -234,10 +234,7 @@ class PagedDecodeAttention:
         and v_cache are torch.float8_e4m3fn (or uint8) tensors; k_scale and
         v_scale are fp32 device tensors of Hkv (per kv head) or 1 values, or,
         for a block-scaled cache (append_kv_fp8), both [num_blocks, Hkv]."""
-        # two dimensions and more values than heads: block scales (with one block they are
-        # the heads' scales)
-        if self.kv_fp8 and (_is_block_scale(k_scale, self._geometry[1]) or
-                            _is_block_scale(v_scale, self._geometry[1])):
+        if self.kv_fp8 and _are_block_scales(k_scale, v_scale, k_cache, self._geometry[1]):
             return self._run_block_scaled(q, k_cache, v_cache, block_table, context_lens, scale,
                                           out, num_splits, max_context_len_hint, out_dtype,
                                           stream, k_scale, v_scale)
@@ -537,9 +534,15 @@ def _pointers(device: int, named) -> list[int]:
     return out
 
 
-def _is_block_scale(t, num_kv_heads: int) -> bool:
-    """Two dimensions and more values than heads (with one block they are the heads' scales)."""
-    return t is not None and t.dim() == 2 and t.numel() not in (1, num_kv_heads)
+def _are_block_scales(k_scale, v_scale, k_cache, num_kv_heads: int) -> bool:
+    """Either has two dimensions and more values than heads; of a cache of one block, both are
+    [1, Hkv] (the heads' scales as well, but fp16 queries keep all their bits in this call)."""
+    for t in (k_scale, v_scale):
+        if t is not None and t.dim() == 2 and t.numel() not in (1, num_kv_heads):
+            return True
+    one = (1, num_kv_heads)
+    return (k_scale is not None and v_scale is not None and k_scale.shape == one and
+            v_scale.shape == one and k_cache.shape[0] == 1)
 
 
 def _rows16(name: str, t: torch.Tensor, device: int, dtype) -> tuple[int, int]:

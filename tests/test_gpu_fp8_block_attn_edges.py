@@ -1,0 +1,52 @@
+"""Decode attention over a block-scaled FP8 cache at the edges of its formats:
+one block, queries that need all of fp16's bits."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from test_gpu_fp8_block_attn import Problem, check, expect  # noqa: E402
+
+
+def two_term_residual(x):
+    """What two E4M3 terms of x, scaled so that the largest is in [128, 256), leave of it."""
+    y = np.asarray(x, np.float64) * 128
+    for _ in range(2):
+        y = y - ref.decode(ref.encode(y))
+    return y / 128
+
+
+@pytest.mark.parametrize("G,Hkv,D,bs", [(4, 2, 128, 16), (8, 1, 128, 64), (2, 8, 64, 32)])
+@pytest.mark.parametrize("blocks", [1, 2])
+def test_fp16_queries_keep_their_bits_however_many_blocks(G, Hkv, D, bs, blocks):
+    """Half the dimensions of q leave a positive rest after two E4M3 terms, half a negative one,
+    and the first of two tokens meets them with large keys of opposite signs: two terms would
+    move its logit by about 0.2. Three hold an fp16 value exactly (4 + 4 + 4 bits), so the tolerance is the
+    one of exact queries."""
+    grid = 1 + np.arange(1024) / 1024  # fp16 values in [1, 2)
+    rest = two_term_residual(grid)
+    near = grid < 1.25
+    hi, lo = grid[near][np.argmax(rest[near])], grid[near][np.argmin(rest[near])]
+    p = Problem(31, G, Hkv, D, bs, [2], "fp16", extra_blocks=blocks - 1)
+    q = np.where(np.arange(D) < D // 2, hi, lo)
+    p.q = torch.from_numpy(np.tile(q, (1, G * Hkv, 1))).to(torch.float16)
+    blk = p.table[0, 0]
+    p.kc[blk] = 0
+    p.kc[blk, 0] = ref.encode(np.where(np.arange(D) < D // 2, 448.0, -448.0))
+    p.ks[blk] = 50 / (448 * D / 2 * p.scale)  # 50 from either half
+    v = np.ones((bs, Hkv, D)) * 2.0
+    v[0] = -2.0
+    p.vc[blk], p.vs[blk] = ref.encode(v), 1.0
+    p.upload()
+    want = expect(p.q.double().numpy(), p.kc, p.vc, p.ks, p.vs, p.table, p.lens, float(np.float32(p.scale)), False)
+    moved = p.scale * float(p.ks[blk, 0]) * 448 * (np.abs(two_term_residual(q)).sum())
+    assert moved > 0.1
+    with p.attn() as attn:
+        check(p.run(attn, out_dtype=torch.float32), want, "fp32 out")
+        check(p.run(attn), want)
