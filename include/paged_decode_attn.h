@@ -418,7 +418,9 @@ int paged_decode_attn_gather_kv_fp8(const void* k_cache, const void* v_cache,
  * blk = block_table[b, t / block_size]. k_scale and v_scale are [num_blocks,
  * Hkv] fp32, finite and >= 0, whatever wrote them (powers of two or not); a
  * block id outside [0, num_blocks) reads zeros. The largest and the smallest
- * nonzero V scale that a sequence uses may lie a factor of 2^100 apart.
+ * V scale that a sequence uses may lie a factor of 2^100 apart, scales below
+ * 2^-60 and 0 counting as 2^-60. Values of V are to be below 2^121 (beyond,
+ * sums of several splits may overflow).
  * num_splits 0: a rule of this call's own (a batch's lengths may be spread out,
  * chunks of 128 tokens are whole); paged_decode_attn_plan and
  * paged_decode_attn_launch_shape describe the other run calls. */

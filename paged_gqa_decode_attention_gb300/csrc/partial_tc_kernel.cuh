@@ -1688,9 +1688,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
       U.n_splits_b = reinterpret_cast<volatile int*>(st)[kStU + 1];
       const int hq0 = U.h * G;
       // V dequantisation scale (and the fp8 split factor of P)
-      // (BSC: the V scales are in the weights)
-      const float vsc = (!BSC && p.v_scale ? __ldg(p.v_scale + (p.scale_per_head ? U.h : 0)) : 1.f) *
-                        (KV8 ? 1.f / kP8Scale : 1.f);
+      // (BSC: the V scales are in the weights, and the sum is about 1 / vs: the split
+      // factor comes off first, or large values would overflow)
+      const float vsc = BSC ? 1.f
+                            : (p.v_scale ? __ldg(p.v_scale + (p.scale_per_head ? U.h : 0)) : 1.f) *
+                                  (KV8 ? 1.f / kP8Scale : 1.f);
+      constexpr float kAccScale = BSC ? 1.f / kP8Scale : 1.f;
       if (p.cluster > 1 && U.n_splits_b > 1) {
         // Cluster launch: this split's normalised partial and log-sum-exp stay
         // in this CTA's state slot; once every other CTA of the cluster has
@@ -1698,7 +1701,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
         // reading the other splits' slots through distributed shared memory.
         if (t < D) {
 #pragma unroll
-          for (int g = 0; g < G; ++g) st[g * kHeadDim + t] = st[g * kHeadDim + t] / st[kStSum + g] * vsc;
+          for (int g = 0; g < G; ++g) st[g * kHeadDim + t] = st[g * kHeadDim + t] * kAccScale / st[kStSum + g] * vsc;
         }
         if (t == 0) {
 #pragma unroll
@@ -1764,7 +1767,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float Ls = st[kStSum + g];
-          const float o = st[g * kHeadDim + t] / Ls * vsc;
+          const float o = st[g * kHeadDim + t] * kAccScale / Ls * vsc;
           const int64_t row = (int64_t)U.b * p.Hq + hq0 + g;
           if (U.n_splits_b == 1) {
             if (p.out_f32) static_cast<float*>(p.out)[row * D + t] = o;

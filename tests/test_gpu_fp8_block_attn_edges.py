@@ -1,5 +1,5 @@
 """Decode attention over a block-scaled FP8 cache at the edges of its formats:
-one block, queries that need all of fp16's bits."""
+one block, queries that need all of fp16's bits, the largest scales."""
 import numpy as np
 import pytest
 import torch
@@ -49,4 +49,18 @@ def test_fp16_queries_keep_their_bits_however_many_blocks(G, Hkv, D, bs, blocks)
     assert moved > 0.1
     with p.attn() as attn:
         check(p.run(attn, out_dtype=torch.float32), want, "fp32 out")
+        check(p.run(attn), want)
+
+
+@pytest.mark.parametrize("G,Hkv,D,bs", [(4, 2, 128, 16), (8, 1, 128, 32), (3, 2, 64, 64), (16, 1, 64, 16)])
+def test_large_values(G, Hkv, D, bs):
+    """V up to nearly 2^121, over one split and several; one token's come out as they are."""
+    p = Problem(32, G, Hkv, D, bs, [700, 1, 130, 3], "bf16", spread=0)
+    p.vs *= np.float32(2.0 ** 113)
+    p.upload()
+    want = p.want()
+    assert np.abs(want[0]).max() > 2.0 ** 120
+    with p.attn() as attn:
+        for s in (1, 0, 4):
+            check(p.run(attn, num_splits=s, out_dtype=torch.float32), want, f"splits {s}")
         check(p.run(attn), want)
