@@ -93,6 +93,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "pda_internal.h"
@@ -176,6 +177,9 @@ constexpr float kP8Scale = 256.f;          // FP8 K/V: P is split at p * 256
 // Block-scaled FP8 K/V: the smallest V scale that enters a weight's exponent;
 // a smaller one (a block of zeros) multiplies the weight instead.
 constexpr float kMinBlockScale = 0x1p-60f;
+// No fp8 dot product of 128 terms (|q| <= 256, |k| <= 448) is larger: times a K scale
+// over this it does not overflow, whatever finite scale that is.
+constexpr float kDotBound = 0x1p24f;
 // Its units beyond one a CTA are taken longest sequence first, from a directory
 // that every CTA builds of a batch of up to kDirMax sequences.
 constexpr int kDirMax = 1024;
@@ -964,7 +968,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
   // maximum m' of s' stands where that of s does everywhere (accumulators, sums
   // and log-sum-exp are relative to it). A scale below kMinBlockScale (a block of
   // zeros) enters s' as that and multiplies P' by the rest. Lane i turns page
-  // i's scales into (ks, log2 vs, 1 / vs, the split factor of P'); the second arrival
+  // i's scales into (ks / kDotBound, log2 vs, 1 / vs, the split factor of P'); the second arrival
   // on the chunk's s_full says that they are there.
   // Not in the softmax, whose steps set the pace (58.8 us against 58.0 in the
   // QK^T warp for B = 4, L = 32768 at 32/8 heads).
@@ -976,13 +980,14 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
       if (!__all_sync(kFull, ok)) failed = true;
       if (failed) return;
       if (lane < PPS) {  // lanes past the chunk's pages: stale, not read
+        // (2^-24 * ks is exact from 2^-102 on)
         const float* sc = reinterpret_cast<const float*>(base + L::kOffSc) + e * 2 * kMaxPps;
         const float vs = sc[kMaxPps + lane], vse = fmaxf(vs, kMinBlockScale);
         // 2^lvs and ivs are vs and 1 / vs to about 2^-22; their product is 1 to an ulp or
         // two, so the sum takes the weight that the V bytes are multiplied with
         const float lvs = __log2f(vse), ivs = exp2f(-lvs);
         reinterpret_cast<float4*>(base + L::kOffTs)[(c & 1) * kMaxPps + lane] = make_float4(
-            sc[lane], lvs, ivs, vs < kMinBlockScale ? kP8Scale * (vs * ivs) : kP8Scale);
+            sc[lane] * (1.f / kDotBound), lvs, ivs, vs < kMinBlockScale ? kP8Scale * (vs * ivs) : kP8Scale);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(s_full(c & 1));
@@ -1476,7 +1481,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
           if (!__all_sync(kFull, okq)) failed = true;
           const float* qs = reinterpret_cast<const float*>(base + kOffQs) + (jq & 1) * kGE;
 #pragma unroll
-          for (int j = 0; j < kGA; ++j) qsc[j] = j < ng ? p.qscale * ksc * qs[g0 + j] : 0.f;
+          for (int j = 0; j < kGA; ++j) {
+            qsc[j] = j < ng ? p.qscale * ksc * qs[g0 + j] : 0.f;
+            // BSC: with kDotBound, which the K scale is divided by; finite, so that a
+            // logit of 0 stays one
+            if constexpr (BSC) qsc[j] = fmaxf(fminf(qsc[j] * kDotBound, FLT_MAX), -FLT_MAX);
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < kGA; ++j) qsc[j] = p.qscale * ksc;
@@ -1491,7 +1501,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
           tld(tS(c & 1) + lane_base + (uint32_t)g0, s);
           if constexpr (KV8) tld(tS(c & 1) + lane_base + (uint32_t)(kN + g0), s2);
           if constexpr (QT == 3) tld(tS(c & 1) + lane_base + (uint32_t)(2 * kN + g0), s3);
-          // (ks, log2 vs, 1 / vs, split factor) of the token's page
+          // (ks / kDotBound, log2 vs, 1 / vs, split factor) of the token's page
           float4 ts = make_float4(1.f, 0.f, 1.f, kP8Scale);
           if constexpr (BSC)
             ts = reinterpret_cast<const float4*>(

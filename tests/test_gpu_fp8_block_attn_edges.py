@@ -64,3 +64,20 @@ def test_large_values(G, Hkv, D, bs):
         for s in (1, 0, 4):
             check(p.run(attn, num_splits=s, out_dtype=torch.float32), want, f"splits {s}")
         check(p.run(attn), want)
+
+
+@pytest.mark.parametrize("G,Hkv,D,bs", [(4, 2, 128, 16), (8, 1, 128, 32), (3, 2, 64, 64), (16, 1, 64, 16)])
+@pytest.mark.parametrize("e", [120, 100, -52])
+def test_large_and_small_keys_against_queries_of_the_other_kind(G, Hkv, D, bs, e):
+    """K scales 2^e times the usual ones and queries as much smaller or larger: the usual logits.
+    One block's keys are zeros under the largest scale."""
+    p = Problem(33, G, Hkv, D, bs, [700, 5, 130], "bf16")
+    p.ks *= np.float32(2.0 ** e)
+    p.q = (p.q.float() * 2.0 ** -e).to(torch.bfloat16)
+    zero = p.table[0, 1]
+    p.kc[zero], p.ks[zero] = 0, 2.0 ** 127
+    p.upload()
+    want = p.want()
+    with p.attn() as attn:
+        for s in (1, 0):
+            check(p.run(attn, num_splits=s, out_dtype=torch.float32), want, f"splits {s}")
