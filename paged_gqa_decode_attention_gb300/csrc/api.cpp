@@ -391,7 +391,7 @@ int run_any(pda_handle h, const void* q, const void* k_cache, const void* v_cach
     return fail(PDA_EINVAL, "k_scale and v_scale must hold [num_blocks, Hkv] block scales");
   if (max_blocks < 1 || max_blocks > c.max_blocks_per_seq)
     return fail(PDA_EINVAL, "max_blocks out of [1, max_blocks_per_seq]");
-  if (num_blocks < 1 || num_blocks * c.block_size > (int64_t)INT_MAX)
+  if (num_blocks < 1 || num_blocks > INT_MAX / c.block_size)
     return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
   if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
   if (num_splits < 0 || num_splits > c.max_splits)

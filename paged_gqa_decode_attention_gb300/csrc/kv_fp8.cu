@@ -637,7 +637,7 @@ int check_cache(int num_kv_heads, int head_dim, int block_size, int64_t num_bloc
   if (head_dim != 64 && head_dim != 128) return fail(PDA_EUNSUPPORTED, "head_dim must be 64 or 128");
   if (block_size != 16 && block_size != 32 && block_size != 64)
     return fail(PDA_EUNSUPPORTED, "block_size must be 16, 32 or 64");
-  if (num_blocks < 1 || num_blocks * block_size > (int64_t)INT_MAX)
+  if (num_blocks < 1 || num_blocks > INT_MAX / block_size)
     return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
   return PDA_OK;
 }

@@ -151,7 +151,7 @@ extern "C" int paged_decode_attn_run_noalloc(const void* q, const void* k_cache,
   if (batch == 0) return PDA_OK;
   if (!q || !k_cache || !v_cache || !block_table || !context_lens || !out)
     return fail(PDA_EINVAL, "a tensor pointer is NULL");
-  if (num_blocks < 1 || num_blocks * block_size > (int64_t)INT_MAX)
+  if (num_blocks < 1 || num_blocks > INT_MAX / block_size)
     return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
   if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
   if (num_splits < 0 || num_splits > pda::kMaxSplits)
