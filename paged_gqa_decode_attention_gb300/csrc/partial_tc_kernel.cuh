@@ -174,6 +174,10 @@ __host__ __device__ constexpr int epi_heads(int G) { return G > 8 ? 16 : 8; }
 __host__ __device__ constexpr int epi_floats(int G) { return epi_heads(G) * 128 + 2 * epi_heads(G) + 4; }
 __host__ __device__ constexpr int epi_slots(int G, bool kv8) { return G > 8 && !kv8 ? 1 : 2; }
 constexpr float kP8Scale = 256.f;          // FP8 K/V: P is split at p * 256
+// fp16 K/V: P_hi + P_lo = p * 2^14. Unscaled, weights below 2^-25 were no fp16 values and
+// left the weighted sum but not the denominator (131072 tokens that hold 0.1% of the
+// weight came out as zeros).
+constexpr float kP16Scale = 0x1p14f;
 // Block-scaled FP8 K/V: the smallest V scale that enters a weight's exponent;
 // a smaller one (a block of zeros) multiplies the weight instead.
 constexpr float kMinBlockScale = 0x1p-60f;
@@ -1572,7 +1576,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
           }
 #pragma unroll
           for (int j = 0; j < (KV8 ? 0 : kGA); ++j) {
-            const float pr = prs[j];
+            const float pr = FP16 ? prs[j] * kP16Scale : prs[j];
             if (j < ng) {  // rows of padding heads stay zero
               const int g = g0 + j;
               const typename H::T hi = H::from(pr);
@@ -1697,12 +1701,12 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
       U.b = u / p.num_splits / p.Hkv;
       U.n_splits_b = reinterpret_cast<volatile int*>(st)[kStU + 1];
       const int hq0 = U.h * G;
-      // V dequantisation scale (and the fp8 split factor of P)
+      // V dequantisation scale (and the factor that P is split at)
       // (BSC: the V scales are in the weights, and the sum is about 1 / vs: the split
       // factor comes off first, or large values would overflow)
       const float vsc = BSC ? 1.f
                             : (p.v_scale ? __ldg(p.v_scale + (p.scale_per_head ? U.h : 0)) : 1.f) *
-                                  (KV8 ? 1.f / kP8Scale : 1.f);
+                                  (KV8 ? 1.f / kP8Scale : FP16 ? 1.f / kP16Scale : 1.f);
       constexpr float kAccScale = BSC ? 1.f / kP8Scale : 1.f;
       if (p.cluster > 1 && U.n_splits_b > 1) {
         // Cluster launch: this split's normalised partial and log-sum-exp stay
