@@ -423,7 +423,8 @@ int paged_decode_attn_gather_kv_fp8(const void* k_cache, const void* v_cache,
  * sums of several splits may overflow).
  * num_splits 0: a rule of this call's own (a batch's lengths may be spread out,
  * chunks of 128 tokens are whole); paged_decode_attn_plan and
- * paged_decode_attn_launch_shape describe the other run calls. */
+ * paged_decode_attn_launch_shape describe the other run calls. The
+ * allocation-free entry point below takes 16-bit caches only. */
 int paged_decode_attn_run_block_scaled(pda_handle handle, const void* q, const void* k_cache,
                                        const void* v_cache, const float* k_scale,
                                        const float* v_scale, const int32_t* block_table,

@@ -23,10 +23,13 @@
 // 16-byte vectors a lane, at most 8: with 16 only two CTAs fit an SM and their
 // chains of loads did not overlap, 51 us against 40), so each is read once.
 // Measured on GB300 (back to back, copy rate 6784.5 GB/s): 41984 fp16 rows of 8
-// heads, D 128, blocks of 32: 40.0 us, 6450 GB/s; 256 single bf16 tokens 4.2 us.
-// With rotation the exact rounding's instructions bound it: 21631 bf16 rows at
-// 32/8 heads 99.6 us, 4940 GB/s (57% of issue slots, no row read twice).
-// Read-back of 24058 tokens to bf16: 24.8 us, 5950 GB/s.
+// heads, D 128, blocks of 32: 39.9 us, 6460 GB/s; 256 single bf16 tokens 4.1 us.
+// With rotation 21631 bf16 rows at 32/8 heads take 99.4 us, 4940 GB/s (adjacent
+// pairs 97.8, half the dimensions rotated 94.5): each q row is one chain of load,
+// rotation and store, at 24 warps an SM, whose latency (first stall: long scoreboard)
+// the exact rounding's instructions (57% of the issue slots) do not hide; no row is read
+// twice. Read-back of 24058 tokens to bf16 or fp16: 24.5 us, 6030 GB/s, to fp32
+// 40.4 us, 6100 GB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -81,9 +81,10 @@
 // (chunk_scales) and, at G <= 4, the fp8 q terms; the V scale is part of the
 // weights; fp16 queries take three fp8 terms; the next unit is claimed while the
 // current one runs, and units beyond one a CTA are taken longest sequence first.
-// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 52.9 us (0.75
-// of the 269 MB's time at the copy rate), 128 x 32-4096 at 64/8 heads 63.8 us (0.57),
-// 8 x 32768 at 32/8 heads 90.7 us (0.87), 128/8 heads 8 x 16384 80 us.
+// Measured (GB300, back to back): 4 x 32768 tokens at 32/8 heads, D 128 53.4 us (0.74
+// of the 269 MB's time at the copy rate; fp16 queries 53.8), 128 x 32-4096 at 64/8
+// heads 63.8 us (0.58), 8 x 32768 at 32/8 heads 92.0 us (0.86; D 64 75.5 us, 0.53),
+// 8 x 16384 at 128/8 heads 82.1 us (0.48).
 // Every wait is bounded; a timed-out CTA records error code 3, stops issuing
 // work, still passes every barrier, counts itself done with the work counter
 // (so the counters are reset for the next call) and frees its TMEM.
@@ -155,9 +156,10 @@ __host__ __device__ constexpr int warp_pv2(int G, int D, bool kv8) {
 }
 // TMEM columns: S and O, double-buffered. The terms of a split operand are
 // stacked along N so one MMA carries all of them (the tensor pipe's cost
-// is per instruction at these small N): S holds 16 columns (32 with FP8
-// K/V: q_hi and q_lo), O 32 (P_hi, P_lo; 48 with FP8: three P terms); the
-// softmax adds the stacked columns of a head.
+// is per instruction at these small N): S holds 16 columns (with FP8 K/V 32,
+// q_hi and q_lo, or 48, three terms of block-scaled calls' fp16 queries), O 32
+// (P_hi, P_lo; 48 with FP8: three P terms); the softmax adds the stacked columns
+// of a head, fold() those of O with the terms' factors (split_weights).
 constexpr uint32_t kTmemCols = 256;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kUnitRing = 4;               // slots of the shared unit queue
@@ -1251,7 +1253,7 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
       if (lane == 0) {
         const uint32_t kb = base_u32 + kOffK + slot * kSlotBytes;
         if constexpr (KV8) {
-          // S = K . [Q_hi; Q_lo]^T (N = 32: rows 16..31 of the operand are q_lo):
+          // S = K . [Q_0; Q_1(; Q_2)]^T (N = 32 or 48, one 16-row block per term):
           // 32 fp8 dims (32 bytes) per step
           const uint32_t q8 = base_u32 + kOffQ8 + qb * L::kQ8Bytes;
 #pragma unroll
@@ -1554,6 +1556,8 @@ __global__ void __launch_bounds__(tc_threads(G, D, KV8, BSC), 1)
               mx = fmaxf(fmaxf(rb[j], rb[8 + j]), fmaxf(rb[16 + j], rb[24 + j]));
             }
             const float mn = fmaxf(m_run[j], mx);  // finite: every chunk holds a valid token
+            // (ex2_ftz drops what is below 2^-126 of the largest P': times 1 / vs of a
+            // block of zeros, 2^60, that is 2^-66 of the sum)
             alpha[j] = BSC ? ex2_ftz(m_run[j] - mn) : exp2f(m_run[j] - mn);
             m_run[j] = mn;
             prs[j] = BSC ? ex2_ftz(s[j] - mn) : exp2f(s[j] - mn);
