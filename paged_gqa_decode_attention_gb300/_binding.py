@@ -234,7 +234,10 @@ class PagedDecodeAttention:
         and v_cache are torch.float8_e4m3fn (or uint8) tensors; k_scale and
         v_scale are fp32 device tensors of Hkv (per kv head) or 1 values, or,
         for a block-scaled cache (append_kv_fp8), both [num_blocks, Hkv]."""
-        if self.kv_fp8 and _are_block_scales(k_scale, v_scale, k_cache, self._geometry[1]):
+        if self.kv_fp8 and (_is_block_scale(k_scale, self._geometry[1]) or
+                            _is_block_scale(v_scale, self._geometry[1]) or
+                            self._one_block_scales(q, k_cache, v_cache, block_table,
+                                                   context_lens, out, k_scale, v_scale)):
             return self._run_block_scaled(q, k_cache, v_cache, block_table, context_lens, scale,
                                           out, num_splits, max_context_len_hint, out_dtype,
                                           stream, k_scale, v_scale)
@@ -274,6 +277,19 @@ class PagedDecodeAttention:
                 int(num_splits), int(max_context_len_hint), _DT[out_dtype])
         _check(self.lib, self.lib.paged_decode_attn_run_scaled(*args))
         return out
+
+    def _one_block_scales(self, q, k_cache, v_cache, block_table, context_lens, out, k_scale,
+                          v_scale) -> bool:
+        """[1, Hkv] scales of a cache of one block: the heads' scales as well, but fp16 queries
+        keep all their bits in the block-scaled call. Tensors in other shapes than it takes
+        (a flat q, a table of more rows than the batch) go on as per-head calls."""
+        Hq, Hkv, bs, D = self._geometry
+        if k_scale is None or v_scale is None or k_scale.shape != (1, Hkv) or v_scale.shape != (1, Hkv):
+            return False
+        one, B = (1, bs, Hkv, D), len(q)
+        return (k_cache.shape == one and v_cache.shape == one and q.shape == (B, Hq, D) and
+                block_table.dim() == 2 and len(block_table) == B and context_lens.shape == (B,) and
+                (out is None or out.shape == q.shape))
 
     def _run_block_scaled(self, q, k_cache, v_cache, block_table, context_lens, scale, out,
                           num_splits, max_context_len_hint, out_dtype, stream, k_scale, v_scale):
@@ -534,15 +550,9 @@ def _pointers(device: int, named) -> list[int]:
     return out
 
 
-def _are_block_scales(k_scale, v_scale, k_cache, num_kv_heads: int) -> bool:
-    """Either has two dimensions and more values than heads; of a cache of one block, both are
-    [1, Hkv] (the heads' scales as well, but fp16 queries keep all their bits in this call)."""
-    for t in (k_scale, v_scale):
-        if t is not None and t.dim() == 2 and t.numel() not in (1, num_kv_heads):
-            return True
-    one = (1, num_kv_heads)
-    return (k_scale is not None and v_scale is not None and k_scale.shape == one and
-            v_scale.shape == one and k_cache.shape[0] == 1)
+def _is_block_scale(t, num_kv_heads: int) -> bool:
+    """Two dimensions and more values than heads."""
+    return t is not None and t.dim() == 2 and t.numel() not in (1, num_kv_heads)
 
 
 def _rows16(name: str, t: torch.Tensor, device: int, dtype) -> tuple[int, int]:

@@ -81,3 +81,25 @@ def test_large_and_small_keys_against_queries_of_the_other_kind(G, Hkv, D, bs, e
     with p.attn() as attn:
         for s in (1, 0):
             check(p.run(attn, num_splits=s, out_dtype=torch.float32), want, f"splits {s}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_one_block_calls_in_the_per_head_shapes(dt):
+    """What the per-head call takes runs with [1, Hkv] scales of a one-block cache as well: a flat
+    q and out, a table and lengths with more rows than the batch."""
+    p = Problem(34, 4, 8, 128, 16, [13, 7], dt, extra_blocks=0)
+    p.kc, p.vc, p.ks, p.vs = p.kc[:1], p.vc[:1], p.ks[:1], p.vs[:1]
+    for c in (p.kc, p.vc):
+        c[(c & 0x7F) == 0x7F] = 0x30
+    p.table[:] = 0
+    p.upload()
+    want = p.want()
+    q, kc, vc, table, lens, scale = p.dev
+    out = torch.empty(2, 32 * 128, dtype=q.dtype, device=q.device)
+    more = torch.cat([table, table]), torch.cat([lens, lens])
+    with p.attn() as attn:
+        check(attn.run(q, kc, vc, table, lens, scale, **p.scales), want)
+        check(attn.run(q.view(2, -1), kc, vc, table, lens, scale, **p.scales), want, "flat q")
+        check(attn.run(q, kc, vc, table, lens, scale, out=out, **p.scales).view(q.shape), want, "flat out")
+        check(attn.run(q, kc, vc, *more, scale, **p.scales), want, "more rows")
+        assert attn.check_device_error() == (0, 0)
