@@ -108,7 +108,9 @@ const char* paged_decode_attn_last_error(void);
 
 /* Validate `cfg`, select cfg->device, and allocate the handle plus its
  * device workspace: max_batch * Hq * max_splits * (head_dim + 1) floats of
- * split partials, max_batch * Hkv ints of split tickets (the last split of a
+ * split partials (at least the rows that paged_decode_attn_run_scored and
+ * paged_decode_attn_run_shared_prefix need: 4 * max_batch * Hq, and two rows per
+ * SM for each of up to 128 rows of max_batch * Hq / Hkv), max_batch * Hkv ints of split tickets (the last split of a
  * sequence's kv head to finish merges the splits; tickets return to zero by
  * the end of every call) and a small error-word area, all zeroed.
  * Returns PDA_OK and stores the handle in *out_handle, or an error (and
@@ -164,6 +166,44 @@ int paged_decode_attn_run_scaled(pda_handle handle, const void* q, const void* k
                                  const float* v_scale, int scale_per_head, void* out,
                                  void* stream, int num_splits, int max_context_len_hint,
                                  int out_dtype);
+
+/* As paged_decode_attn_run, with the scores of token t of a context of L tokens
+ *   s = scale * q . k_t
+ *   s = softcap * tanh(s / softcap)             if softcap > 0
+ *   s = s + alibi_slopes[hq] * (t - (L - 1))    if alibi_slopes (fp32 [Hq], device) is not NULL
+ * and, with window > 0, only the last `window` tokens (t >= L - window) attended to.
+ * 16-bit K/V at head_dim 64 or 128, any group size up to 16 (else
+ * PDA_EUNSUPPORTED); batch <= 16384; `out` has cfg->dtype. The weights enter the
+ * product with V rounded to 16 bits (8 significant bits with bf16, 11 with
+ * fp16) and their rounded values are what the result is divided by. The
+ * work is cut evenly over the GPU; two launches. */
+int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_table,
+                                 const int32_t* context_lens, int batch, int max_blocks,
+                                 int64_t num_blocks, float scale, float softcap,
+                                 const float* alibi_slopes, int window, void* out, void* stream);
+
+/* The same (without a window) for a batch whose sequences share the start of
+ * their contexts: for i < num_prefixes (<= 192), the sequences cu_seqs[i] ..
+ * cu_seqs[i + 1] - 1 have the same ids in their block_table rows for the
+ * first prefix_lens[i] tokens, and those blocks are read once for all of them
+ * (tiles of up to 256 query rows of a kv head). cu_seqs [num_prefixes + 1] and
+ * prefix_lens [num_prefixes] are int32 on the device; block_table and
+ * context_lens hold whole contexts, and the result is that of
+ * paged_decode_attn_run. Of a prefix, whole blocks are shared, and no more than the
+ * shortest context of the group that is not empty holds; a group of one and
+ * a sequence outside every group share nothing. Rows of a group that
+ * do not name the same blocks are the caller's mistake: the ids of the first
+ * sequence that is not empty are the ones read. cu_seqs that does not ascend within
+ * [0, batch] is recorded (code 6 of paged_decode_attn_check_device_error), and the
+ * call then shares nothing. */
+int paged_decode_attn_run_shared_prefix(pda_handle handle, const void* q, const void* k_cache,
+                                        const void* v_cache, const int32_t* block_table,
+                                        const int32_t* context_lens, int batch, int max_blocks,
+                                        int64_t num_blocks, const int32_t* cu_seqs,
+                                        const int32_t* prefix_lens, int num_prefixes, float scale,
+                                        float softcap, const float* alibi_slopes, void* out,
+                                        void* stream);
 
 /* The split plan the heuristic picks (host only, no CUDA call): for a
  * problem of `batch` sequences, `max_blocks` table columns and an optional
@@ -222,7 +262,8 @@ int paged_decode_attn_validate(pda_handle handle, const int32_t* block_table,
 /* Synchronise `stream`, read and clear the handle's device error word.
  * *code receives 0 (no error) or a nonzero code:
  *   1 = context length out of range, 2 = block id out of range (validator);
- *   3 = a pipeline wait inside a kernel gave up after its time limit.
+ *   3 = a pipeline wait inside a kernel gave up after its time limit;
+ *   6 = cu_seqs of a shared-prefix call does not ascend within the batch.
  * (Codes 4 and 5 belong to the error words of paged_decode_attn_rope_kv_write and of
  * the KV-cache movement calls.)
  * *detail receives the sequence index (codes 1, 2) or the split index (3).

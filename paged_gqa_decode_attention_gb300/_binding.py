@@ -51,6 +51,8 @@ EXPORTS = [
     "paged_decode_attn_rope_append_kv_fp8",
     "paged_decode_attn_gather_kv_fp8",
     "paged_decode_attn_run_block_scaled",
+    "paged_decode_attn_run_scored",
+    "paged_decode_attn_run_shared_prefix",
 ]
 
 
@@ -139,6 +141,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.paged_decode_attn_gather_kv_fp8.argtypes = [P, P, P, P, I64, I, I, I, P, I, P, P, I, I,
                                                         P, P, I64, I, P, I, P]
         lib.paged_decode_attn_gather_kv_fp8.restype = I
+        lib.paged_decode_attn_run_scored.argtypes = [P, P, P, P, P, P, I, I, I64, F, F, P, I, P, P]
+        lib.paged_decode_attn_run_scored.restype = I
+        lib.paged_decode_attn_run_shared_prefix.argtypes = [P, P, P, P, P, P, I, I, I64, P, P, I, F,
+                                                            F, P, P, P]
+        lib.paged_decode_attn_run_shared_prefix.restype = I
         if lib.paged_decode_attn_abi_version() != ABI_VERSION:
             raise RuntimeError("ABI version mismatch between binding and library")
         if path is None:
@@ -228,12 +235,31 @@ class PagedDecodeAttention:
 
     def run(self, q, k_cache, v_cache, block_table, context_lens, scale: float | None = None,
             out=None, num_splits: int = 0, max_context_len_hint: int = 0, out_dtype=None,
-            stream=None, k_scale=None, v_scale=None):
+            stream=None, k_scale=None, v_scale=None, softcap: float = 0.0, alibi_slopes=None,
+            window: int = 0):
         """out[B, Hq, D] = paged decode attention; asynchronous on ``stream``
-        (default: torch's current stream). With FP8 caches (kv_fp8), k_cache
+        (default: torch's current stream).
+
+        The scores of token t of a context of L tokens are scale * q.k_t; with
+        ``softcap`` c > 0 they become c * tanh(score / c), ``alibi_slopes``
+        (fp32 [Hq]) then add slope[head] * (t - (L - 1)), and with ``window``
+        w > 0 only the last w tokens are attended to. These three need 16-bit
+        K/V, head_dim 64 or 128 and the query's output type, and take no
+        split count (the work is cut evenly; the length hint is not needed).
+
+        With FP8 caches (kv_fp8), k_cache
         and v_cache are torch.float8_e4m3fn (or uint8) tensors; k_scale and
         v_scale are fp32 device tensors of Hkv (per kv head) or 1 values, or,
         for a block-scaled cache (append_kv_fp8), both [num_blocks, Hkv]."""
+        if softcap or window or alibi_slopes is not None:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("capped, biased or windowed scores take no K/V scales")
+            if num_splits:
+                raise ValueError("capped, biased or windowed scores take no split count")
+            if out_dtype not in (None, self.dtype):
+                raise ValueError(f"capped, biased or windowed scores write {self.dtype}")
+            return self._run_rows(q, k_cache, v_cache, block_table, context_lens, scale, softcap,
+                                  alibi_slopes, out, stream, window=window)
         if self.kv_fp8 and (_is_block_scale(k_scale, self._geometry[1]) or
                             _is_block_scale(v_scale, self._geometry[1]) or
                             self._one_block_scales(q, k_cache, v_cache, block_table,
@@ -276,6 +302,66 @@ class PagedDecodeAttention:
                 per_head, _dev_ptr(out, "out", out_dtype), _stream_ptr(stream),
                 int(num_splits), int(max_context_len_hint), _DT[out_dtype])
         _check(self.lib, self.lib.paged_decode_attn_run_scaled(*args))
+        return out
+
+    def run_shared_prefix(self, q, k_cache, v_cache, block_table, context_lens, cu_seqs,
+                          prefix_lens, scale: float | None = None, softcap: float = 0.0,
+                          alibi_slopes=None, out=None, stream=None):
+        """``run`` for a batch in which sequences share the start of their
+        contexts: the same out, with the shared K/V read once for all of them.
+
+        cu_seqs (int32 [P + 1], ascending) and prefix_lens (int32 [P]): the
+        sequences cu_seqs[i] .. cu_seqs[i + 1] - 1 name the same blocks, in
+        the same order, for their first prefix_lens[i] tokens (of which whole
+        blocks are shared, and no more than the shortest of the contexts that
+        are not empty). Sequences outside every group, and a prefix of 0,
+        share nothing. block_table and context_lens hold whole contexts, as
+        for ``run``. P <= 192. softcap and alibi_slopes as in ``run``."""
+        return self._run_rows(q, k_cache, v_cache, block_table, context_lens, scale, softcap,
+                              alibi_slopes, out, stream, cu_seqs=cu_seqs, prefix_lens=prefix_lens)
+
+    def _run_rows(self, q, k_cache, v_cache, block_table, context_lens, scale, softcap,
+                  alibi_slopes, out, stream, window=0, cu_seqs=None, prefix_lens=None):
+        dt, dev = self.dtype, self.device
+        Hq, Hkv, bs, D = self._geometry
+        B = len(q)
+        if q.shape != (B, Hq, D):
+            raise ValueError("q must be [batch, Hq, D] with the handle's sizes")
+        shape = k_cache.shape
+        if len(shape) != 4 or v_cache.shape != shape or shape[1:] != (bs, Hkv, D):
+            raise ValueError("caches must be [num_blocks, block_size, Hkv, D] with the handle's sizes")
+        if block_table.dim() != 2 or len(block_table) != B or context_lens.shape != (B,):
+            raise ValueError("block_table must be [batch, max_blocks] and context_lens [batch]")
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        kv = None if self.kv_fp8 else dt
+        named = [("q", q, dt), ("k_cache", k_cache, kv), ("v_cache", v_cache, kv),
+                 ("block_table", block_table, torch.int32),
+                 ("context_lens", context_lens, torch.int32), ("out", out, dt)]
+        if alibi_slopes is not None:
+            if alibi_slopes.shape != (Hq,):
+                raise ValueError("alibi_slopes must be [Hq]")
+            named.append(("alibi_slopes", alibi_slopes, torch.float32))
+        if cu_seqs is not None:
+            if prefix_lens.dim() != 1 or cu_seqs.shape != (len(prefix_lens) + 1,):
+                raise ValueError("cu_seqs must be [P + 1] and prefix_lens [P]")
+            named += [("cu_seqs", cu_seqs, torch.int32), ("prefix_lens", prefix_lens, torch.int32)]
+        p = _pointers(dev, named)
+        slopes = p[6] if alibi_slopes is not None else None
+        if scale is None:
+            scale = D ** -0.5
+        stream = _raw_stream(dev) if stream is None else _stream_ptr(stream)
+        head = (self.handle, *p[:5], B, block_table.shape[1], shape[0])
+        if cu_seqs is None:
+            status = self.lib.paged_decode_attn_run_scored(*head, scale, softcap, slopes,
+                                                           int(window), p[5], stream)
+        else:
+            status = self.lib.paged_decode_attn_run_shared_prefix(
+                *head, p[-2], p[-1], len(prefix_lens), scale, softcap, slopes, p[5], stream)
+        if status:
+            _check(self.lib, status)
         return out
 
     def _one_block_scales(self, q, k_cache, v_cache, block_table, context_lens, out, k_scale,

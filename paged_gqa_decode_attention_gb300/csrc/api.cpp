@@ -17,6 +17,7 @@
 
 #include "paged_decode_attn.h"
 #include "pda_internal.h"
+#include "row_attn.h"
 
 namespace {
 
@@ -247,6 +248,23 @@ int encode_q_map(CUtensorMap* m, const void* q, int64_t rows, int D, int group) 
   return PDA_OK;
 }
 
+// A [B, Hq, D] view of q, loaded as boxes of 64 dims x G heads x n sequences with
+// 128-byte swizzle: the rows (sequence, head of the group) of a row tile.
+int encode_q_rows_map(CUtensorMap* m, const void* q, int64_t batch, int Hq, int D, int group, int n) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(PDA_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)batch};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)n};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(q), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(PDA_ECUDA, "cuTensorMapEncodeTiled (q) failed with CUresult " + std::to_string(r));
+  return PDA_OK;
+}
+
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return na && nb && a0 < b0 + nb && b0 < a0 + na;
@@ -322,6 +340,9 @@ struct pda_handle_s {
   int64_t tm_nb = -1;
   alignas(64) CUtensorMap tmap_k;
   alignas(64) CUtensorMap tmap_v;
+  // Row-tiled calls (shared prefixes, capped and biased scores): null where the geometry
+  // has none. They use ws_o and ws_lse too.
+  int* row_plan = nullptr;  // [1 + max_batch][pda::row::kPlanInts]
 };
 
 namespace {
@@ -371,6 +392,27 @@ LaunchShape launch_shape(const pda_handle_s* h, int batch, int max_blocks, int h
     r.ctas = (int)(r.units < INT_MAX ? r.units : INT_MAX);
   }
   return r;
+}
+
+// The TMA descriptors of the caches, kept in the handle for the next call on the same ones.
+int cache_maps(pda_handle h, const void* k_cache, const void* v_cache, int64_t num_blocks) {
+  const pda_config& c = h->cfg;
+  if (h->tm_k != k_cache || h->tm_v != v_cache || h->tm_nb != num_blocks) {
+    int st = encode_cache_map(&h->tmap_k, k_cache, c.num_kv_heads, c.head_dim, c.block_size,
+                              num_blocks, c.kv_fp8 != 0);
+    if (st == PDA_OK)
+      st = encode_cache_map(&h->tmap_v, v_cache, c.num_kv_heads, c.head_dim, c.block_size,
+                            num_blocks, c.kv_fp8 != 0);
+    if (st != PDA_OK) {
+      h->tm_k = h->tm_v = nullptr;
+      h->tm_nb = -1;
+      return st;
+    }
+    h->tm_k = k_cache;
+    h->tm_v = v_cache;
+    h->tm_nb = num_blocks;
+  }
+  return PDA_OK;
 }
 
 // Every run call. block_scales: k_scale and v_scale are [num_blocks, Hkv].
@@ -429,21 +471,8 @@ int run_any(pda_handle h, const void* q, const void* k_cache, const void* v_cach
   DeviceGuard guard(c.device);
   if (guard.err != cudaSuccess) return cuda_fail("cudaSetDevice", guard.err);
 
-  if (h->tm_k != k_cache || h->tm_v != v_cache || h->tm_nb != num_blocks) {
-    int st = encode_cache_map(&h->tmap_k, k_cache, c.num_kv_heads, c.head_dim, c.block_size,
-                              num_blocks, c.kv_fp8 != 0);
-    if (st == PDA_OK)
-      st = encode_cache_map(&h->tmap_v, v_cache, c.num_kv_heads, c.head_dim, c.block_size,
-                            num_blocks, c.kv_fp8 != 0);
-    if (st != PDA_OK) {
-      h->tm_k = h->tm_v = nullptr;
-      h->tm_nb = -1;
-      return st;
-    }
-    h->tm_k = k_cache;
-    h->tm_v = v_cache;
-    h->tm_nb = num_blocks;
-  }
+  int st = cache_maps(h, k_cache, v_cache, num_blocks);
+  if (st != PDA_OK) return st;
 
   const LaunchShape shape =
       launch_shape(h, batch, max_blocks, max_context_len_hint, num_splits, block_scales);
@@ -452,7 +481,7 @@ int run_any(pda_handle h, const void* q, const void* k_cache, const void* v_cach
   if (units > INT_MAX) return fail(PDA_EINVAL, "splits * num_kv_heads * batch exceeds 2^31");
   alignas(64) CUtensorMap tmap_q;
   if (shape.kernel == pda::kPartialTensorCore) {
-    int st = encode_q_map(&tmap_q, q, (int64_t)batch * c.num_q_heads, c.head_dim, h->group);
+    st = encode_q_map(&tmap_q, q, (int64_t)batch * c.num_q_heads, c.head_dim, h->group);
     if (st != PDA_OK) return st;
   } else {
     std::memset(&tmap_q, 0, sizeof tmap_q);
@@ -494,6 +523,97 @@ int run_any(pda_handle h, const void* q, const void* k_cache, const void* v_cach
                                                       : pda::kKv16,
                                       &h->tmap_k, &h->tmap_v, &tmap_q, p, batch, s);
   if (e != cudaSuccess) return cuda_fail("partial kernel launch", e);
+  return PDA_OK;
+}
+
+// The row-tiled calls: decode attention with a cap, a distance bias or a window on the scores,
+// and over shared prefixes (num_prefixes > 0).
+int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cache,
+             const int32_t* block_table, const int32_t* context_lens, int batch, int max_blocks,
+             int64_t num_blocks, const int32_t* cu_seqs, const int32_t* prefix_lens,
+             int num_prefixes, float scale, float softcap, const float* alibi_slopes, int window,
+             void* out, void* stream) {
+  if (!h) return fail(PDA_EINVAL, "handle is NULL");
+  const pda_config& c = h->cfg;
+  if (c.kv_fp8) return fail(PDA_EUNSUPPORTED, "this call needs 16-bit K/V caches");
+  if (!h->row_plan) return fail(PDA_EUNSUPPORTED, "this call needs head_dim 64 or 128");
+  if (batch < 0 || batch > c.max_batch) return fail(PDA_EINVAL, "batch out of [0, max_batch]");
+  if (batch > pda::row::kMaxBatch) return fail(PDA_EUNSUPPORTED, "this call takes up to 16384 sequences");
+  if (num_prefixes < 0) return fail(PDA_EINVAL, "num_prefixes < 0");
+  if (num_prefixes > pda::row::kMaxPrefixes) return fail(PDA_EUNSUPPORTED, "this call takes up to 192 prefixes");
+  if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
+  if (!std::isfinite(softcap) || softcap < 0.f)
+    return fail(PDA_EINVAL, "softcap must be finite and >= 0 (0: none)");
+  if (softcap > 0.f && !std::isfinite(scale / softcap))
+    return fail(PDA_EINVAL, "scale / softcap is not finite");
+  if (window < 0) return fail(PDA_EINVAL, "window < 0 (0: none)");
+  if (batch == 0) return PDA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !context_lens || !out)
+    return fail(PDA_EINVAL, "a tensor pointer is NULL");
+  if (num_prefixes > 0 && (!cu_seqs || !prefix_lens))
+    return fail(PDA_EINVAL, "cu_seqs and prefix_lens must be given with prefixes");
+  if (max_blocks < 1 || max_blocks > c.max_blocks_per_seq)
+    return fail(PDA_EINVAL, "max_blocks out of [1, max_blocks_per_seq]");
+  if (num_blocks < 1 || num_blocks > INT_MAX / c.block_size)
+    return fail(PDA_EINVAL, "num_blocks * block_size must be in [1, 2^31)");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return fail(PDA_EINVAL, "q, k_cache, v_cache and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(context_lens) |
+       reinterpret_cast<uintptr_t>(cu_seqs) | reinterpret_cast<uintptr_t>(prefix_lens) |
+       reinterpret_cast<uintptr_t>(alibi_slopes)) & 3u)
+    return fail(PDA_EINVAL, "block_table, context_lens, cu_seqs, prefix_lens and alibi_slopes must be 4-byte aligned");
+  // chunks of 128 tokens that the kernel counts in 32 bits: every sequence's own, and every
+  // group's (at most one row tile a sequence)
+  const int64_t chunks = ((int64_t)max_blocks * c.block_size + pda::row::kT - 1) / pda::row::kT;
+  if (2 * (int64_t)batch * c.num_kv_heads * chunks > INT_MAX)
+    return fail(PDA_EINVAL, "batch * num_kv_heads * max_blocks is too large for this call");
+  const size_t n_q = (size_t)batch * c.num_q_heads * c.head_dim;
+  const size_t cache_bytes = (size_t)num_blocks * c.block_size * c.num_kv_heads * c.head_dim * 2;
+  if (overlaps(out, n_q * 2, q, n_q * 2) || overlaps(out, n_q * 2, k_cache, cache_bytes) ||
+      overlaps(out, n_q * 2, v_cache, cache_bytes) ||
+      overlaps(out, n_q * 2, block_table, (size_t)batch * max_blocks * 4) ||
+      overlaps(out, n_q * 2, context_lens, (size_t)batch * 4) ||
+      (num_prefixes > 0 && (overlaps(out, n_q * 2, cu_seqs, ((size_t)num_prefixes + 1) * 4) ||
+                            overlaps(out, n_q * 2, prefix_lens, (size_t)num_prefixes * 4))) ||
+      (alibi_slopes && overlaps(out, n_q * 2, alibi_slopes, (size_t)c.num_q_heads * 4)))
+    return fail(PDA_EALIAS, "out overlaps an input");
+
+  DeviceGuard guard(c.device);
+  if (guard.err != cudaSuccess) return cuda_fail("cudaSetDevice", guard.err);
+  int st = cache_maps(h, k_cache, v_cache, num_blocks);
+  alignas(64) CUtensorMap tmap_q, tmap_q1;
+  if (st == PDA_OK)
+    st = encode_q_rows_map(&tmap_q, q, batch, c.num_q_heads, c.head_dim, h->group,
+                           pda::row::kT / h->group);
+  if (st == PDA_OK)
+    st = encode_q_rows_map(&tmap_q1, q, batch, c.num_q_heads, c.head_dim, h->group, 1);
+  if (st != PDA_OK) return st;
+  pda::row::Params p = {};
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.cu_seqs = cu_seqs;
+  p.prefix_lens = prefix_lens;
+  p.slopes = alibi_slopes;
+  p.out = out;
+  p.ws_o = h->ws_o;
+  p.ws_lse = h->ws_lse;
+  p.plan = h->row_plan;
+  p.err = h->err;
+  p.B = batch;
+  p.P = num_prefixes;
+  p.Hq = c.num_q_heads;
+  p.Hkv = c.num_kv_heads;
+  p.G = h->group;
+  p.max_blocks = max_blocks;
+  p.block_size = c.block_size;
+  p.num_blocks = num_blocks;
+  p.window = window;
+  p.qscale = scale * pda::kLog2e;
+  p.cap = softcap;
+  p.cap_in = softcap > 0.f ? scale / softcap : 0.f;
+  const cudaError_t e = pda::row::launch(c.head_dim, c.dtype, h->tmap_k, h->tmap_v, tmap_q, tmap_q1, p,
+                                         h->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("row-tiled kernel launch", e);
   return PDA_OK;
 }
 
@@ -579,13 +699,26 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
         pda::partial_ctas_per_sm_hint(pda::kPartialCudaCore, h->group, cfg->head_dim);
     h->cc_ctas_per_sm = occ_cc < hint_cc ? occ_cc : hint_cc;
   }
-  const size_t rows = (size_t)cfg->max_batch * cfg->num_q_heads * cfg->max_splits;
+  size_t rows = (size_t)cfg->max_batch * cfg->num_q_heads * cfg->max_splits;
+  const bool row_calls = !kv8 && pda::row::supported(h->group, cfg->head_dim);
+  if (row_calls) {
+    e = pda::row::prepare(cfg->head_dim, cfg->dtype);
+    if (e != cudaSuccess) {
+      delete h;
+      return cuda_fail("cudaFuncSetAttribute", e);
+    }
+    const int most = cfg->max_batch < pda::row::kMaxBatch ? cfg->max_batch : pda::row::kMaxBatch;
+    const size_t need = (size_t)pda::row::workspace_rows(most, cfg->num_q_heads, h->group, h->num_sms);
+    if (need > rows) rows = need;
+  }
   const size_t o_bytes = rows * cfg->head_dim * sizeof(float);
   const size_t lse_bytes = ((rows * sizeof(float)) + 255) & ~size_t(255);
   const size_t err_bytes = 256;
   // split tickets [max_batch, Hkv], then the persistent kernel's 2 counters
   h->counter_bytes = ((size_t)cfg->max_batch * cfg->num_kv_heads + 2) * sizeof(int);
-  e = cudaMalloc(&h->ws, o_bytes + lse_bytes + err_bytes + h->counter_bytes);
+  const size_t plan_off = (o_bytes + lse_bytes + err_bytes + h->counter_bytes + 31) & ~size_t(31);
+  const size_t plan_bytes = row_calls ? ((size_t)cfg->max_batch + 1) * pda::row::kPlanInts * sizeof(int) : 0;
+  e = cudaMalloc(&h->ws, plan_off + plan_bytes);
   if (e != cudaSuccess) {
     delete h;
     cudaGetLastError();
@@ -595,6 +728,7 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
   h->ws_lse = reinterpret_cast<float*>(static_cast<char*>(h->ws) + o_bytes);
   h->err = reinterpret_cast<int*>(static_cast<char*>(h->ws) + o_bytes + lse_bytes);
   h->counters = reinterpret_cast<int*>(static_cast<char*>(h->ws) + o_bytes + lse_bytes + err_bytes);
+  if (row_calls) h->row_plan = reinterpret_cast<int*>(static_cast<char*>(h->ws) + plan_off);
   e = cudaMemset(h->err, 0, err_bytes + h->counter_bytes);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
@@ -665,6 +799,26 @@ int paged_decode_attn_run_block_scaled(pda_handle h, const void* q, const void* 
   return run_any(h, q, k_cache, v_cache, block_table, context_lens, batch, max_blocks, num_blocks,
                  scale, k_scale, v_scale, 0, true, out, stream, num_splits, max_context_len_hint,
                  out_dtype);
+}
+
+int paged_decode_attn_run_scored(pda_handle h, const void* q, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_table,
+                                 const int32_t* context_lens, int batch, int max_blocks,
+                                 int64_t num_blocks, float scale, float softcap,
+                                 const float* alibi_slopes, int window, void* out, void* stream) {
+  return run_rows(h, q, k_cache, v_cache, block_table, context_lens, batch, max_blocks, num_blocks,
+                  nullptr, nullptr, 0, scale, softcap, alibi_slopes, window, out, stream);
+}
+
+int paged_decode_attn_run_shared_prefix(pda_handle h, const void* q, const void* k_cache,
+                                        const void* v_cache, const int32_t* block_table,
+                                        const int32_t* context_lens, int batch, int max_blocks,
+                                        int64_t num_blocks, const int32_t* cu_seqs,
+                                        const int32_t* prefix_lens, int num_prefixes, float scale,
+                                        float softcap, const float* alibi_slopes, void* out,
+                                        void* stream) {
+  return run_rows(h, q, k_cache, v_cache, block_table, context_lens, batch, max_blocks, num_blocks,
+                  cu_seqs, prefix_lens, num_prefixes, scale, softcap, alibi_slopes, 0, out, stream);
 }
 
 int paged_decode_attn_run(pda_handle h, const void* q, const void* k_cache, const void* v_cache,

@@ -21,6 +21,7 @@ enum DeviceError : int {
   kErrWaitTimeout = 3,
   kErrPosition = 4,  // RoPE + KV write: position outside the cos/sin table
   kErrSlot = 5,      // RoPE + KV write: slot beyond the cache
+  kErrCuSeqs = 6,    // shared prefixes: cu_seqs not ascending within the batch
 };
 
 struct PartialParams {

@@ -1,0 +1,55 @@
+// Launch boundary of the row-tiled decode-attention kernel (row_attn_kernel.cuh) and
+// its merge: shared prefixes, capped and biased scores.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace pda {
+namespace row {
+
+constexpr int kT = 128;             // tokens of a chunk, and query rows of a tile
+constexpr int kMaxPrefixes = 192;   // prefix groups a call may have
+constexpr int kMaxBatch = 16384;    // sequences a call may have
+constexpr int kPlanInts = 8;        // plan entry of a sequence (SeqPlan)
+
+struct Params {
+  const int32_t* block_table;   // [B, max_blocks]
+  const int32_t* context_lens;  // [B]
+  const int32_t* cu_seqs;       // [P + 1], P = 0: none
+  const int32_t* prefix_lens;   // [P]
+  const float* slopes;          // [Hq] distance bias per token and head, or null
+  void* out;                    // [B, Hq, D]
+  float* ws_o;                  // partial rows (normalised outputs), D floats each
+  float* ws_lse;                // and their log-sum-exps, base 2
+  int* plan;                    // [1 + ...]: chunks per CTA; then SeqPlan of each sequence
+  int* err;
+  int B, P, Hq, Hkv, G, max_blocks, block_size;
+  int64_t num_blocks;
+  int window;      // > 0: only the last `window` tokens
+  float qscale;    // scale * log2(e)
+  float cap;       // > 0: cap on the scores (natural units)
+  float cap_in;    // scale / cap
+};
+
+// Rows of partials a call of `batch` sequences may need on `ctas` CTAs.
+inline int64_t workspace_rows(int64_t batch, int num_q_heads, int group, int ctas) {
+  const int64_t rows = batch * group < kT ? batch * group : kT;
+  return 4 * batch * num_q_heads + 2 * rows * ctas;
+}
+
+// 16-bit K/V, head dim 64 or 128, any group size up to 16.
+inline bool supported(int group, int head_dim) {
+  return group >= 1 && group <= 16 && (head_dim == 64 || head_dim == 128);
+}
+
+cudaError_t prepare(int head_dim, int dtype);
+// tmap_q: boxes of kT / G sequences' G rows; tmap_q1: of one sequence's.
+cudaError_t launch(int head_dim, int dtype, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                   const CUtensorMap& tmap_q, const CUtensorMap& tmap_q1, const Params& p,
+                   int num_sms, cudaStream_t stream);
+
+}  // namespace row
+}  // namespace pda

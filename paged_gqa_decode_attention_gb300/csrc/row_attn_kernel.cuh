@@ -1,0 +1,846 @@
+// Decode attention with query rows as the M side of the tensor-core tiles: for batches
+// that share a prefix, and for capped, biased or windowed scores.
+//
+// For query row r = (sequence b, head) of kv head h, over the tokens t of b's context:
+//   s_t = scale * q_r . k_t;  s_t = c tanh(s_t / c) with a cap c;  s_t += slope (t - (L_b - 1))
+//   out_r = sum_t softmax_t(s) v_t,  tokens t < L_b - window masked.
+// Sequences of one group hold the same blocks for their first tokens, so those tokens'
+// K/V serve rows = sequences x G query rows of a kv head at once (G: query heads per kv
+// head) and are read once for up to 256 of them. An item is
+//   (group, kv head, tile of 256 rows) over the group's shared pages, or
+//   (sequence, kv head) over the sequence's own pages,
+// and consists of chunks of 128 tokens. All chunks of all items in a row are cut into one
+// equal range per CTA (every CTA computes the same cuts from the lengths, so there is no
+// work queue and the load is even whatever the lengths); the part of an item in one CTA is
+// a segment, which leaves a normalised partial output and its log-sum-exp per row, and a
+// second small launch merges a row's partials.
+//
+// Inside a CTA two pipes, each a softmax warpgroup with one TMEM score tile S (128 rows x
+// 128 tokens, fp32), whose columns then hold the weights P (16 bits), and one output tile O:
+//   S = Q . K^T  (Q 128 x D from shared memory, K chunk 128 x D)       tcgen05 kind::f16
+//   O += P . V   (P from TMEM, V chunk as an MN-major operand)
+// A wide segment (more than 128 rows) gives each pipe one of its two row tiles, and both
+// read every chunk; in a narrow one the pipes take alternate chunks. The tensor pipe works
+// for one pipe while the other's warpgroup does its softmax: QK^T of step n + 1 is issued
+// before PV of step n. One thread owns one row, so maxima and sums need no exchange. The
+// running maximum is only followed when it grows by more than a threshold (2^8 in bf16,
+// 2 in fp16), which spares nearly every rescaling of O; the final division makes up for it.
+// In a wide segment P is rounded to 16 bits once: a weight is off by at most 2^-8 (bf16) or
+// 2^-11 (fp16) of itself, as much as the output's own rounding, and the denominator adds
+// the rounded weights, so that they still sum to one and an error is only ever relative to
+// v_t - out. In a narrow one, which waits for memory, P is the sum of two 16-bit terms
+// (16 or 22 significant bits) and PV takes twice the MMAs. fp16 weights carry a factor 2^14,
+// so that weights down to 2^-28 of the running maximum keep all their bits.
+//
+// Warps 0-3 and 4-7: the pipes. Warp 8: page loads (TMA) into a ring of K and V slots, the
+// walk over segments. Warp 9: TMEM, both MMAs. Every wait is bounded.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "pda_internal.h"
+#include "ptx.cuh"
+#include "row_attn.h"
+
+namespace pda {
+namespace row {
+
+constexpr int kThreads = 320;
+constexpr int kWarpLoad = 8;
+constexpr int kWarpMma = 9;
+constexpr int kHalf = kT * 128;   // 64 dims of 128 rows: 16 KiB
+constexpr int kSegRing = 4;
+constexpr int kSegInts = 12;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr uint32_t kTmemCols = 512;
+
+// What the merge needs to know of a sequence.
+struct SeqPlan {
+  int pre_start;   // first chunk of its tile's item of kv head 0 in its group, in the row of all chunks
+  int pre_stride;  // chunks from one kv head's item to the next one's
+  int pre_n;       // chunks of the shared part (0: none)
+  int pre_row;     // row of its first query head in the item (tile 1 from kT on), + kWide if wide
+  int own_start;   // first chunk of its own part's item of kv head 0
+  int own_n;       // chunks of its own part
+  int pad0, pad1;
+};
+static_assert(sizeof(SeqPlan) == kPlanInts * 4, "plan entry");
+constexpr int kWide = 1 << 16;
+
+// Partial rows in the workspace: [B * Hq][2] of the segments that start a shared item (by
+// pipe, or entry 0 for a wide one), [B * Hq][2] of those that start an own item, then per
+// CTA 2 * cap rows of the one segment that continues another CTA's item.
+__device__ __forceinline__ int64_t ws_first(const Params& p, bool own, int64_t row, int pipe) {
+  return ((own ? (int64_t)p.B * p.Hq : 0) + row) * 2 + pipe;
+}
+__device__ __forceinline__ int64_t ws_next(const Params& p, int cta, int cap, int tile, int r) {
+  return 4 * (int64_t)p.B * p.Hq + (int64_t)cta * 2 * cap + tile * cap + r;
+}
+__device__ __forceinline__ int ws_cap(const Params& p) { return min(kT, p.B * p.G); }
+
+template <int D>
+struct Layout {
+  static constexpr int kTile = kT * D * 2;                // Q tile, K or V chunk
+  static constexpr int kSlots = D == 128 ? 5 : 10;        // K and V slots, 160 KiB
+  static constexpr int kOffQ = kSlots * kTile;
+  static constexpr int kOffBar = kOffQ + 2 * kTile;
+  static constexpr int kBars = 2 * kSlots + 4 + 2 * kSegRing + 8;
+  static constexpr int kOffTmem = kOffBar + kBars * 8;
+  static constexpr int kOffSeg = kOffTmem + 16;
+  static constexpr int kOffScan = kOffSeg + kSegRing * kSegInts * 4;  // warp sums, start, total
+  static constexpr int kOffCu = kOffScan + 16 * 4;
+  static constexpr int kOffShared = kOffCu + (kMaxPrefixes + 4) * 4;
+  static constexpr int kOffRow = kOffShared + kMaxPrefixes * 4;
+  static constexpr int kBytes = kOffRow + kMaxPrefixes * 4;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+  static_assert((kMaxBatch + kMaxPrefixes) * 4 <= kSlots * kTile, "the plan's sums fit the ring");
+};
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool FP16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if constexpr (FP16) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  } else {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+}
+
+// 32 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Eight consecutive floats (32-byte aligned) in one store.
+__device__ __forceinline__ void store8(float* dst, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ int context_len(const Params& p, int b) {
+  const int L = __ldg(p.context_lens + b);
+  const int64_t most = (int64_t)p.max_blocks * p.block_size;
+  return L < 0 ? 0 : (L > most ? (int)most : L);
+}
+
+// The last prefix group g with cu[g] <= b, if b < cu[g + 1] (else -1).
+__device__ __forceinline__ int group_of(const volatile int* cu, int P, int b) {
+  int lo = 0, hi = P + 1;  // first g with cu[g] > b
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= b) lo = mid + 1; else hi = mid;
+  }
+  return lo >= 1 && lo <= P ? lo - 1 : -1;
+}
+
+// A sequence's own part: its first token and page, and its chunks.
+struct Own {
+  int L, first_tok, first_page, n;
+};
+__device__ __forceinline__ Own own_part(const Params& p, int b, int shared_pages) {
+  Own o;
+  o.L = context_len(p, b);
+  o.first_tok = p.window > 0 && o.L > p.window ? o.L - p.window : 0;
+  o.first_page = o.first_tok / p.block_size;
+  if (shared_pages > 0) {
+    o.first_page = shared_pages;
+    o.first_tok = shared_pages * p.block_size;
+  }
+  const int first = o.first_page * p.block_size;
+  o.n = o.L > first ? (o.L - first + kT - 1) / kT : 0;
+  return o;
+}
+
+struct Seg {
+  int n, wide, b0, n_seq, h, t0, t_end, t_lo, first, own, cc;
+};
+__device__ __forceinline__ void seg_put(volatile int* d, const Seg& s) {
+  d[0] = s.n; d[1] = s.wide; d[2] = s.b0; d[3] = s.n_seq; d[4] = s.h; d[5] = s.t0;
+  d[6] = s.t_end; d[7] = s.t_lo; d[8] = s.first; d[9] = s.own; d[10] = s.cc;
+}
+__device__ __forceinline__ void seg_get(const volatile int* d, Seg& s) {
+  s.n = d[0]; s.wide = d[1]; s.b0 = d[2]; s.n_seq = d[3]; s.h = d[4]; s.t0 = d[5];
+  s.t_end = d[6]; s.t_lo = d[7]; s.first = d[8]; s.own = d[9]; s.cc = d[10];
+}
+
+template <int D, bool FP16, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+    row_attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v,
+                    const __grid_constant__ CUtensorMap tmap_q,
+                    const __grid_constant__ CUtensorMap tmap_q1, const Params p) {
+  using L = Layout<D>;
+  constexpr int NB = D / 64;
+  constexpr int kSlots = L::kSlots;
+  extern __shared__ __align__(1024) uint8_t base[];
+  const uint32_t base_u32 = smem_u32(base);
+  const uint32_t bar0 = base_u32 + L::kOffBar;
+  auto kv_full = [&](int s) { return bar0 + 8u * s; };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (kSlots + s); };
+  auto q_full = [&](int s) { return bar0 + 8u * (2 * kSlots + s); };
+  auto q_empty = [&](int s) { return bar0 + 8u * (2 * kSlots + 2 + s); };
+  auto seg_full = [&](int s) { return bar0 + 8u * (2 * kSlots + 4 + s); };
+  auto seg_empty = [&](int s) { return bar0 + 8u * (2 * kSlots + 4 + kSegRing + s); };
+  auto s_full = [&](int t) { return bar0 + 8u * (2 * kSlots + 4 + 2 * kSegRing + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (2 * kSlots + 6 + 2 * kSegRing + t); };
+  auto o_full = [&](int t) { return bar0 + 8u * (2 * kSlots + 8 + 2 * kSegRing + t); };
+  auto o_free = [&](int t) { return bar0 + 8u * (2 * kSlots + 10 + 2 * kSegRing + t); };
+  volatile int* seg_ring = reinterpret_cast<volatile int*>(base + L::kOffSeg);
+  volatile int* scan = reinterpret_cast<volatile int*>(base + L::kOffScan);
+  volatile int* cu = reinterpret_cast<volatile int*>(base + L::kOffCu);
+  int* shared_pages = reinterpret_cast<int*>(base + L::kOffShared);  // of each group
+  int* shared_row = reinterpret_cast<int*>(base + L::kOffRow);       // a sequence that holds them
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.G, spt = kT / G;  // sequences of a row tile
+  bool failed = false;
+
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 1);
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 4);
+      mbar_init(o_full(s), 1);
+      mbar_init(o_free(s), 4);
+    }
+    for (int s = 0; s < kSegRing; ++s) {
+      mbar_init(seg_full(s), 1);
+      mbar_init(seg_empty(s), 9);
+    }
+    fence_mbar_init();
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+    prefetch_tensormap(&tmap_q);
+    prefetch_tensormap(&tmap_q1);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(base_u32 + L::kOffTmem, kTmemCols);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  if (tid == 0) griddep_launch_dependents();
+
+  // ------------------------------- the plan -------------------------------
+  // Chunks of every element (the groups, then the sequences) and their running sum; the
+  // ring's memory holds them.
+  int P = p.P;
+  int* sum = reinterpret_cast<int*>(base);
+  if (P > 0) {
+    for (int g = tid; g <= P; g += kThreads) cu[g] = __ldg(p.cu_seqs + g);
+    for (int g = tid; g < P; g += kThreads) shared_pages[g] = shared_row[g] = 0x7fffffff;
+    __syncthreads();
+    bool bad = false;
+    for (int g = tid; g < P; g += kThreads) bad |= cu[g] > cu[g + 1];
+    if (tid == 0) bad |= cu[0] < 0 || cu[P] > p.B;
+    if (__syncthreads_or(bad)) {  // no grouping: every sequence reads its own table row
+      P = 0;
+      if (tid == 0 && blockIdx.x == 0 && atomicCAS(p.err, 0, kErrCuSeqs) == 0) p.err[1] = 0;
+    }
+  }
+  if (P > 0) {
+    for (int b = tid; b < p.B; b += kThreads) {
+      // an empty sequence (a padded batch) has no say, and its table row is not read
+      const int g = group_of(cu, P, b), n = context_len(p, b);
+      if (g >= 0 && n > 0) {
+        atomicMin(shared_pages + g, n);
+        atomicMin(shared_row + g, b);
+      }
+    }
+    __syncthreads();
+    for (int g = tid; g < P; g += kThreads) {
+      const int n = min(shared_pages[g], max(0, __ldg(p.prefix_lens + g)));
+      shared_pages[g] = cu[g + 1] - cu[g] > 1 && shared_row[g] < p.B ? n / p.block_size : 0;
+    }
+    __syncthreads();
+  }
+  auto tiles_of = [&](int g) { return (cu[g + 1] - cu[g] + 2 * spt - 1) / (2 * spt); };
+  auto group_chunks = [&](int g) { return (shared_pages[g] * p.block_size + kT - 1) / kT; };
+  auto seq_shared = [&](int b) {
+    const int g = P > 0 ? group_of(cu, P, b) : -1;
+    return g >= 0 ? shared_pages[g] : 0;
+  };
+  const int n_elem = P + p.B;
+  for (int e = tid; e < n_elem; e += kThreads)
+    sum[e] = p.Hkv * (e < P ? tiles_of(e) * group_chunks(e) : own_part(p, e - P, seq_shared(e - P)).n);
+  __syncthreads();
+  const int per_thread = (n_elem + kThreads - 1) / kThreads;
+  const int e0 = min(n_elem, tid * per_thread), e1 = min(n_elem, e0 + per_thread);
+  {
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += sum[e];
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    int at = before + incl - mine;
+    for (int e = e0; e < e1; ++e) {
+      const int n = sum[e];
+      sum[e] = at;
+      at += n;
+    }
+    if (tid == kThreads - 1) scan[10] = at;
+    __syncthreads();
+  }
+  const int total = scan[10];
+  const int per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int r0 = min((int64_t)total, (int64_t)blockIdx.x * per);
+  const int r1 = min(total, r0 + per);
+  // the element that holds chunk r0
+  for (int e = e0; e < e1; ++e) {
+    const int next = e + 1 < n_elem ? sum[e + 1] : total;
+    if (r0 >= sum[e] && r0 < next) {
+      scan[11] = e;
+      scan[12] = r0 - sum[e];
+    }
+  }
+  if (blockIdx.x == 0) {  // for the merge
+    if (tid == 0) p.plan[0] = per;
+    SeqPlan* plan = reinterpret_cast<SeqPlan*>(p.plan + kPlanInts);
+    for (int b = tid; b < p.B; b += kThreads) {
+      SeqPlan s = {};
+      const int g = P > 0 ? group_of(cu, P, b) : -1;
+      if (g >= 0 && shared_pages[g] > 0 && context_len(p, b) > 0) {
+        const int i = b - cu[g], tile = i / (2 * spt), r = i - tile * 2 * spt;
+        const int n_seq = min(2 * spt, cu[g + 1] - cu[g] - tile * 2 * spt);
+        s.pre_n = group_chunks(g);
+        s.pre_start = sum[g] + tile * s.pre_n;
+        s.pre_stride = tiles_of(g) * s.pre_n;
+        s.pre_row = (r >= spt ? kT + (r - spt) * G : r * G) + (n_seq > spt ? kWide : 0);
+      }
+      s.own_start = sum[P + b];
+      s.own_n = own_part(p, b, g >= 0 ? shared_pages[g] : 0).n;
+      plan[b] = s;
+    }
+  }
+  fence_proxy_async_smem();  // the ring's memory goes to the TMA unit
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::kOffTmem);
+  auto tS = [&](int t) { return tmem + (uint32_t)(t * kT); };
+  auto tO = [&](int t) { return tmem + (uint32_t)(2 * kT + t * D); };
+
+  if (r0 < r1) {
+    if (warp == kWarpLoad) {
+      // ------------------------- segments and loads -------------------------
+      const int PPS = kT / p.block_size;
+      const int out_of_range = (int)(p.num_blocks * p.block_size);  // rows there read as zeros
+      int e = scan[11], off = scan[12];
+      int fill = 0, qfill = 0, k = 0, cc = 0, left = r1 - r0;
+      int n_item, shared = 0;
+      Own own = {};
+      auto load_elem = [&]() {  // n_item and the like of element e
+        if (e < P) {
+          n_item = group_chunks(e);
+        } else {
+          shared = seq_shared(e - P);
+          own = own_part(p, e - P, shared);
+          n_item = own.n;
+        }
+      };
+      load_elem();
+      int item = off / n_item, chunk = off - item * n_item;  // item: (h, tile) of a group, h of a sequence
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity);
+        if (!__all_sync(kFull, ok)) failed = true;
+        return !failed;
+      };
+      auto publish = [&](const Seg& s) {
+        const int slot = k % kSegRing;
+        if (k >= kSegRing && !wait(seg_empty(slot), (k / kSegRing - 1) & 1)) return false;
+        if (lane == 0) {
+          seg_put(seg_ring + slot * kSegInts, s);
+          mbar_arrive(seg_full(slot));
+        }
+        __syncwarp();
+        ++k;
+        return true;
+      };
+      while (left > 0 && !failed) {
+        const bool is_own = e >= P;
+        const int n = min(left, n_item - chunk);
+        Seg s;
+        s.n = n;
+        s.cc = cc;
+        s.first = chunk == 0;
+        s.own = is_own;
+        int page, page_end, n_items;
+        if (is_own) {
+          s.b0 = e - P;
+          s.n_seq = 1;
+          s.h = item;
+          s.t_end = own.L;
+          s.t_lo = own.first_tok;
+          page = own.first_page;
+          page_end = (own.L + p.block_size - 1) / p.block_size;
+          n_items = p.Hkv;
+        } else {
+          const int tiles = tiles_of(e);
+          s.h = item / tiles;
+          const int tile = item - s.h * tiles;
+          s.b0 = cu[e] + tile * 2 * spt;
+          s.n_seq = min(2 * spt, cu[e + 1] - s.b0);
+          s.t_end = shared_pages[e] * p.block_size;
+          s.t_lo = 0;
+          page = 0;
+          page_end = shared_pages[e];
+          n_items = p.Hkv * tiles;
+        }
+        s.wide = s.n_seq > spt;
+        page += chunk * PPS;
+        s.t0 = page * p.block_size;
+        if (!publish(s)) break;
+        const int32_t* table = p.block_table + (int64_t)(is_own ? e - P : shared_row[e]) * p.max_blocks;
+        const int my_page = lane % PPS, my_half = lane / PPS;  // PPS * NB <= 32: a box per lane
+        int id = page + my_page < page_end ? __ldg(table + page + my_page) : 0;
+        // the queries
+        for (int t = 0; t <= s.wide; ++t, ++qfill) {
+          const int slot = qfill & 1;
+          if (qfill >= 2 && !wait(q_empty(slot), ((qfill >> 1) - 1) & 1)) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full(slot), (uint32_t)((is_own ? 1 : spt) * G * 128 * NB));
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+              tma_load_3d(base_u32 + L::kOffQ + slot * L::kTile + i * kHalf,
+                          is_own ? &tmap_q1 : &tmap_q, i * 64, s.h * G, s.b0 + t * spt,
+                          q_full(slot));
+          }
+          __syncwarp();
+        }
+        if (failed) break;
+        for (int c = 0; c < n; ++c) {
+          const int np = min(PPS, page_end - page);
+          const int row = (unsigned)id < (unsigned long long)p.num_blocks ? id * p.block_size : out_of_range;
+          page += PPS;
+          if (c + 1 < n) id = page + my_page < page_end ? __ldg(table + page + my_page) : 0;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = fill % kSlots;
+            if (fill >= kSlots && !wait(kv_empty(slot), (fill / kSlots - 1) & 1)) break;
+            if (lane == 0)
+              mbar_arrive_expect_tx(kv_full(slot), (uint32_t)(np * p.block_size * 128 * NB));
+            __syncwarp();
+            if (my_page < np && my_half < NB)
+              tma_load_2d(base_u32 + slot * L::kTile + my_half * kHalf + my_page * p.block_size * 128,
+                          kv ? &tmap_v : &tmap_k, s.h * D + my_half * 64, row, kv_full(slot));
+            ++fill;
+          }
+          if (failed) break;
+        }
+        cc += n;
+        left -= n;
+        chunk = 0;
+        if (left > 0 && ++item == n_items) {
+          item = 0;
+          do { ++e; load_elem(); } while (n_item == 0);
+        }
+      }
+      Seg end = {};
+      if (!failed) publish(end);
+      // no copy or MMA may be in flight when the CTA exits: wait for the last releases
+      for (int i = max(0, fill - kSlots); i < fill && !failed; ++i) wait(kv_empty(i % kSlots), (i / kSlots) & 1);
+      for (int i = max(0, qfill - 2); i < qfill && !failed; ++i) wait(q_empty(i & 1), (i >> 1) & 1);
+    } else if (warp == kWarpMma) {
+      // -------------------------------- MMAs --------------------------------
+      constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
+      struct Step {
+        int t, cc, qslot;
+        bool start, last;      // first and last step of pipe t in the segment
+        bool q_wait, q_done;   // first and last use of the Q tile
+        bool kv_done;          // last use of the chunk
+        bool two;              // P has two terms
+        uint32_t qphase;
+      };
+      Seg s = {};
+      int i = 0, t = 0, k = 0, qfill = 0, q_used = 0;
+      int steps[2] = {0, 0}, outs[2] = {0, 0};  // steps and segments of each pipe
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity);
+        if (!__all_sync(kFull, ok)) failed = true;
+        return !failed;
+      };
+      auto next = [&](Step& st) {
+        if (i == s.n) {  // the next segment
+          qfill += q_used;
+          const int slot = k % kSegRing;
+          if (!wait(seg_full(slot), (k / kSegRing) & 1)) return false;
+          seg_get(seg_ring + slot * kSegInts, s);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(seg_empty(slot));
+          ++k;
+          i = t = 0;
+          q_used = s.wide ? 2 : 1;
+          if (s.n == 0) return false;
+        }
+        st.cc = s.cc + i;
+        st.t = s.wide ? t : st.cc & 1;
+        st.start = s.wide ? i == 0 : i < 2;
+        st.last = s.wide ? i == s.n - 1 : i >= s.n - 2;
+        const int q = qfill + (s.wide ? t : 0);
+        st.qslot = q & 1;
+        st.qphase = (q >> 1) & 1;
+        st.q_wait = i == 0;
+        st.q_done = i == s.n - 1;
+        st.kv_done = !s.wide || t == 1;
+        st.two = !s.wide;
+        if (s.wide && t == 0) {
+          t = 1;
+        } else {
+          t = 0;
+          ++i;
+        }
+        return true;
+      };
+      auto issue_qk = [&](const Step& st) {
+        const int slot = (2 * st.cc) % kSlots;
+        if (st.q_wait && !wait(q_full(st.qslot), st.qphase)) return;
+        if (!wait(kv_full(slot), (2 * st.cc / kSlots) & 1)) return;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t qa = base_u32 + L::kOffQ + st.qslot * L::kTile, kb = base_u32 + slot * L::kTile;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            const uint32_t o = (d >> 2) * kHalf + (d & 3) * 32;
+            mma_f16_ss(tS(st.t), sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(kb + o, 16, 1024), idesc_qk,
+                       d > 0 ? 1u : 0u);
+          }
+          mma_commit(s_full(st.t));
+          if (st.kv_done) mma_commit(kv_empty(slot));
+          if (st.q_done) mma_commit(q_empty(st.qslot));
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](const Step& st) {
+        const int f = 2 * st.cc + 1, slot = f % kSlots;
+        if (!wait(kv_full(slot), (f / kSlots) & 1)) return;
+        if (st.start) {
+          if (outs[st.t] > 0 && !wait(o_free(st.t), (outs[st.t] - 1) & 1)) return;
+          ++outs[st.t];
+        }
+        if (!wait(p_full(st.t), steps[st.t]++ & 1)) return;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t vb = base_u32 + slot * L::kTile;
+#pragma unroll
+          for (int j = 0; j < kT / 16; ++j)
+            mma_f16_ts(tO(st.t), tS(st.t) + j * 8, sdesc_sw128(vb + j * 2048, kHalf, 1024), idesc_pv,
+                       st.start && j == 0 ? 0u : 1u);
+          if (st.two) {
+#pragma unroll
+            for (int j = 0; j < kT / 16; ++j)
+              mma_f16_ts(tO(st.t), tS(st.t) + kT / 2 + j * 8, sdesc_sw128(vb + j * 2048, kHalf, 1024),
+                         idesc_pv, 1u);
+          }
+          if (st.last) mma_commit(o_full(st.t));
+          if (st.kv_done) mma_commit(kv_empty(slot));
+        }
+        __syncwarp();
+      };
+      Step st, pend;
+      bool have = false;
+      while (!failed && next(st)) {
+        issue_qk(st);
+        if (have && !failed) issue_pv(pend);
+        pend = st;
+        have = true;
+      }
+      if (have && !failed) issue_pv(pend);
+    } else {
+      // ------------------------------- softmax -------------------------------
+      const int t = warp >> 2, wq = warp & 3;
+      const int r = wq * 32 + lane;  // row of the tile, and token row that this thread clears
+      const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+      const uint32_t s_addr = tS(t) + lane_base, o_addr = tO(t) + lane_base;
+      constexpr float kGrow = FP16 ? 1.f : 8.f;     // log2 of the growth that is let pass
+      constexpr float kShift = FP16 ? 14.f : 0.f;   // log2 of the weights' factor
+      const int cap_rows = ws_cap(p);
+      int steps = 0, outs = 0;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity);
+        if (!__all_sync(kFull, ok)) failed = true;
+        return !failed;
+      };
+      for (int k = 0; !failed; ++k) {
+        Seg s;
+        if (!wait(seg_full(k % kSegRing), (k / kSegRing) & 1)) break;
+        seg_get(seg_ring + (k % kSegRing) * kSegInts, s);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty(k % kSegRing));
+        if (s.n == 0) break;
+        const int n_rows = (s.wide ? (t ? s.n_seq - spt : spt) : s.n_seq) * G;
+        const bool row_ok = r < n_rows, warp_ok = wq * 32 < n_rows;
+        const int rs = r / G, b = s.b0 + (s.wide && t ? spt : 0) + rs, hq = s.h * G + r - rs * G;
+        float m = -INFINITY, l = 0.f;  // running maximum (base 2), sum of the weights
+        [[maybe_unused]] float slope = 0.f, far0 = 0.f;
+        if constexpr (MOD) {
+          if (p.slopes != nullptr && row_ok) {
+            slope = __ldg(p.slopes + hq) * kLog2e;
+            far0 = (float)(s.t0 - (context_len(p, b) - 1));
+          }
+        }
+        int done = 0;  // steps of this pipe in the segment
+        for (int i = s.wide ? 0 : ((s.cc & 1) ^ t); i < s.n; i += s.wide ? 1 : 2) {
+          const int t0 = s.t0 + i * kT;
+          const int lo = max(0, s.t_lo - t0), hi = min(kT, s.t_end - t0);  // valid tokens of the chunk
+          const bool part = lo > 0 || hi < kT;
+          if (!wait(s_full(t), steps & 1)) break;
+          ++steps;
+          tc_fence_after();
+          if (warp_ok) {
+            float x[kT];
+#pragma unroll
+            for (int j = 0; j < kT / 32; ++j) tmem_ld32(s_addr + j * 32, x + j * 32);
+            tmem_ld_wait();
+            float qs = p.qscale;
+            if (MOD || part) {
+              // scores in base-2 units, masked tokens -inf
+              if constexpr (MOD) {
+                if (p.cap > 0.f && p.cap <= 128.f) {
+                  // c tanh(y) = c - 2 c / (1 + e^2y): off by at most a few 2^-24 c
+                  const float y2 = 2.f * kLog2e * p.cap_in, c = p.cap * kLog2e;
+#pragma unroll
+                  for (int j = 0; j < kT; ++j) {
+                    const float z = ex2_ftz(x[j] * y2) + 1.f;
+                    float rz;
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rz) : "f"(z));
+                    x[j] = fmaf(-2.f * c, rz, c);
+                  }
+                } else if (p.cap > 0.f) {
+                  // a large cap: small arguments by the series of tanh y, off by at most
+                  // 2^-26 y below 1/4
+                  const float c = p.cap * kLog2e;
+#pragma unroll
+                  for (int j = 0; j < kT; ++j) {
+                    const float y = x[j] * p.cap_in, y2 = y * y;
+                    const float series =
+                        fmaf(fmaf(fmaf(fmaf(62.f / 2835.f, y2, -17.f / 315.f), y2, 2.f / 15.f), y2, -1.f / 3.f), y2, 1.f) * y;
+                    float rz;
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rz) : "f"(ex2_ftz(y * (2.f * kLog2e)) + 1.f));
+                    x[j] = c * (fabsf(y) < 0.25f ? series : fmaf(-2.f, rz, 1.f));
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < kT; ++j) x[j] *= qs;
+                }
+                if (p.slopes != nullptr) {
+                  const float f0 = far0 + (float)(i * kT);
+#pragma unroll
+                  for (int j = 0; j < kT; ++j) x[j] = fmaf(slope, f0 + (float)j, x[j]);
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < kT; ++j) x[j] *= qs;
+              }
+              if (part) {
+#pragma unroll
+                for (int j = 0; j < kT; ++j)
+                  if (j < lo || j >= hi) x[j] = -INFINITY;
+              }
+              qs = 1.f;
+            }
+            float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
+            if (qs >= 0.f) {
+#pragma unroll
+              for (int j = 4; j < kT; j += 4) {
+                a0 = fmaxf(a0, x[j]); a1 = fmaxf(a1, x[j + 1]);
+                a2 = fmaxf(a2, x[j + 2]); a3 = fmaxf(a3, x[j + 3]);
+              }
+              a0 = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+            } else {
+#pragma unroll
+              for (int j = 4; j < kT; j += 4) {
+                a0 = fminf(a0, x[j]); a1 = fminf(a1, x[j + 1]);
+                a2 = fminf(a2, x[j + 2]); a3 = fminf(a3, x[j + 3]);
+              }
+              a0 = fminf(fminf(a0, a1), fminf(a2, a3));
+            }
+            const float top = a0 * qs;
+            if (__any_sync(kFull, row_ok && top > m + kGrow)) {
+              const float mn = fmaxf(m, top);
+              const float alpha = m == mn ? 1.f : ex2_ftz(m - mn);
+              m = mn;
+              l *= alpha;
+              if (done > 0) {  // O of the steps before is complete: its MMAs precede this S
+#pragma unroll 1
+                for (int j = 0; j < D / 32; ++j) {
+                  float o[32];
+                  tmem_ld32(o_addr + j * 32, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) o[q] *= alpha;
+                  tmem_st32(o_addr + j * 32, o);
+                }
+              }
+            }
+            const float neg = (m == -INFINITY ? 0.f : -m) + kShift;
+            float l0 = 0.f, l1 = 0.f;
+            auto weights = [&](auto two) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[16], w2[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                  const float p0 = ex2_ftz(fmaf(x[j * 32 + 2 * q], qs, neg));
+                  const float p1 = ex2_ftz(fmaf(x[j * 32 + 2 * q + 1], qs, neg));
+                  w[q] = pack16<FP16>(p0, p1);
+                  const float2 f = unpack16<FP16>(w[q]);
+                  if constexpr (decltype(two)::value) {
+                    w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
+                    l0 += p0;
+                    l1 += p1;
+                  } else {
+                    l0 += f.x;
+                    l1 += f.y;
+                  }
+                }
+                tmem_st16(s_addr + j * 16, w);
+                if constexpr (decltype(two)::value) tmem_st16(s_addr + kT / 2 + j * 16, w2);
+              }
+            };
+            if (s.wide) weights(std::false_type{});
+            else weights(std::true_type{});
+            l += l0 + l1;
+            tmem_st_wait();
+          }
+          if (part && (!s.wide || t == 0)) {
+            // V rows of masked tokens are zeros: 0 times whatever they hold would be no zero
+            const int f = 2 * (s.cc + i) + 1, slot = f % kSlots;
+            if (!wait(kv_full(slot), (f / kSlots) & 1)) break;
+            if (r < lo || r >= hi) {
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  *reinterpret_cast<uint4*>(base + slot * L::kTile + j * kHalf + r * 128 + q * 16) =
+                      make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(t));
+          ++done;
+        }
+        if (failed) break;
+        // the segment's partial of this row
+        const int64_t out_row = (int64_t)b * p.Hq + hq;
+        const int64_t w = s.first ? ws_first(p, s.own, out_row, s.wide ? 0 : t)
+                                  : ws_next(p, blockIdx.x, cap_rows, t, r);
+        if (done == 0) {
+          if (row_ok) p.ws_lse[w] = -INFINITY;
+          continue;
+        }
+        if (!wait(o_full(t), outs & 1)) break;
+        ++outs;
+        tc_fence_after();
+        if (warp_ok) {
+          const float inv = 1.f / l;
+          float* dst = p.ws_o + w * D;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            float o[32];
+            tmem_ld32(o_addr + j * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] *= inv;
+            if (row_ok) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) store8(dst + j * 32 + q, o + q);
+            }
+          }
+          if (row_ok) p.ws_lse[w] = m - kShift + log2f(l);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free(t));
+      }
+    }
+  }
+  if (failed && lane == 0 && atomicCAS(p.err, 0, kErrWaitTimeout) == 0) p.err[1] = blockIdx.x;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace row
+}  // namespace pda

@@ -1,0 +1,50 @@
+// Launch of one (head dim, type) of the row-tiled kernel, in a translation unit of its own.
+#pragma once
+
+#include "row_attn_kernel.cuh"
+
+namespace pda {
+namespace row {
+
+template <int D, bool FP16, bool MOD>
+cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                       const CUtensorMap& tq1, const Params& p, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, row_attn_kernel<D, FP16, MOD>, tk, tv, tq, tq1, p);
+}
+
+template <int D, bool FP16>
+cudaError_t prepare_one() {
+  cudaError_t e = cudaFuncSetAttribute(row_attn_kernel<D, FP16, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(row_attn_kernel<D, FP16, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+  return e;
+}
+
+}  // namespace row
+}  // namespace pda
+
+#define PDA_ROW_ATTN(dt, D, FP16)                                                                \
+  namespace pda {                                                                                \
+  namespace row {                                                                                \
+  cudaError_t prepare_##dt##_d##D() { return prepare_one<D, FP16>(); }                           \
+  cudaError_t launch_##dt##_d##D(const CUtensorMap& tk, const CUtensorMap& tv,                   \
+                                 const CUtensorMap& tq, const CUtensorMap& tq1, const Params& p, \
+                                 int ctas, cudaStream_t s) {                                     \
+    return p.cap > 0.f || p.slopes != nullptr                                                    \
+               ? launch_one<D, FP16, true>(tk, tv, tq, tq1, p, ctas, s)                          \
+               : launch_one<D, FP16, false>(tk, tv, tq, tq1, p, ctas, s);                        \
+  }                                                                                              \
+  }                                                                                              \
+  }
