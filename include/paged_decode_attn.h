@@ -319,6 +319,21 @@ int paged_decode_attn_rope_kv_write(const void* q, int64_t q_token_stride, const
                                     int64_t q_out_token_stride, void* k_cache, void* v_cache,
                                     int64_t num_slots, int* err, int device, void* stream);
 
+/* The same with num_axes (1..4) positions a token (e.g. time, height and width of
+ * image and video tokens): positions is [num_axes, num_tokens], and pair j <
+ * rot_dim / 2 of every head turns by entries j of table row
+ * positions[pair_axis[j]][t]. pair_axis holds rot_dim / 2 bytes in HOST memory, read
+ * before the call returns (sections one after the other, axes in turns, or
+ * any other assignment). A token with a bad position on any axis writes
+ * nothing (code 4 and its index). */
+int paged_decode_attn_rope_axes_kv_write(
+    const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,
+    int64_t v_token_stride, const int32_t* positions, int num_axes, const uint8_t* pair_axis,
+    const int64_t* slot_mapping, const float* cos_sin_cache, int max_position, int rot_dim,
+    int neox_style, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int dtype,
+    void* q_out, int64_t q_out_token_stride, void* k_cache, void* v_cache, int64_t num_slots,
+    int* err, int device, void* stream);
+
 /* KV-cache movement (landing page, "Next boundaries": KV-cache movement -
  * block copy, gather, scatter and compact work for prefix reuse and
  * preemption). Caches are [num_blocks, block_size, Hkv, D] of any element

@@ -10,10 +10,12 @@ from ._binding import (ABI_VERSION, EXPORTS, PDA_BF16, PDA_EALIAS, PDA_ECUDA, PD
                        PDA_EINVAL, PDA_ENOMEM, PDA_EUNSUPPORTED, PDA_F32, PDA_FP16, PDA_OK,
                        Config, PagedDecodeAttention, PDAError, load_library, make_config, merge,
                        plan, rope_kv_write, copy_blocks, gather_kv, scatter_kv, remap_table,
-                       append_kv_fp8, rope_append_kv_fp8, gather_kv_fp8)
+                       append_kv_fp8, rope_append_kv_fp8, gather_kv_fp8, rope_axes_kv_write,
+                       rope_pair_axes)
 
 __all__ = ["ABI_VERSION", "EXPORTS", "PDA_BF16", "PDA_EALIAS", "PDA_ECUDA", "PDA_EDEVICE",
            "PDA_EINVAL", "PDA_ENOMEM", "PDA_EUNSUPPORTED", "PDA_F32", "PDA_FP16", "PDA_OK",
            "Config", "PagedDecodeAttention", "PDAError", "load_library", "make_config", "merge",
            "plan", "rope_kv_write", "copy_blocks", "gather_kv", "scatter_kv", "remap_table",
-           "append_kv_fp8", "rope_append_kv_fp8", "gather_kv_fp8"]
+           "append_kv_fp8", "rope_append_kv_fp8", "gather_kv_fp8", "rope_axes_kv_write",
+           "rope_pair_axes"]

@@ -53,6 +53,7 @@ EXPORTS = [
     "paged_decode_attn_run_block_scaled",
     "paged_decode_attn_run_scored",
     "paged_decode_attn_run_shared_prefix",
+    "paged_decode_attn_rope_axes_kv_write",
 ]
 
 
@@ -141,6 +142,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.paged_decode_attn_gather_kv_fp8.argtypes = [P, P, P, P, I64, I, I, I, P, I, P, P, I, I,
                                                         P, P, I64, I, P, I, P]
         lib.paged_decode_attn_gather_kv_fp8.restype = I
+        lib.paged_decode_attn_rope_axes_kv_write.argtypes = [
+            P, I64, P, I64, P, I64, P, I, ctypes.c_char_p, P, P, I, I, I, I, I, I, I, I, P, I64, P,
+            P, I64, P, I, P]
+        lib.paged_decode_attn_rope_axes_kv_write.restype = I
         lib.paged_decode_attn_run_scored.argtypes = [P, P, P, P, P, P, I, I, I64, F, F, P, I, P, P]
         lib.paged_decode_attn_run_scored.restype = I
         lib.paged_decode_attn_run_shared_prefix.argtypes = [P, P, P, P, P, P, I, I, I64, P, P, I, F,
@@ -520,6 +525,70 @@ def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
         _dev_ptr(v_cache, "v_cache", dt), k_cache.shape[0] * k_cache.shape[1],
         _dev_ptr(err, "err", torch.int32) if err is not None else None, dev,
         _stream_ptr(stream)))
+    return q_out
+
+
+def rope_pair_axes(sections, interleaved: bool = False) -> list[int]:
+    """The axis of each rotary pair: ``sections[a]`` pairs for axis a, one
+    section after the other or, interleaved, the axes in turns (an axis whose
+    section is used up is left out of the following turns)."""
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    return [a for turn in range(max(sections, default=0)) for a, n in enumerate(sections) if turn < n]
+
+
+def rope_axes_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                       slot_mapping: torch.Tensor, cos_sin_cache: torch.Tensor,
+                       k_cache: torch.Tensor, v_cache: torch.Tensor, pair_axis, neox: bool = True,
+                       q_out: torch.Tensor | None = None, err: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """``rope_kv_write`` with several positions a token (time, height and
+    width, say): positions [axes, T] int32 (axes <= 4), and pair j of every
+    head turns by the position on axis pair_axis[j] (rot_dim / 2 integers, see
+    ``rope_pair_axes``). Everything else as in ``rope_kv_write``."""
+    lib = _lib or load_library()
+    dt = q.dtype
+    if dt not in _DT16 or q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be bfloat16 or float16 [tokens, heads, head_dim]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+        raise ValueError("k and v must be [T, Hkv, D] with q's T and D")
+    dev = _cuda_device(k_cache)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or shape[2:] != (Hkv, D):
+        raise ValueError("caches must be [num_blocks, block_size, Hkv, D]")
+    if cos_sin_cache.dim() != 2:
+        raise ValueError("cos_sin_cache must be [max_position, rot_dim]")
+    if positions.dim() != 2 or positions.shape[1] != T or slot_mapping.shape != (T,):
+        raise ValueError("positions must be [axes, T] and slot_mapping [T]")
+    max_pos, rot_dim = cos_sin_cache.shape
+    axes = bytes(pair_axis)
+    if len(axes) != rot_dim // 2:
+        raise ValueError("pair_axis must hold rot_dim / 2 axes")
+    qp, qs = _rows16("q", q, dev, dt)
+    kp, ks = _rows16("k", k, dev, dt)
+    vp, vs = _rows16("v", v, dev, dt)
+    qop, qos = (qp, qs) if q_out is q else _rows16("q_out", q_out, dev, dt)
+    named = [("positions", positions, torch.int32), ("slot_mapping", slot_mapping, torch.int64),
+             ("cos_sin_cache", cos_sin_cache, torch.float32), ("k_cache", k_cache, dt),
+             ("v_cache", v_cache, dt)]
+    if err is not None:
+        if err.numel() < 2:
+            raise ValueError("err must hold two int32 values")
+        named.append(("err", err, torch.int32))
+    p = _pointers(dev, named)
+    status = lib.paged_decode_attn_rope_axes_kv_write(
+        qp, qs, kp, ks, vp, vs, p[0], positions.shape[0], axes, p[1], p[2], max_pos, rot_dim,
+        1 if neox else 0, T, Hq, Hkv, D, _DT16[dt], qop, qos, p[3], p[4], shape[0] * shape[1],
+        p[5] if err is not None else None, dev,
+        _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if status:
+        _check(lib, status)
     return q_out
 
 

@@ -21,6 +21,11 @@
 // (Boldo and Melquiond, "Emulation of FMA and correctly rounded sums: proved
 // algorithms using rounding to odd", 2008), which avoids double rounding.
 //
+// With several position axes (time, height, width of image and video tokens) pair j of a
+// token turns by the angle of its position on axis a_j: its cosine and sine are entries j of
+// table row pos[a_j][t]. An item of 8 pairs on one axis reads one row as above; one whose
+// pairs differ (interleaved axes) reads the 8 entries of every axis in it and selects.
+//
 // Memory-bound: token rows move through shared memory by bulk asynchronous
 // copies (no registers hold data in flight), so a ring of up to six ~16 KB
 // tiles per CTA keeps enough bytes in flight to stream at HBM speed, and a
@@ -56,7 +61,7 @@ struct RopeParams {
   int64_t k_stride;
   int64_t v_stride;
   int64_t qo_stride;
-  const int32_t* positions;  // [T]
+  const int32_t* positions;  // [T], or [axes, T]
   const int64_t* slots;      // [T]
   const float* cos_sin;      // [max_position, rot_dim]
   uint16_t* q_out;
@@ -73,7 +78,23 @@ struct RopeParams {
   int stages;       // ring stages (<= kRopeMaxStages)
   int lag;          // a stage is refilled `lag` tiles after its stores were issued
   int fused;        // q, k, v are consecutive parts of one [T, row_elems] buffer
+  int axes;         // position axes (kAxes kernels)
+  uint64_t pair_axis[64];  // axis of each pair, a byte each; entry u: the pairs of item u
 };
+constexpr int kRopeMaxAxes = 4;
+
+// Position of token t on axis a, and whether all of them are inside the table.
+template <bool kAxes>
+__device__ __forceinline__ bool load_positions(const RopeParams& p, int64_t t, int (&pos)[kRopeMaxAxes]) {
+  bool ok = true;
+#pragma unroll
+  for (int a = 0; a < (kAxes ? kRopeMaxAxes : 1); ++a) {
+    pos[a] = 0;
+    if (!kAxes || a < p.axes) pos[a] = __ldg(p.positions + (int64_t)a * p.T + t);
+    ok &= pos[a] >= 0 && pos[a] < p.max_position;
+  }
+  return ok;
+}
 
 __device__ __forceinline__ int fast_div(int x, uint32_t mul, uint32_t shift) {
   return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
@@ -92,20 +113,45 @@ constexpr int kRopeMaxTileTokens = 32;       // one lane of warp 0 per token
 
 // Rotates the pairs of one 32-byte item in shared memory: angles j = 8u ..
 // 8u + 7 of a head row, elements at offA and offB (16-byte vectors).
-template <typename F, bool kNeox>
-__device__ __forceinline__ void rotate_item(uint16_t* row, const float* cs_row, int half, int u) {
+template <typename F, bool kNeox, bool kAxes>
+__device__ __forceinline__ void rotate_item(uint16_t* row, const RopeParams& p,
+                                            const int (&pos)[kRopeMaxAxes], int half, int u) {
   const int offA = kNeox ? 8 * u : 16 * u;
   const int offB = kNeox ? half + 8 * u : 16 * u + 8;
   uint4* pa = reinterpret_cast<uint4*>(row + offA);
   uint4* pb = reinterpret_cast<uint4*>(row + offB);
   const uint4 A = *pa, B = *pb;
-  const float* cs = cs_row + 8 * u;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs));
-  const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half));
-  const float4 s1 = __ldg(reinterpret_cast<const float4*>(cs + half + 4));
-  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+  float c[8], s[8];
+  auto read = [&](int at, float (&cc)[8], float (&ss)[8]) {
+    const float* cs = p.cos_sin + (int64_t)at * p.rot_dim + 8 * u;
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs));
+    const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half));
+    const float4 s1 = __ldg(reinterpret_cast<const float4*>(cs + half + 4));
+    cc[0] = c0.x, cc[1] = c0.y, cc[2] = c0.z, cc[3] = c0.w;
+    cc[4] = c1.x, cc[5] = c1.y, cc[6] = c1.z, cc[7] = c1.w;
+    ss[0] = s0.x, ss[1] = s0.y, ss[2] = s0.z, ss[3] = s0.w;
+    ss[4] = s1.x, ss[5] = s1.y, ss[6] = s1.z, ss[7] = s1.w;
+  };
+  if constexpr (kAxes) {
+    const uint64_t codes = p.pair_axis[u];
+    const int a0 = (int)(codes & 255);
+    auto pos_of = [&](int a) { return a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3]; };
+    read(pos_of(a0), c, s);
+    if (codes != 0x0101010101010101ull * (uint64_t)a0) {
+      for (int a = 0; a < p.axes; ++a) {
+        if (a == a0) continue;
+        float c1[8], s1[8];
+        read(pos_of(a), c1, s1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if ((int)((codes >> (8 * i)) & 255) == a) c[i] = c1[i], s[i] = s1[i];
+        }
+      }
+    }
+  } else {
+    read(pos[0], c, s);
+  }
   const uint32_t wa[4] = {A.x, A.y, A.z, A.w};
   const uint32_t wb[4] = {B.x, B.y, B.z, B.w};
   uint32_t oa[4], ob[4];
@@ -147,8 +193,8 @@ __device__ __forceinline__ void rotate_item(uint16_t* row, const float* cs_row, 
 //     place, release it. They never wait for stores, so up to
 //     stages - lag tiles of loads stay in flight ahead of the rotation.
 // No block-wide barrier inside the loop; every wait is bounded.
-template <typename F, bool kNeox>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const RopeParams p) {
+template <typename F, bool kNeox, bool kAxes>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* done = full + kRopeMaxStages;
@@ -204,10 +250,11 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const Ro
       }
       const int t0 = first_token(i), nt = tile_len(t0);
       const int64_t t = t0 + lane;
-      int pos = 0;
+      int pos[kRopeMaxAxes];
+      bool pos_ok = false;
       int64_t slot = -1;
       if (lane < nt) {  // in flight while the stage is being rotated
-        pos = __ldg(p.positions + t);
+        pos_ok = load_positions<kAxes>(p, t, pos);
         slot = __ldg(p.slots + t);
       }
       const bool ok = mbar_wait_sleep(smem_u32(&done[s]), (uint32_t)(i / K) & 1u);
@@ -217,7 +264,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const Ro
       }
       if (lane < nt) {
         const uint32_t src = smem_u32(data + s * stage_elems + (int64_t)lane * p.row_elems);
-        if (pos < 0 || pos >= p.max_position) {
+        if (!pos_ok) {
           record_error(p.err, kErrPosition, (int)t);
         } else {
           bulk_store(p.q_out + t * p.qo_stride, src, q_bytes);
@@ -253,18 +300,16 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const Ro
     int rem = tid - j * per_token;
     int cur_j = -1;
     bool valid = false;
-    const float* cs_row = p.cos_sin;
+    int pos[kRopeMaxAxes];
     for (int it = tid; it < nt * per_token; it += kRopeRotThreads) {
       if (j != cur_j) {
         cur_j = j;
-        const int pos = __ldg(p.positions + t0 + j);
-        valid = pos >= 0 && pos < p.max_position;
-        cs_row = p.cos_sin + (int64_t)(valid ? pos : 0) * p.rot_dim;
+        valid = load_positions<kAxes>(p, t0 + j, pos);
       }
       if (valid) {
         const int r = fast_div(rem, p.div_rot_mul, p.div_rot_shift);
-        rotate_item<F, kNeox>(st + (int64_t)j * p.row_elems + r * p.D, cs_row, half,
-                              rem - r * rot_items);
+        rotate_item<F, kNeox, kAxes>(st + (int64_t)j * p.row_elems + r * p.D, p, pos, half,
+                                     rem - r * rot_items);
       }
       rem += kRopeRotThreads;
       while (rem >= per_token) {
@@ -303,8 +348,11 @@ DeviceInfo g_dev[64];
 
 template <typename F, bool kNeox>
 cudaError_t prepare_one(int smem_max) {
-  return cudaFuncSetAttribute(rope_kv_write_kernel<F, kNeox>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
+  const cudaError_t e = cudaFuncSetAttribute(rope_kv_write_kernel<F, kNeox, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(rope_kv_write_kernel<F, kNeox, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
 }
 
 // SM count of `device`, and the kernels' shared-memory limit set once.
@@ -329,13 +377,16 @@ cudaError_t device_info(int device, int* num_sms) {
 }  // namespace
 }  // namespace pda
 
-extern "C" int paged_decode_attn_rope_kv_write(
-    const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,
-    int64_t v_token_stride, const int32_t* positions, const int64_t* slot_mapping,
-    const float* cos_sin_cache, int max_position, int rot_dim, int neox_style, int num_tokens,
-    int num_q_heads, int num_kv_heads, int head_dim, int dtype, void* q_out,
-    int64_t q_out_token_stride, void* k_cache, void* v_cache, int64_t num_slots, int* err,
-    int device, void* stream) {
+namespace {
+
+// Both entry points. num_axes 0: positions [num_tokens], one axis; else [num_axes, num_tokens]
+// and pair_axis (host memory) the axis of each of the rot_dim / 2 pairs.
+int rope_call(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride,
+              const void* v, int64_t v_token_stride, const int32_t* positions, int num_axes,
+              const uint8_t* pair_axis, const int64_t* slot_mapping, const float* cos_sin_cache,
+              int max_position, int rot_dim, int neox_style, int num_tokens, int num_q_heads,
+              int num_kv_heads, int head_dim, int dtype, void* q_out, int64_t q_out_token_stride,
+              void* k_cache, void* v_cache, int64_t num_slots, int* err, int device, void* stream) {
   using pda::fail;
   using pda::Rows;
   if (num_tokens < 0) return fail(PDA_EINVAL, "num_tokens < 0");
@@ -348,6 +399,11 @@ extern "C" int paged_decode_attn_rope_kv_write(
   if (num_slots < 0) return fail(PDA_EINVAL, "num_slots < 0");
   if (max_position < 0) return fail(PDA_EINVAL, "max_position < 0");
   if (device < 0) return fail(PDA_EINVAL, "device must be >= 0");
+  if (num_axes > 0) {
+    if (rot_dim > 0 && !pair_axis) return fail(PDA_EINVAL, "pair_axis is NULL");
+    for (int j = 0; j < rot_dim / 2; ++j)
+      if (pair_axis[j] >= num_axes) return fail(PDA_EINVAL, "pair_axis names an axis that positions does not have");
+  }
   const int64_t hq_d = (int64_t)num_q_heads * head_dim, hkv_d = (int64_t)num_kv_heads * head_dim;
   const int64_t row_elems = hq_d + 2 * hkv_d;
   if (row_elems * 2 > pda::kRopeMaxRowBytes)
@@ -380,7 +436,7 @@ extern "C" int paged_decode_attn_rope_kv_write(
   const Rows rq = rows(q, q_token_stride, hq_d), rk = rows(k, k_token_stride, hkv_d);
   const Rows rv = rows(v, v_token_stride, hkv_d), rqo = rows(q_out, q_out_token_stride, hq_d);
   const Rows rkc = span(k_cache, num_slots * hkv_d * 2), rvc = span(v_cache, num_slots * hkv_d * 2);
-  const Rows rpos = span(positions, T * 4), rslot = span(slot_mapping, T * 8);
+  const Rows rpos = span(positions, T * 4 * (num_axes > 0 ? num_axes : 1)), rslot = span(slot_mapping, T * 8);
   const Rows rcs = span(cos_sin_cache, cos_sin_cache ? (int64_t)max_position * rot_dim * 4 : 0);
   const Rows rerr = span(err, err ? 8 : 0);
   const bool q_in_place = (q == q_out && q_token_stride == q_out_token_stride);
@@ -422,7 +478,7 @@ extern "C" int paged_decode_attn_rope_kv_write(
   const int smem = pda::kRopeDataOff + stages * stage_bytes;
   const int per_sm = std::max(1, std::min(3, 233472 / (smem + 1024)));  // 3 by registers
   const int64_t grid = std::min<int64_t>(num_tiles, (int64_t)num_sms * per_sm);
-  pda::RopeParams p;
+  pda::RopeParams p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
@@ -453,19 +509,58 @@ extern "C" int paged_decode_attn_rope_kv_write(
   p.lag = lag;
   p.fused = (k == p.q + hq_d && v == p.q + hq_d + hkv_d && q_token_stride == row_elems &&
              k_token_stride == row_elems && v_token_stride == row_elems);
+  p.axes = num_axes;
+  for (int j = 0; num_axes > 0 && j < rot_dim / 2; ++j)
+    p.pair_axis[j / 8] |= (uint64_t)pair_axis[j] << (8 * (j % 8));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool neox = neox_style != 0;
+  const bool neox = neox_style != 0, several = num_axes > 0;
   const dim3 g((unsigned)grid), b(pda::kRopeThreads);
+  using pda::Bf16;
+  using pda::Fp16;
   if (dtype == PDA_BF16) {
-    if (neox) pda::rope_kv_write_kernel<pda::Bf16, true><<<g, b, smem, s>>>(p);
-    else pda::rope_kv_write_kernel<pda::Bf16, false><<<g, b, smem, s>>>(p);
+    if (several && neox) pda::rope_kv_write_kernel<Bf16, true, true><<<g, b, smem, s>>>(p);
+    else if (several) pda::rope_kv_write_kernel<Bf16, false, true><<<g, b, smem, s>>>(p);
+    else if (neox) pda::rope_kv_write_kernel<Bf16, true, false><<<g, b, smem, s>>>(p);
+    else pda::rope_kv_write_kernel<Bf16, false, false><<<g, b, smem, s>>>(p);
   } else {
-    if (neox) pda::rope_kv_write_kernel<pda::Fp16, true><<<g, b, smem, s>>>(p);
-    else pda::rope_kv_write_kernel<pda::Fp16, false><<<g, b, smem, s>>>(p);
+    if (several && neox) pda::rope_kv_write_kernel<Fp16, true, true><<<g, b, smem, s>>>(p);
+    else if (several) pda::rope_kv_write_kernel<Fp16, false, true><<<g, b, smem, s>>>(p);
+    else if (neox) pda::rope_kv_write_kernel<Fp16, true, false><<<g, b, smem, s>>>(p);
+    else pda::rope_kv_write_kernel<Fp16, false, false><<<g, b, smem, s>>>(p);
   }
   e = cudaGetLastError();
   if (prev >= 0 && prev != device) cudaSetDevice(prev);
   if (e != cudaSuccess)
     return fail(PDA_ECUDA, std::string("rope_kv_write launch: ") + cudaGetErrorString(e));
   return PDA_OK;
+}
+
+}  // namespace
+
+extern "C" int paged_decode_attn_rope_kv_write(
+    const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,
+    int64_t v_token_stride, const int32_t* positions, const int64_t* slot_mapping,
+    const float* cos_sin_cache, int max_position, int rot_dim, int neox_style, int num_tokens,
+    int num_q_heads, int num_kv_heads, int head_dim, int dtype, void* q_out,
+    int64_t q_out_token_stride, void* k_cache, void* v_cache, int64_t num_slots, int* err,
+    int device, void* stream) {
+  return rope_call(q, q_token_stride, k, k_token_stride, v, v_token_stride, positions, 0, nullptr,
+                   slot_mapping, cos_sin_cache, max_position, rot_dim, neox_style, num_tokens,
+                   num_q_heads, num_kv_heads, head_dim, dtype, q_out, q_out_token_stride, k_cache,
+                   v_cache, num_slots, err, device, stream);
+}
+
+extern "C" int paged_decode_attn_rope_axes_kv_write(
+    const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, const void* v,
+    int64_t v_token_stride, const int32_t* positions, int num_axes, const uint8_t* pair_axis,
+    const int64_t* slot_mapping, const float* cos_sin_cache, int max_position, int rot_dim,
+    int neox_style, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int dtype,
+    void* q_out, int64_t q_out_token_stride, void* k_cache, void* v_cache, int64_t num_slots,
+    int* err, int device, void* stream) {
+  if (num_axes < 1 || num_axes > pda::kRopeMaxAxes)
+    return pda::fail(PDA_EINVAL, "num_axes must be in [1, 4]");
+  return rope_call(q, q_token_stride, k, k_token_stride, v, v_token_stride, positions, num_axes,
+                   pair_axis, slot_mapping, cos_sin_cache, max_position, rot_dim, neox_style,
+                   num_tokens, num_q_heads, num_kv_heads, head_dim, dtype, q_out,
+                   q_out_token_stride, k_cache, v_cache, num_slots, err, device, stream);
 }
