@@ -22,7 +22,7 @@
 // A wide segment (more than 128 rows) gives each pipe one of its two row tiles, and both
 // read every chunk; in a narrow one the pipes take alternate chunks. The tensor pipe works
 // for one pipe while the other's warpgroup does its softmax: QK^T of step n + 1 is issued
-// before PV of step n. One thread owns one row, so maxima and sums need no exchange. The
+// before PV of step n, which belongs to the other pipe. One thread owns one row, so maxima and sums need no exchange. The
 // running maximum is only followed when it grows by more than a threshold (2^8 in bf16,
 // 2 in fp16), which spares nearly every rescaling of O; the final division makes up for it.
 // In a wide segment P is rounded to 16 bits once: a weight is off by at most 2^-8 (bf16) or
@@ -157,6 +157,16 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of the (converged) warp. The compiler knows of elect.sync that a single thread is
+// active, and issues MMAs from uniform registers without a loop around each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], issued by one thread.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
@@ -181,6 +191,70 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]),
                "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+// Pairs of floats in one 64-bit register: one instruction for two fused multiply-adds or sums.
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max32(const float* x) {
+  float a[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int q = 4; q < 32; q += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], x[q + i]);
+  }
+  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+}
+
+// Products q . k of 32 tokens to capped and biased scores in base-2 units; far: the first
+// token's distance from the context's last one (t - (L - 1)).
+__device__ __forceinline__ void score_mods(const Params& p, float* x, float slope, float far) {
+  if (p.cap > 0.f && p.cap <= 128.f) {
+    // c tanh(y) = c - 2 c / (1 + e^2y): off by at most a few 2^-24 c
+    const float y2 = 2.f * kLog2e * p.cap_in, c = p.cap * kLog2e;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_ftz(x[q] * y2) + 1.f));
+      x[q] = fmaf(-2.f * c, r, c);
+    }
+  } else if (p.cap > 0.f) {
+    // a large cap: small arguments by the series of tanh y, off by at most 2^-26 y below 1/4
+    const float c = p.cap * kLog2e;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      const float y = x[q] * p.cap_in, y2 = y * y;
+      const float series =
+          fmaf(fmaf(fmaf(fmaf(62.f / 2835.f, y2, -17.f / 315.f), y2, 2.f / 15.f), y2, -1.f / 3.f), y2, 1.f) * y;
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_ftz(y * (2.f * kLog2e)) + 1.f));
+      x[q] = c * (fabsf(y) < 0.25f ? series : fmaf(-2.f, r, 1.f));
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 32; ++q) x[q] *= p.qscale;
+  }
+  if (p.slopes != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 32; ++q) x[q] = fmaf(slope, far + (float)q, x[q]);
+  }
 }
 
 __device__ __forceinline__ int context_len(const Params& p, int b) {
@@ -219,14 +293,15 @@ __device__ __forceinline__ Own own_part(const Params& p, int b, int shared_pages
 
 struct Seg {
   int n, wide, b0, n_seq, h, t0, t_end, t_lo, first, own, cc;
+  int par;  // pipe of its first step: steps take the pipes in turns, across segments too
 };
 __device__ __forceinline__ void seg_put(volatile int* d, const Seg& s) {
   d[0] = s.n; d[1] = s.wide; d[2] = s.b0; d[3] = s.n_seq; d[4] = s.h; d[5] = s.t0;
-  d[6] = s.t_end; d[7] = s.t_lo; d[8] = s.first; d[9] = s.own; d[10] = s.cc;
+  d[6] = s.t_end; d[7] = s.t_lo; d[8] = s.first; d[9] = s.own; d[10] = s.cc; d[11] = s.par;
 }
 __device__ __forceinline__ void seg_get(const volatile int* d, Seg& s) {
   s.n = d[0]; s.wide = d[1]; s.b0 = d[2]; s.n_seq = d[3]; s.h = d[4]; s.t0 = d[5];
-  s.t_end = d[6]; s.t_lo = d[7]; s.first = d[8]; s.own = d[9]; s.cc = d[10];
+  s.t_end = d[6]; s.t_lo = d[7]; s.first = d[8]; s.own = d[9]; s.cc = d[10]; s.par = d[11];
 }
 
 template <int D, bool FP16, bool MOD>
@@ -256,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* cu = reinterpret_cast<volatile int*>(base + L::kOffCu);
   int* shared_pages = reinterpret_cast<int*>(base + L::kOffShared);  // of each group
   int* shared_row = reinterpret_cast<int*>(base + L::kOffRow);       // a sequence that holds them
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int G = p.G, spt = kT / G;  // sequences of a row tile
   bool failed = false;
 
@@ -392,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::kOffTmem);
+  const uint32_t tmem = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(base + L::kOffTmem), 0);
   auto tS = [&](int t) { return tmem + (uint32_t)(t * kT); };
   auto tO = [&](int t) { return tmem + (uint32_t)(2 * kT + t * D); };
 
@@ -402,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int PPS = kT / p.block_size;
       const int out_of_range = (int)(p.num_blocks * p.block_size);  // rows there read as zeros
       int e = scan[11], off = scan[12];
-      int fill = 0, qfill = 0, k = 0, cc = 0, left = r1 - r0;
+      int fill = 0, qfill = 0, k = 0, cc = 0, par = 0, left = r1 - r0;
       int n_item, shared = 0;
       Own own = {};
       auto load_elem = [&]() {  // n_item and the like of element e
@@ -463,6 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           n_items = p.Hkv * tiles;
         }
         s.wide = s.n_seq > spt;
+        s.par = par;
+        if (!s.wide) par ^= n & 1;
         page += chunk * PPS;
         s.t0 = page * p.block_size;
         if (!publish(s)) break;
@@ -518,110 +595,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, qfill - 2); i < qfill && !failed; ++i) wait(q_empty(i & 1), (i >> 1) & 1);
     } else if (warp == kWarpMma) {
       // -------------------------------- MMAs --------------------------------
-      constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
-      constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
-      struct Step {
-        int t, cc, qslot;
-        bool start, last;      // first and last step of pipe t in the segment
-        bool q_wait, q_done;   // first and last use of the Q tile
-        bool kv_done;          // last use of the chunk
-        bool two;              // P has two terms
-        uint32_t qphase;
-      };
-      Seg s = {};
-      int i = 0, t = 0, k = 0, qfill = 0, q_used = 0;
-      int steps[2] = {0, 0}, outs[2] = {0, 0};  // steps and segments of each pipe
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        const bool ok = mbar_wait(bar, parity);
-        if (!__all_sync(kFull, ok)) failed = true;
-        return !failed;
-      };
-      auto next = [&](Step& st) {
-        if (i == s.n) {  // the next segment
-          qfill += q_used;
-          const int slot = k % kSegRing;
-          if (!wait(seg_full(slot), (k / kSegRing) & 1)) return false;
-          seg_get(seg_ring + slot * kSegInts, s);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(seg_empty(slot));
-          ++k;
-          i = t = 0;
-          q_used = s.wide ? 2 : 1;
-          if (s.n == 0) return false;
-        }
-        st.cc = s.cc + i;
-        st.t = s.wide ? t : st.cc & 1;
-        st.start = s.wide ? i == 0 : i < 2;
-        st.last = s.wide ? i == s.n - 1 : i >= s.n - 2;
-        const int q = qfill + (s.wide ? t : 0);
-        st.qslot = q & 1;
-        st.qphase = (q >> 1) & 1;
-        st.q_wait = i == 0;
-        st.q_done = i == s.n - 1;
-        st.kv_done = !s.wide || t == 1;
-        st.two = !s.wide;
-        if (s.wide && t == 0) {
-          t = 1;
-        } else {
-          t = 0;
-          ++i;
-        }
-        return true;
-      };
-      auto issue_qk = [&](const Step& st) {
-        const int slot = (2 * st.cc) % kSlots;
-        if (st.q_wait && !wait(q_full(st.qslot), st.qphase)) return;
-        if (!wait(kv_full(slot), (2 * st.cc / kSlots) & 1)) return;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t qa = base_u32 + L::kOffQ + st.qslot * L::kTile, kb = base_u32 + slot * L::kTile;
+      // One thread does all of it: what it does between two MMAs the tensor pipe, whose queue
+      // is short, waits for.
+      if (elect_one()) {
+        constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
+        constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
+        // descriptors of the ring's first slot; another place is 16 bytes a unit further
+        const uint64_t k_desc = sdesc_sw128(base_u32, 16, 1024);
+        const uint64_t v_desc = sdesc_sw128(base_u32, kHalf, 1024);
+        const uint64_t q_desc = sdesc_sw128(base_u32 + L::kOffQ, 16, 1024);
+        struct Step {
+          int t, kslot, vslot, qslot;
+          uint32_t kphase, vphase, qphase;
+          bool start, last;      // first and last step of pipe t in the segment
+          bool q_wait, q_done;   // first and last use of the Q tile
+          bool kv_done;          // last use of the chunk
+          bool two;              // P has two terms
+        };
+        Seg s = {};
+        int i = 0, k = 0, qfill = 0, q_used = 0;
+        bool second = false;                      // the next step is a wide chunk's second one
+        int kslot = -2;                           // ring slot of the chunk's K
+        uint32_t kphase = 0;
+        int steps[2] = {0, 0}, outs[2] = {0, 0};  // steps and segments of each pipe
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (!mbar_wait(bar, parity)) failed = true;
+          return !failed;
+        };
+        auto next = [&](Step& st) {
+          if (i == s.n) {  // the next segment
+            qfill += q_used;
+            const int slot = k % kSegRing;
+            if (!wait(seg_full(slot), (k / kSegRing) & 1)) return false;
+            seg_get(seg_ring + slot * kSegInts, s);
+            mbar_arrive(seg_empty(slot));
+            ++k;
+            i = 0;
+            q_used = s.wide ? 2 : 1;
+            if (s.n == 0) return false;
+          }
+          if (!second) {  // a new chunk
+            kslot += 2;
+            if (kslot >= kSlots) {
+              kslot -= kSlots;
+              kphase ^= 1;
+            }
+          }
+          st.t = (s.par + (s.wide ? (second ? 1 : 0) : i)) & 1;
+          st.start = i < (s.wide ? 1 : 2);
+          st.last = i >= s.n - (s.wide ? 1 : 2);
+          const int q = qfill + (s.wide ? st.t : 0);
+          st.qslot = q & 1;
+          st.qphase = (q >> 1) & 1;
+          st.kslot = kslot;
+          st.kphase = kphase;
+          st.vslot = kslot + 1 == kSlots ? 0 : kslot + 1;
+          st.vphase = kslot + 1 == kSlots ? kphase ^ 1 : kphase;
+          st.q_wait = i == 0;
+          st.q_done = i == s.n - 1;
+          st.kv_done = !s.wide || second;
+          st.two = !s.wide;
+          if (s.wide && !second) {
+            second = true;
+          } else {
+            second = false;
+            ++i;
+          }
+          return true;
+        };
+        auto issue_qk = [&](const Step& st) {
+          if (st.q_wait && !wait(q_full(st.qslot), st.qphase)) return;
+          if (!wait(kv_full(st.kslot), st.kphase)) return;
+          tc_fence_after();
+          const uint64_t qa = q_desc + (uint32_t)(st.qslot * (L::kTile >> 4));
+          const uint64_t kb = k_desc + (uint32_t)(st.kslot * (L::kTile >> 4));
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
-            const uint32_t o = (d >> 2) * kHalf + (d & 3) * 32;
-            mma_f16_ss(tS(st.t), sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(kb + o, 16, 1024), idesc_qk,
-                       d > 0 ? 1u : 0u);
+            const uint32_t o = ((d >> 2) * kHalf + (d & 3) * 32) >> 4;
+            mma_f16_ss(tS(st.t), qa + o, kb + o, idesc_qk, d > 0 ? 1u : 0u);
           }
           mma_commit(s_full(st.t));
-          if (st.kv_done) mma_commit(kv_empty(slot));
+          if (st.kv_done) mma_commit(kv_empty(st.kslot));
           if (st.q_done) mma_commit(q_empty(st.qslot));
-        }
-        __syncwarp();
-      };
-      auto issue_pv = [&](const Step& st) {
-        const int f = 2 * st.cc + 1, slot = f % kSlots;
-        if (!wait(kv_full(slot), (f / kSlots) & 1)) return;
-        if (st.start) {
-          if (outs[st.t] > 0 && !wait(o_free(st.t), (outs[st.t] - 1) & 1)) return;
-          ++outs[st.t];
-        }
-        if (!wait(p_full(st.t), steps[st.t]++ & 1)) return;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t vb = base_u32 + slot * L::kTile;
+        };
+        auto issue_pv = [&](const Step& st) {
+          if (!wait(kv_full(st.vslot), st.vphase)) return;
+          if (st.start) {
+            if (outs[st.t] > 0 && !wait(o_free(st.t), (outs[st.t] - 1) & 1)) return;
+            ++outs[st.t];
+          }
+          if (!wait(p_full(st.t), steps[st.t]++ & 1)) return;
+          tc_fence_after();
+          const uint64_t vb = v_desc + (uint32_t)(st.vslot * (L::kTile >> 4));
+          const uint32_t pa = tS(st.t), o = tO(st.t);
 #pragma unroll
           for (int j = 0; j < kT / 16; ++j)
-            mma_f16_ts(tO(st.t), tS(st.t) + j * 8, sdesc_sw128(vb + j * 2048, kHalf, 1024), idesc_pv,
+            mma_f16_ts(o, pa + (j >> 1) * 32 + (j & 1) * 8, vb + (uint32_t)(j * 2048 >> 4), idesc_pv,
                        st.start && j == 0 ? 0u : 1u);
           if (st.two) {
 #pragma unroll
             for (int j = 0; j < kT / 16; ++j)
-              mma_f16_ts(tO(st.t), tS(st.t) + kT / 2 + j * 8, sdesc_sw128(vb + j * 2048, kHalf, 1024),
-                         idesc_pv, 1u);
+              mma_f16_ts(o, pa + (j >> 1) * 32 + 16 + (j & 1) * 8, vb + (uint32_t)(j * 2048 >> 4), idesc_pv, 1u);
           }
           if (st.last) mma_commit(o_full(st.t));
-          if (st.kv_done) mma_commit(kv_empty(slot));
+          if (st.kv_done) mma_commit(kv_empty(st.vslot));
+        };
+        Step st, pend;
+        bool have = false;
+        while (!failed && next(st)) {
+          issue_qk(st);
+          if (have && !failed) issue_pv(pend);
+          pend = st;
+          have = true;
         }
-        __syncwarp();
-      };
-      Step st, pend;
-      bool have = false;
-      while (!failed && next(st)) {
-        issue_qk(st);
         if (have && !failed) issue_pv(pend);
-        pend = st;
-        have = true;
       }
-      if (have && !failed) issue_pv(pend);
+      failed = __any_sync(kFull, failed);
     } else {
       // ------------------------------- softmax -------------------------------
       const int t = warp >> 2, wq = warp & 3;
@@ -656,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         int done = 0;  // steps of this pipe in the segment
-        for (int i = s.wide ? 0 : ((s.cc & 1) ^ t); i < s.n; i += s.wide ? 1 : 2) {
+        for (int i = s.wide ? 0 : s.par ^ t; i < s.n; i += s.wide ? 1 : 2) {
           const int t0 = s.t0 + i * kT;
           const int lo = max(0, s.t_lo - t0), hi = min(kT, s.t_end - t0);  // valid tokens of the chunk
           const bool part = lo > 0 || hi < kT;
@@ -664,74 +753,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++steps;
           tc_fence_after();
           if (warp_ok) {
-            float x[kT];
-#pragma unroll
-            for (int j = 0; j < kT / 32; ++j) tmem_ld32(s_addr + j * 32, x + j * 32);
-            tmem_ld_wait();
+            // Two passes over S in TMEM, in blocks of 32 columns: the maximum, then the
+            // weights. (All 128 columns in registers unrolled to 30 KB of code, and eight
+            // warps on their own ways through it waited for instructions: 173 us for 128
+            // sequences of 64/8 heads behind 16384 tokens.)
             float qs = p.qscale;
+            float top;
             if (MOD || part) {
-              // scores in base-2 units, masked tokens -inf
-              if constexpr (MOD) {
-                if (p.cap > 0.f && p.cap <= 128.f) {
-                  // c tanh(y) = c - 2 c / (1 + e^2y): off by at most a few 2^-24 c
-                  const float y2 = 2.f * kLog2e * p.cap_in, c = p.cap * kLog2e;
+              // scores in base-2 units, masked tokens -inf, back into TMEM
+              top = -INFINITY;
+#pragma unroll 1
+              for (int j = 0; j < kT; j += 32) {
+                float x[32];
+                tmem_ld32(s_addr + j, x);
+                tmem_ld_wait();
+                if constexpr (MOD) score_mods(p, x, slope, far0 + (float)(i * kT + j));
+                else
 #pragma unroll
-                  for (int j = 0; j < kT; ++j) {
-                    const float z = ex2_ftz(x[j] * y2) + 1.f;
-                    float rz;
-                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rz) : "f"(z));
-                    x[j] = fmaf(-2.f * c, rz, c);
-                  }
-                } else if (p.cap > 0.f) {
-                  // a large cap: small arguments by the series of tanh y, off by at most
-                  // 2^-26 y below 1/4
-                  const float c = p.cap * kLog2e;
+                  for (int q = 0; q < 32; ++q) x[q] *= qs;
+                if (part) {
 #pragma unroll
-                  for (int j = 0; j < kT; ++j) {
-                    const float y = x[j] * p.cap_in, y2 = y * y;
-                    const float series =
-                        fmaf(fmaf(fmaf(fmaf(62.f / 2835.f, y2, -17.f / 315.f), y2, 2.f / 15.f), y2, -1.f / 3.f), y2, 1.f) * y;
-                    float rz;
-                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rz) : "f"(ex2_ftz(y * (2.f * kLog2e)) + 1.f));
-                    x[j] = c * (fabsf(y) < 0.25f ? series : fmaf(-2.f, rz, 1.f));
-                  }
-                } else {
-#pragma unroll
-                  for (int j = 0; j < kT; ++j) x[j] *= qs;
+                  for (int q = 0; q < 32; ++q)
+                    if (j + q < lo || j + q >= hi) x[q] = -INFINITY;
                 }
-                if (p.slopes != nullptr) {
-                  const float f0 = far0 + (float)(i * kT);
-#pragma unroll
-                  for (int j = 0; j < kT; ++j) x[j] = fmaf(slope, f0 + (float)j, x[j]);
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < kT; ++j) x[j] *= qs;
+                tmem_st32(s_addr + j, x);
+                top = fmaxf(top, max32(x));
               }
-              if (part) {
-#pragma unroll
-                for (int j = 0; j < kT; ++j)
-                  if (j < lo || j >= hi) x[j] = -INFINITY;
-              }
+              tmem_st_wait();
               qs = 1.f;
-            }
-            float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
-            if (qs >= 0.f) {
-#pragma unroll
-              for (int j = 4; j < kT; j += 4) {
-                a0 = fmaxf(a0, x[j]); a1 = fmaxf(a1, x[j + 1]);
-                a2 = fmaxf(a2, x[j + 2]); a3 = fmaxf(a3, x[j + 3]);
-              }
-              a0 = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
             } else {
+              // of the scaled scores: a negative scale turns the order around
+              const float sign = qs < 0.f ? -1.f : 1.f;
+              top = -INFINITY;
+#pragma unroll 1
+              for (int j = 0; j < kT; j += 64) {
+                float x[64];
+                tmem_ld32(s_addr + j, x);
+                tmem_ld32(s_addr + j + 32, x + 32);
+                tmem_ld_wait();
+                if (sign < 0.f) {
 #pragma unroll
-              for (int j = 4; j < kT; j += 4) {
-                a0 = fminf(a0, x[j]); a1 = fminf(a1, x[j + 1]);
-                a2 = fminf(a2, x[j + 2]); a3 = fminf(a3, x[j + 3]);
+                  for (int q = 0; q < 64; ++q) x[q] = -x[q];
+                }
+                top = fmaxf(top, fmaxf(max32(x), max32(x + 32)));
               }
-              a0 = fminf(fminf(a0, a1), fminf(a2, a3));
+              top *= sign * qs;
             }
-            const float top = a0 * qs;
             if (__any_sync(kFull, row_ok && top > m + kGrow)) {
               const float mn = fmaxf(m, top);
               const float alpha = m == mn ? 1.f : ex2_ftz(m - mn);
@@ -750,36 +817,50 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float neg = (m == -INFINITY ? 0.f : -m) + kShift;
-            float l0 = 0.f, l1 = 0.f;
-            auto weights = [&](auto two) {
+            const uint64_t qs2 = f32x2(qs, qs), neg2 = f32x2(neg, neg);
+            uint64_t sum2 = f32x2(0.f, 0.f);
+            // columns 32 j .. of S become the weights of those tokens: 16 columns of first
+            // terms, 16 of second ones
+            auto weights = [&](auto two, const float* x, int j) {
+              uint32_t w[16], w2[16];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t w[16], w2[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                  const float p0 = ex2_ftz(fmaf(x[j * 32 + 2 * q], qs, neg));
-                  const float p1 = ex2_ftz(fmaf(x[j * 32 + 2 * q + 1], qs, neg));
-                  w[q] = pack16<FP16>(p0, p1);
-                  const float2 f = unpack16<FP16>(w[q]);
-                  if constexpr (decltype(two)::value) {
-                    w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
-                    l0 += p0;
-                    l1 += p1;
-                  } else {
-                    l0 += f.x;
-                    l1 += f.y;
-                  }
+              for (int q = 0; q < 16; ++q) {
+                float y0, y1;
+                f32x2_split(f32x2_fma(f32x2(x[2 * q], x[2 * q + 1]), qs2, neg2), y0, y1);
+                const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+                w[q] = pack16<FP16>(p0, p1);
+                const float2 f = unpack16<FP16>(w[q]);
+                if constexpr (decltype(two)::value) {
+                  w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
+                  sum2 = f32x2_add(sum2, f32x2(p0, p1));
+                } else {
+                  sum2 = f32x2_add(sum2, f32x2(f.x, f.y));
                 }
-                tmem_st16(s_addr + j * 16, w);
-                if constexpr (decltype(two)::value) tmem_st16(s_addr + kT / 2 + j * 16, w2);
+              }
+              tmem_st16(s_addr + j, w);
+              if constexpr (decltype(two)::value) tmem_st16(s_addr + j + 16, w2);
+            };
+            auto all_weights = [&](auto two) {
+              float xa[32], xb[32];
+              tmem_ld32(s_addr, xa);
+#pragma unroll 1
+              for (int j = 0; j < kT; j += 64) {
+                tmem_ld_wait();
+                tmem_ld32(s_addr + j + 32, xb);
+                weights(two, xa, j);
+                tmem_ld_wait();
+                if (j == 0) tmem_ld32(s_addr + 64, xa);
+                weights(two, xb, j + 32);
               }
             };
-            if (s.wide) weights(std::false_type{});
-            else weights(std::true_type{});
-            l += l0 + l1;
+            if (s.wide) all_weights(std::false_type{});
+            else all_weights(std::true_type{});
+            float s0, s1;
+            f32x2_split(sum2, s0, s1);
+            l += s0 + s1;
             tmem_st_wait();
           }
-          if (part && (!s.wide || t == 0)) {
+          if (part && (!s.wide || t == s.par)) {
             // V rows of masked tokens are zeros: 0 times whatever they hold would be no zero
             const int f = 2 * (s.cc + i) + 1, slot = f % kSlots;
             if (!wait(kv_full(slot), (f / kSlots) & 1)) break;
