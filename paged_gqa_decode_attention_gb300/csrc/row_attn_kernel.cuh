@@ -20,7 +20,11 @@
 //   S = Q . K^T  (Q 128 x D from shared memory, K chunk 128 x D)       tcgen05 kind::f16
 //   O += P . V   (P from TMEM, V chunk as an MN-major operand)
 // A wide segment (more than 128 rows) gives each pipe one of its two row tiles, and both
-// read every chunk; in a narrow one the pipes take alternate chunks. The tensor pipe works
+// read every chunk; in a narrow one the pipes take alternate chunks. A sequence's own item has
+// only G rows: they stand in Q four times, once for the TMEM lanes of each warp of a pipe,
+// and each warp takes a quarter of the chunk's tokens (its P is zero elsewhere), with a
+// maximum and a sum of its own; at the segment's end the four parts are joined through
+// shared memory. The tensor pipe works
 // for one pipe while the other's warpgroup does its softmax: QK^T of step n + 1 is issued
 // before PV of step n, which belongs to the other pipe. One thread owns one row, so maxima and sums need no exchange. The
 // running maximum is only followed when it grows by more than a threshold (2^8 in bf16,
@@ -53,6 +57,9 @@ constexpr int kWarpLoad = 8;
 constexpr int kWarpMma = 9;
 constexpr int kHalf = kT * 128;   // 64 dims of 128 rows: 16 KiB
 constexpr int kSegRing = 4;
+constexpr int kSmallQ = 4;           // places for the queries of small segments, at most
+constexpr int kQBars = 2 + kSmallQ;  // Q tiles, then those places
+constexpr int kJoinBytes = 16 * 1024;
 constexpr int kSegInts = 12;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kTmemCols = 512;
@@ -86,8 +93,11 @@ struct Layout {
   static constexpr int kTile = kT * D * 2;                // Q tile, K or V chunk
   static constexpr int kSlots = D == 128 ? 5 : 10;        // K and V slots, 160 KiB
   static constexpr int kOffQ = kSlots * kTile;
-  static constexpr int kOffBar = kOffQ + 2 * kTile;
-  static constexpr int kBars = 2 * kSlots + 4 + 2 * kSegRing + 8;
+  // [pipe][16 KiB] for the join of a small segment's four parts: the second Q tile (an own
+  // segment follows no wide one that still needs it), or at D 64 memory of its own
+  static constexpr int kOffJoin = D == 128 ? kOffQ + kTile : kOffQ + 2 * kTile;
+  static constexpr int kOffBar = kOffJoin + 2 * kJoinBytes;
+  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 10;
   static constexpr int kOffTmem = kOffBar + kBars * 8;
   static constexpr int kOffSeg = kOffTmem + 16;
   static constexpr int kOffScan = kOffSeg + kSegRing * kSegInts * 4;  // warp sums, start, total
@@ -213,6 +223,36 @@ __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float f32x2_sum(uint64_t v) {
+  float a, b;
+  f32x2_split(v, a, b);
+  return a + b;
+}
+
+// 32 scores x to weights 2^(x qs + neg): the TMEM columns at addr get 16 of first terms and,
+// with two terms, 16 of second ones; sum2 adds what was written.
+template <bool FP16, bool kTwo>
+__device__ __forceinline__ void weights(uint32_t addr, const float* x, uint64_t qs2, uint64_t neg2,
+                                        uint64_t& sum2) {
+  uint32_t w[16], w2[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    float y0, y1;
+    f32x2_split(f32x2_fma(f32x2(x[2 * q], x[2 * q + 1]), qs2, neg2), y0, y1);
+    const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+    w[q] = pack16<FP16>(p0, p1);
+    const float2 f = unpack16<FP16>(w[q]);
+    if constexpr (kTwo) {
+      w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
+      sum2 = f32x2_add(sum2, f32x2(p0, p1));
+    } else {
+      sum2 = f32x2_add(sum2, f32x2(f.x, f.y));
+    }
+  }
+  tmem_st16(addr, w);
+  if constexpr (kTwo) tmem_st16(addr + 16, w2);
+}
+
 __device__ __forceinline__ float max32(const float* x) {
   float a[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -319,13 +359,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto kv_full = [&](int s) { return bar0 + 8u * s; };
   auto kv_empty = [&](int s) { return bar0 + 8u * (kSlots + s); };
   auto q_full = [&](int s) { return bar0 + 8u * (2 * kSlots + s); };
-  auto q_empty = [&](int s) { return bar0 + 8u * (2 * kSlots + 2 + s); };
-  auto seg_full = [&](int s) { return bar0 + 8u * (2 * kSlots + 4 + s); };
-  auto seg_empty = [&](int s) { return bar0 + 8u * (2 * kSlots + 4 + kSegRing + s); };
-  auto s_full = [&](int t) { return bar0 + 8u * (2 * kSlots + 4 + 2 * kSegRing + t); };
-  auto p_full = [&](int t) { return bar0 + 8u * (2 * kSlots + 6 + 2 * kSegRing + t); };
-  auto o_full = [&](int t) { return bar0 + 8u * (2 * kSlots + 8 + 2 * kSegRing + t); };
-  auto o_free = [&](int t) { return bar0 + 8u * (2 * kSlots + 10 + 2 * kSegRing + t); };
+  auto q_empty = [&](int s) { return bar0 + 8u * (2 * kSlots + kQBars + s); };
+  constexpr int kBar1 = 2 * kSlots + 2 * kQBars;
+  auto seg_full = [&](int s) { return bar0 + 8u * (kBar1 + s); };
+  auto seg_empty = [&](int s) { return bar0 + 8u * (kBar1 + kSegRing + s); };
+  auto s_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 + t); };
+  auto o_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 4 + t); };
+  auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 6 + t); };
+  auto joint = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 8 + t); };
+  // small segments' queries: rows 32 w .. 32 w + G - 1 of a tile for w < 4, so that tiles 8
+  // (16) rows further in the same memory hold those of four (two) segments
+  const int small_rows = p.G > 8 ? 16 : 8, n_small = 32 / small_rows;
   volatile int* seg_ring = reinterpret_cast<volatile int*>(base + L::kOffSeg);
   volatile int* scan = reinterpret_cast<volatile int*>(base + L::kOffScan);
   volatile int* cu = reinterpret_cast<volatile int*>(base + L::kOffCu);
@@ -340,9 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(kv_full(s), 1);
       mbar_init(kv_empty(s), 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQBars; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(joint(s), 4);
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), 4);
       mbar_init(o_full(s), 1);
@@ -477,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int PPS = kT / p.block_size;
       const int out_of_range = (int)(p.num_blocks * p.block_size);  // rows there read as zeros
       int e = scan[11], off = scan[12];
-      int fill = 0, qfill = 0, k = 0, cc = 0, par = 0, left = r1 - r0;
+      int fill = 0, qfill = 0, qsmall = 0, k = 0, cc = 0, par = 0, left = r1 - r0;
       int n_item, shared = 0;
       Own own = {};
       auto load_elem = [&]() {  // n_item and the like of element e
@@ -547,18 +595,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my_page = lane % PPS, my_half = lane / PPS;  // PPS * NB <= 32: a box per lane
         int id = page + my_page < page_end ? __ldg(table + page + my_page) : 0;
         // the queries
-        for (int t = 0; t <= s.wide; ++t, ++qfill) {
-          const int slot = qfill & 1;
-          if (qfill >= 2 && !wait(q_empty(slot), ((qfill >> 1) - 1) & 1)) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(q_full(slot), (uint32_t)((is_own ? 1 : spt) * G * 128 * NB));
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-              tma_load_3d(base_u32 + L::kOffQ + slot * L::kTile + i * kHalf,
-                          is_own ? &tmap_q1 : &tmap_q, i * 64, s.h * G, s.b0 + t * spt,
-                          q_full(slot));
-          }
+        if (is_own) {
+          if (qsmall == 0)  // the tile that the small places are in
+            for (int i = max(0, qfill - 2); i < qfill; ++i)
+              if (!wait(q_empty(i & 1), (i >> 1) & 1)) break;
+          const int slot = qsmall % n_small;
+          if (qsmall >= n_small && !failed) wait(q_empty(2 + slot), (qsmall / n_small - 1) & 1);
+          if (failed) break;
+          if (lane == 0) mbar_arrive_expect_tx(q_full(2 + slot), (uint32_t)(4 * G * 128 * NB));
           __syncwarp();
+          if (lane < 4 * NB)
+            tma_load_3d(base_u32 + L::kOffQ + (lane >> 2) * kHalf + ((lane & 3) * 32 + slot * small_rows) * 128,
+                        &tmap_q1, (lane >> 2) * 64, s.h * G, s.b0, q_full(2 + slot));
+          ++qsmall;
+        } else {
+          for (int t = 0; t <= s.wide; ++t, ++qfill) {
+            const int slot = qfill & 1;
+            if (qfill >= 2 && !wait(q_empty(slot), ((qfill >> 1) - 1) & 1)) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(q_full(slot), (uint32_t)(spt * G * 128 * NB));
+#pragma unroll
+              for (int i = 0; i < NB; ++i)
+                tma_load_3d(base_u32 + L::kOffQ + slot * L::kTile + i * kHalf, &tmap_q, i * 64, s.h * G,
+                            s.b0 + t * spt, q_full(slot));
+            }
+            __syncwarp();
+          }
         }
         if (failed) break;
         for (int c = 0; c < n; ++c) {
@@ -593,6 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no copy or MMA may be in flight when the CTA exits: wait for the last releases
       for (int i = max(0, fill - kSlots); i < fill && !failed; ++i) wait(kv_empty(i % kSlots), (i / kSlots) & 1);
       for (int i = max(0, qfill - 2); i < qfill && !failed; ++i) wait(q_empty(i & 1), (i >> 1) & 1);
+      for (int i = max(0, qsmall - n_small); i < qsmall && !failed; ++i)
+        wait(q_empty(2 + i % n_small), (i / n_small) & 1);
     } else if (warp == kWarpMma) {
       // -------------------------------- MMAs --------------------------------
       // One thread does all of it: what it does between two MMAs the tensor pipe, whose queue
@@ -606,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc = sdesc_sw128(base_u32 + L::kOffQ, 16, 1024);
         struct Step {
           int t, kslot, vslot, qslot;
+          uint32_t qoff;         // place of the queries, in descriptor units
           uint32_t kphase, vphase, qphase;
           bool start, last;      // first and last step of pipe t in the segment
           bool q_wait, q_done;   // first and last use of the Q tile
@@ -613,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool two;              // P has two terms
         };
         Seg s = {};
-        int i = 0, k = 0, qfill = 0, q_used = 0;
+        int i = 0, k = 0, qfill = 0, qsmall = -1;
         bool second = false;                      // the next step is a wide chunk's second one
         int kslot = -2;                           // ring slot of the chunk's K
         uint32_t kphase = 0;
@@ -624,15 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto next = [&](Step& st) {
           if (i == s.n) {  // the next segment
-            qfill += q_used;
+            if (!s.own) qfill += s.n == 0 ? 0 : s.wide ? 2 : 1;
             const int slot = k % kSegRing;
             if (!wait(seg_full(slot), (k / kSegRing) & 1)) return false;
             seg_get(seg_ring + slot * kSegInts, s);
             mbar_arrive(seg_empty(slot));
             ++k;
             i = 0;
-            q_used = s.wide ? 2 : 1;
             if (s.n == 0) return false;
+            if (s.own) ++qsmall;
           }
           if (!second) {  // a new chunk
             kslot += 2;
@@ -644,9 +709,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           st.t = (s.par + (s.wide ? (second ? 1 : 0) : i)) & 1;
           st.start = i < (s.wide ? 1 : 2);
           st.last = i >= s.n - (s.wide ? 1 : 2);
-          const int q = qfill + (s.wide ? st.t : 0);
-          st.qslot = q & 1;
-          st.qphase = (q >> 1) & 1;
+          if (s.own) {
+            const int slot = qsmall % n_small;
+            st.qslot = 2 + slot;
+            st.qphase = (qsmall / n_small) & 1;
+            st.qoff = (uint32_t)(slot * small_rows * 128 >> 4);
+          } else {
+            const int q = qfill + (s.wide ? st.t : 0);
+            st.qslot = q & 1;
+            st.qphase = (q >> 1) & 1;
+            st.qoff = (uint32_t)(st.qslot * (L::kTile >> 4));
+          }
           st.kslot = kslot;
           st.kphase = kphase;
           st.vslot = kslot + 1 == kSlots ? 0 : kslot + 1;
@@ -667,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (st.q_wait && !wait(q_full(st.qslot), st.qphase)) return;
           if (!wait(kv_full(st.kslot), st.kphase)) return;
           tc_fence_after();
-          const uint64_t qa = q_desc + (uint32_t)(st.qslot * (L::kTile >> 4));
+          const uint64_t qa = q_desc + st.qoff;
           const uint64_t kb = k_desc + (uint32_t)(st.kslot * (L::kTile >> 4));
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
@@ -726,6 +799,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(kFull, ok)) failed = true;
         return !failed;
       };
+      int meets = 0;
+      [[maybe_unused]] float slope = 0.f, far0 = 0.f;
+      // products q . k of 32 tokens to scores in base-2 units, those outside [lo, hi) -inf
+      auto scores = [&](float* x, float far, bool part, int lo, int hi) {
+        if constexpr (MOD) score_mods(p, x, slope, far);
+        else
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[q] *= p.qscale;
+        if (part) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            if (q < lo || q >= hi) x[q] = -INFINITY;
+        }
+      };
+      auto shift = [&](float m) {
+        const float neg = (m == -INFINITY ? 0.f : -m) + kShift;
+        return f32x2(neg, neg);
+      };
+      auto meet = [&]() {  // the pipe's four warps, with what they wrote to shared memory
+        __syncwarp();
+        if (lane == 0) mbar_arrive(joint(t));
+        return wait(joint(t), meets++ & 1);
+      };
       for (int k = 0; !failed; ++k) {
         Seg s;
         if (!wait(seg_full(k % kSegRing), (k / kSegRing) & 1)) break;
@@ -734,11 +830,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(seg_empty(k % kSegRing));
         if (s.n == 0) break;
         const int n_rows = (s.wide ? (t ? s.n_seq - spt : spt) : s.n_seq) * G;
-        const bool row_ok = r < n_rows, warp_ok = wq * 32 < n_rows;
-        const int rs = r / G, b = s.b0 + (s.wide && t ? spt : 0) + rs, hq = s.h * G + r - rs * G;
+        // own segments: every warp has the G rows, and a quarter of each chunk's tokens
+        const int ri = s.own ? lane : r;
+        const bool row_ok = ri < n_rows, warp_ok = s.own || wq * 32 < n_rows;
+        const int rs = ri / G, b = s.b0 + (s.wide && t ? spt : 0) + rs, hq = s.h * G + ri - rs * G;
         float m = -INFINITY, l = 0.f;  // running maximum (base 2), sum of the weights
-        [[maybe_unused]] float slope = 0.f, far0 = 0.f;
         if constexpr (MOD) {
+          slope = far0 = 0.f;
           if (p.slopes != nullptr && row_ok) {
             slope = __ldg(p.slopes + hq) * kLog2e;
             far0 = (float)(s.t0 - (context_len(p, b) - 1));
@@ -752,53 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(s_full(t), steps & 1)) break;
           ++steps;
           tc_fence_after();
-          if (warp_ok) {
-            // Two passes over S in TMEM, in blocks of 32 columns: the maximum, then the
-            // weights. (All 128 columns in registers unrolled to 30 KB of code, and eight
-            // warps on their own ways through it waited for instructions: 173 us for 128
-            // sequences of 64/8 heads behind 16384 tokens.)
-            float qs = p.qscale;
-            float top;
-            if (MOD || part) {
-              // scores in base-2 units, masked tokens -inf, back into TMEM
-              top = -INFINITY;
-#pragma unroll 1
-              for (int j = 0; j < kT; j += 32) {
-                float x[32];
-                tmem_ld32(s_addr + j, x);
-                tmem_ld_wait();
-                if constexpr (MOD) score_mods(p, x, slope, far0 + (float)(i * kT + j));
-                else
-#pragma unroll
-                  for (int q = 0; q < 32; ++q) x[q] *= qs;
-                if (part) {
-#pragma unroll
-                  for (int q = 0; q < 32; ++q)
-                    if (j + q < lo || j + q >= hi) x[q] = -INFINITY;
-                }
-                tmem_st32(s_addr + j, x);
-                top = fmaxf(top, max32(x));
-              }
-              tmem_st_wait();
-              qs = 1.f;
-            } else {
-              // of the scaled scores: a negative scale turns the order around
-              const float sign = qs < 0.f ? -1.f : 1.f;
-              top = -INFINITY;
-#pragma unroll 1
-              for (int j = 0; j < kT; j += 64) {
-                float x[64];
-                tmem_ld32(s_addr + j, x);
-                tmem_ld32(s_addr + j + 32, x + 32);
-                tmem_ld_wait();
-                if (sign < 0.f) {
-#pragma unroll
-                  for (int q = 0; q < 64; ++q) x[q] = -x[q];
-                }
-                top = fmaxf(top, fmaxf(max32(x), max32(x + 32)));
-              }
-              top *= sign * qs;
-            }
+          // Follows the running maximum once the chunk's largest score has outgrown it.
+          auto follow = [&](float top) {
             if (__any_sync(kFull, row_ok && top > m + kGrow)) {
               const float mn = fmaxf(m, top);
               const float alpha = m == mn ? 1.f : ex2_ftz(m - mn);
@@ -816,48 +869,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            const float neg = (m == -INFINITY ? 0.f : -m) + kShift;
-            const uint64_t qs2 = f32x2(qs, qs), neg2 = f32x2(neg, neg);
+          };
+          if (s.own) {
+            const int j = wq * 32;
+            float x[32];
+            tmem_ld32(s_addr + j, x);
+            tmem_ld_wait();
+            scores(x, far0 + (float)(i * kT + j), part, lo - j, hi - j);
+            follow(max32(x));
             uint64_t sum2 = f32x2(0.f, 0.f);
-            // columns 32 j .. of S become the weights of those tokens: 16 columns of first
-            // terms, 16 of second ones
-            auto weights = [&](auto two, const float* x, int j) {
-              uint32_t w[16], w2[16];
+            weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum2);
 #pragma unroll
-              for (int q = 0; q < 16; ++q) {
-                float y0, y1;
-                f32x2_split(f32x2_fma(f32x2(x[2 * q], x[2 * q + 1]), qs2, neg2), y0, y1);
-                const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
-                w[q] = pack16<FP16>(p0, p1);
-                const float2 f = unpack16<FP16>(w[q]);
-                if constexpr (decltype(two)::value) {
-                  w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
-                  sum2 = f32x2_add(sum2, f32x2(p0, p1));
-                } else {
-                  sum2 = f32x2_add(sum2, f32x2(f.x, f.y));
-                }
+            for (int q = 0; q < 32; ++q) x[q] = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < kT; c += 32)
+              if (c != j) tmem_st32(s_addr + c, x);
+            l += f32x2_sum(sum2);
+            tmem_st_wait();
+          } else if (warp_ok) {
+            // Two passes over S in TMEM, in blocks of 32 columns: the maximum, then the
+            // weights. (All 128 columns in registers unrolled to 30 KB of code, and eight
+            // warps on their own ways through it waited for instructions: 173 us for 128
+            // sequences of 64/8 heads behind 16384 tokens.)
+            float qs = p.qscale;
+            float top = -INFINITY;
+            if (MOD || part) {
+              // scores in base-2 units, masked tokens -inf, back into TMEM
+#pragma unroll 1
+              for (int j = 0; j < kT; j += 32) {
+                float x[32];
+                tmem_ld32(s_addr + j, x);
+                tmem_ld_wait();
+                scores(x, far0 + (float)(i * kT + j), part, lo - j, hi - j);
+                tmem_st32(s_addr + j, x);
+                top = fmaxf(top, max32(x));
               }
-              tmem_st16(s_addr + j, w);
-              if constexpr (decltype(two)::value) tmem_st16(s_addr + j + 16, w2);
-            };
+              tmem_st_wait();
+              qs = 1.f;
+            } else {
+              // of the scaled scores: a negative scale turns the order around
+              const float sign = qs < 0.f ? -1.f : 1.f;
+#pragma unroll 1
+              for (int j = 0; j < kT; j += 64) {
+                float x[64];
+                tmem_ld32(s_addr + j, x);
+                tmem_ld32(s_addr + j + 32, x + 32);
+                tmem_ld_wait();
+                if (sign < 0.f) {
+#pragma unroll
+                  for (int q = 0; q < 64; ++q) x[q] = -x[q];
+                }
+                top = fmaxf(top, fmaxf(max32(x), max32(x + 32)));
+              }
+              top *= sign * qs;
+            }
+            follow(top);
+            const uint64_t qs2 = f32x2(qs, qs), neg2 = shift(m);
+            uint64_t sum2 = f32x2(0.f, 0.f);
             auto all_weights = [&](auto two) {
+              constexpr bool kTwo = decltype(two)::value;
               float xa[32], xb[32];
               tmem_ld32(s_addr, xa);
 #pragma unroll 1
               for (int j = 0; j < kT; j += 64) {
                 tmem_ld_wait();
                 tmem_ld32(s_addr + j + 32, xb);
-                weights(two, xa, j);
+                weights<FP16, kTwo>(s_addr + j, xa, qs2, neg2, sum2);
                 tmem_ld_wait();
                 if (j == 0) tmem_ld32(s_addr + 64, xa);
-                weights(two, xb, j + 32);
+                weights<FP16, kTwo>(s_addr + j + 32, xb, qs2, neg2, sum2);
               }
             };
             if (s.wide) all_weights(std::false_type{});
             else all_weights(std::true_type{});
-            float s0, s1;
-            f32x2_split(sum2, s0, s1);
-            l += s0 + s1;
+            l += f32x2_sum(sum2);
             tmem_st_wait();
           }
           if (part && (!s.wide || t == s.par)) {
@@ -885,13 +970,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t w = s.first ? ws_first(p, s.own, out_row, s.wide ? 0 : t)
                                   : ws_next(p, blockIdx.x, cap_rows, t, r);
         if (done == 0) {
-          if (row_ok) p.ws_lse[w] = -INFINITY;
+          if (row_ok && (!s.own || wq == 0)) p.ws_lse[w] = -INFINITY;
           continue;
         }
         if (!wait(o_full(t), outs & 1)) break;
         ++outs;
         tc_fence_after();
-        if (warp_ok) {
+        if (s.own) {
+          // the four warps' parts, 32 dims at a time; every step of it between two meetings
+          float4* part4 = reinterpret_cast<float4*>(base + L::kOffJoin + t * kJoinBytes);  // [4][16][8]
+          float2* ml = reinterpret_cast<float2*>(part4 + 4 * 16 * 8);                      // [4][16]
+          if (row_ok) ml[wq * 16 + lane] = make_float2(m, l);
+          if (!meet()) break;
+          float M = -INFINITY, sum = 0.f;
+          if (row_ok) {
+            float2 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[q] = ml[q * 16 + lane];
+              M = fmaxf(M, v[q].x);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum += v[q].x == -INFINITY ? 0.f : ex2_ftz(v[q].x - M) * v[q].y;
+          }
+          const float f = m == -INFINITY ? 0.f : ex2_ftz(m - M) / sum;
+          const int64_t w0 = s.first ? ws_first(p, true, (int64_t)s.b0 * p.Hq + s.h * G, t)
+                                     : ws_next(p, blockIdx.x, cap_rows, t, 0);
+          const int w_step = s.first ? 2 : 1;  // workspace rows from one head's to the next one's
+          const int out_r = r >> 3, out_c = r & 7;
+#pragma unroll 1
+          for (int j = 0; j < D / 32; ++j) {
+            float o[32];
+            tmem_ld32(o_addr + j * 32, o);
+            tmem_ld_wait();
+            if (row_ok) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                part4[(wq * 16 + lane) * 8 + (q ^ (lane & 7))] =
+                    make_float4(o[4 * q] * f, o[4 * q + 1] * f, o[4 * q + 2] * f, o[4 * q + 3] * f);
+            }
+            if (!meet()) break;
+            if (out_r < G) {
+              float4 a = part4[out_r * 8 + (out_c ^ (out_r & 7))];
+#pragma unroll
+              for (int q = 1; q < 4; ++q) {
+                const float4 c = part4[(q * 16 + out_r) * 8 + (out_c ^ (out_r & 7))];
+                a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+              }
+              *reinterpret_cast<float4*>(p.ws_o + (w0 + (int64_t)out_r * w_step) * D + j * 32 + out_c * 4) = a;
+            }
+            if (!meet()) break;
+          }
+          if (failed) break;
+          if (row_ok && wq == 0) p.ws_lse[w] = M - kShift + log2f(sum);
+        } else if (warp_ok) {
           const float inv = 1.f / l;
           float* dst = p.ws_o + w * D;
 #pragma unroll
