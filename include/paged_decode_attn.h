@@ -184,7 +184,7 @@ int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k
                                  const float* alibi_slopes, int window, void* out, void* stream);
 
 /* The same (without a window) for a batch whose sequences share the start of
- * their contexts: for i < num_prefixes (<= 192), the sequences cu_seqs[i] ..
+ * their contexts: for i < num_prefixes (<= 128), the sequences cu_seqs[i] ..
  * cu_seqs[i + 1] - 1 have the same ids in their block_table rows for the
  * first prefix_lens[i] tokens, and those blocks are read once for all of them
  * (tiles of up to 256 query rows of a kv head). cu_seqs [num_prefixes + 1] and

@@ -321,7 +321,7 @@ class PagedDecodeAttention:
         blocks are shared, and no more than the shortest of the contexts that
         are not empty). Sequences outside every group, and a prefix of 0,
         share nothing. block_table and context_lens hold whole contexts, as
-        for ``run``. P <= 192. softcap and alibi_slopes as in ``run``."""
+        for ``run``. P <= 128. softcap and alibi_slopes as in ``run``."""
         return self._run_rows(q, k_cache, v_cache, block_table, context_lens, scale, softcap,
                               alibi_slopes, out, stream, cu_seqs=cu_seqs, prefix_lens=prefix_lens)
 

@@ -540,7 +540,7 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
   if (batch < 0 || batch > c.max_batch) return fail(PDA_EINVAL, "batch out of [0, max_batch]");
   if (batch > pda::row::kMaxBatch) return fail(PDA_EUNSUPPORTED, "this call takes up to 16384 sequences");
   if (num_prefixes < 0) return fail(PDA_EINVAL, "num_prefixes < 0");
-  if (num_prefixes > pda::row::kMaxPrefixes) return fail(PDA_EUNSUPPORTED, "this call takes up to 192 prefixes");
+  if (num_prefixes > pda::row::kMaxPrefixes) return fail(PDA_EUNSUPPORTED, "this call takes up to 128 prefixes");
   if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
   if (!std::isfinite(softcap) || softcap < 0.f)
     return fail(PDA_EINVAL, "softcap must be finite and >= 0 (0: none)");
@@ -562,10 +562,10 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
        reinterpret_cast<uintptr_t>(cu_seqs) | reinterpret_cast<uintptr_t>(prefix_lens) |
        reinterpret_cast<uintptr_t>(alibi_slopes)) & 3u)
     return fail(PDA_EINVAL, "block_table, context_lens, cu_seqs, prefix_lens and alibi_slopes must be 4-byte aligned");
-  // chunks of 128 tokens that the kernel counts in 32 bits: every sequence's own, and every
-  // group's (at most one row tile a sequence)
+  // what the kernel counts in 32 bits: up to 8 a chunk of 128 tokens and 8 an item, for every
+  // sequence's own tokens and every group's (at most one row tile a sequence)
   const int64_t chunks = ((int64_t)max_blocks * c.block_size + pda::row::kT - 1) / pda::row::kT;
-  if (2 * (int64_t)batch * c.num_kv_heads * chunks > INT_MAX)
+  if (2 * (int64_t)batch * c.num_kv_heads * 8 * (chunks + 1) > INT_MAX)
     return fail(PDA_EINVAL, "batch * num_kv_heads * max_blocks is too large for this call");
   const size_t n_q = (size_t)batch * c.num_q_heads * c.head_dim;
   const size_t cache_bytes = (size_t)num_blocks * c.block_size * c.num_kv_heads * c.head_dim * 2;
@@ -606,6 +606,7 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
   p.G = h->group;
   p.max_blocks = max_blocks;
   p.block_size = c.block_size;
+  p.bs_log = c.block_size == 16 ? 4 : c.block_size == 32 ? 5 : 6;
   p.num_blocks = num_blocks;
   p.window = window;
   p.qscale = scale * pda::kLog2e;

@@ -15,29 +15,40 @@ namespace row {
 namespace {
 
 constexpr int kMergeWarps = 4;
-// One warp a row from this many rows on (152 SMs x 16 blocks of 4 rows).
-constexpr int kManyRows = 9728;
+// One warp a row from this many rows on: one block of four warps a row would take more than
+// one round of blocks (152 SMs x 8).
+constexpr int kManyRows = 1216;
 
 // The workspace rows of one part of a row's context.
 struct Part {
+  int kind, n_chunks, x;  // the item, and where the first CTA's range begins in it (<= 0)
+  int per;
   int64_t first;  // partial(s) of the segment that starts the item
   int64_t next;   // of the first CTA's slab, as if it held one
   int64_t slab;   // rows from one CTA's slab to the next one's
   int n, m, cap;  // partials, of which m a segment; rows from one pipe's to the next one's in a slab
+  // Partial i's row, or -1: a CTA whose range holds no chunk's beginning.
   __device__ __forceinline__ int64_t at(int i) const {
     const int seg = m == 2 ? i >> 1 : i, pipe = m == 2 ? i & 1 : 0;
-    return seg == 0 ? first + pipe : next + seg * slab + pipe * cap;
+    if (seg == 0) return first + pipe;
+    const int x0 = x + seg * per;
+    if (chunk_at(kind, n_chunks, x0) >= chunk_at(kind, n_chunks, x0 + per)) return -1;
+    return next + seg * slab + pipe * cap;
   }
 };
-__device__ __forceinline__ Part part_of(const Params& p, bool own, int64_t row, int start, int n,
-                                        int per, int tile, int r, bool wide) {
+__device__ __forceinline__ Part part_of(const Params& p, int64_t row, int kind, int start, int n,
+                                        int per, int tile, int r) {
   Part d = {};
   if (n == 0) return d;
-  const int c0 = start / per, c1 = (start + n - 1) / per;
+  const int c0 = start / per, c1 = (start + item_cost(kind, n) - 1) / per;
+  d.kind = kind;
+  d.n_chunks = n;
+  d.x = c0 * per - start;
+  d.per = per;
   d.cap = ws_cap(p);
-  d.m = wide ? 1 : 2;
+  d.m = kind == kWideItem ? 1 : 2;
   d.n = (c1 - c0 + 1) * d.m;
-  d.first = ws_first(p, own, row, 0);
+  d.first = ws_first(p, kind == kOwnItem, row, 0);
   d.next = ws_next(p, c0, d.cap, tile, r);
   d.slab = 2 * d.cap;
   return d;
@@ -46,7 +57,7 @@ __device__ __forceinline__ Part part_of(const Params& p, bool own, int64_t row, 
 template <int D, bool FP16, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Params p) {
   constexpr int V = D / 32;   // dims of a lane
-  constexpr int U = 8;        // partials in flight
+  constexpr int U = 4;        // partials in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.B * p.Hq;
   const int row = WPR == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x;
@@ -57,11 +68,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Param
   const int b = row / p.Hq, hq = row - b * p.Hq, h = hq / p.G, g = hq - h * p.G;
   const int per = p.plan[0];
   const SeqPlan s = reinterpret_cast<const SeqPlan*>(p.plan + kPlanInts)[b];
-  const bool wide = s.pre_row >= kWide;
   const int pr = s.pre_row & (kWide - 1);
-  const Part pre = part_of(p, false, row, s.pre_start + h * s.pre_stride, s.pre_n, per,
-                           pr >= kT ? 1 : 0, (pr & (kT - 1)) + g, wide);
-  const Part own = part_of(p, true, row, s.own_start + h * s.own_n, s.own_n, per, 0, g, false);
+  const Part pre = part_of(p, row, s.pre_row >= kWide ? kWideItem : kTileItem,
+                           s.pre_start + h * s.pre_stride, s.pre_n, per, pr >= kT ? 1 : 0,
+                           (pr & (kT - 1)) + g);
+  const Part own = part_of(p, row, kOwnItem, s.own_start + h * item_cost(kOwnItem, s.own_n), s.own_n,
+                           per, 0, g);
   const int n = pre.n + own.n;
   float M = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
@@ -74,6 +86,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Param
       if (i0 + u < n) {
         const int i = i0 + u;
         const int64_t at = i < pre.n ? pre.at(i) : own.at(i - pre.n);
+        if (at < 0) continue;
         l[u] = __ldcg(p.ws_lse + at);
         const float* src = p.ws_o + at * D + lane * V;
         if constexpr (V == 4) {

@@ -11,7 +11,7 @@ namespace pda {
 namespace row {
 
 constexpr int kT = 128;             // tokens of a chunk, and query rows of a tile
-constexpr int kMaxPrefixes = 192;   // prefix groups a call may have
+constexpr int kMaxPrefixes = 128;   // prefix groups a call may have
 constexpr int kMaxBatch = 16384;    // sequences a call may have
 constexpr int kPlanInts = 8;        // plan entry of a sequence (SeqPlan)
 
@@ -24,9 +24,10 @@ struct Params {
   void* out;                    // [B, Hq, D]
   float* ws_o;                  // partial rows (normalised outputs), D floats each
   float* ws_lse;                // and their log-sum-exps, base 2
-  int* plan;                    // [1 + ...]: chunks per CTA; then SeqPlan of each sequence
+  int* plan;                    // [1 + ...]: cost per CTA; then SeqPlan of each sequence
   int* err;
   int B, P, Hq, Hkv, G, max_blocks, block_size;
+  int bs_log;      // log2(block_size)
   int64_t num_blocks;
   int window;      // > 0: only the last `window` tokens
   float qscale;    // scale * log2(e)

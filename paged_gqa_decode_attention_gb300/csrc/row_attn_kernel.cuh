@@ -66,16 +66,32 @@ constexpr uint32_t kTmemCols = 512;
 
 // What the merge needs to know of a sequence.
 struct SeqPlan {
-  int pre_start;   // first chunk of its tile's item of kv head 0 in its group, in the row of all chunks
-  int pre_stride;  // chunks from one kv head's item to the next one's
+  int pre_start;   // where its tile's item of kv head 0 begins, in the row of all items
+  int pre_stride;  // from one kv head's item to the next one's
   int pre_n;       // chunks of the shared part (0: none)
   int pre_row;     // row of its first query head in the item (tile 1 from kT on), + kWide if wide
-  int own_start;   // first chunk of its own part's item of kv head 0
+  int own_start;   // where its own part's item of kv head 0 begins
   int own_n;       // chunks of its own part
   int pad0, pad1;
 };
 static_assert(sizeof(SeqPlan) == kPlanInts * 4, "plan entry");
 constexpr int kWide = 1 << 16;
+
+// What an item of n chunks costs, in the units that the cut counts: a chunk, and what comes on
+// top once. Chunk 0 stands for the fixed part too, so that it belongs to the CTA in whose
+// range the item begins.
+enum ItemKind { kOwnItem, kTileItem, kWideItem };  // a sequence's own; shared, up to 128 rows; up to 256
+__device__ __forceinline__ int item_chunk(int kind) { return kind == kWideItem ? 5 : 4; }
+__device__ __forceinline__ int item_fixed(int kind) { return kind == kOwnItem ? 2 : 4; }
+__device__ __forceinline__ int item_cost(int kind, int n) {
+  return n > 0 ? item_fixed(kind) + n * item_chunk(kind) : 0;
+}
+// The chunks of an item that begin before position x of it.
+__device__ __forceinline__ int chunk_at(int kind, int n, int x) {
+  if (x <= 0) return 0;
+  const int c = item_chunk(kind), y = x - item_fixed(kind);
+  return y <= c ? min(1, n) : min(n, (y + c - 1) / c);
+}
 
 // Partial rows in the workspace: [B * Hq][2] of the segments that start a shared item (by
 // pipe, or entry 0 for a wide one), [B * Hq][2] of those that start an own item, then per
@@ -98,11 +114,12 @@ struct Layout {
   static constexpr int kOffJoin = D == 128 ? kOffQ + kTile : kOffQ + 2 * kTile;
   static constexpr int kOffBar = kOffJoin + 2 * kJoinBytes;
   static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 10;
-  static constexpr int kOffTmem = kOffBar + kBars * 8;
+  static constexpr int kOffMl = kOffBar + kBars * 8;  // [pipe][4 warps][16 rows] maximum and sum
+  static constexpr int kOffTmem = kOffMl + 2 * 4 * 16 * 8;
   static constexpr int kOffSeg = kOffTmem + 16;
   static constexpr int kOffScan = kOffSeg + kSegRing * kSegInts * 4;  // warp sums, start, total
   static constexpr int kOffCu = kOffScan + 16 * 4;
-  static constexpr int kOffShared = kOffCu + (kMaxPrefixes + 4) * 4;
+  static constexpr int kOffShared = kOffCu + (kMaxPrefixes + 4) * 2;
   static constexpr int kOffRow = kOffShared + kMaxPrefixes * 4;
   static constexpr int kBytes = kOffRow + kMaxPrefixes * 4;
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
@@ -304,7 +321,7 @@ __device__ __forceinline__ int context_len(const Params& p, int b) {
 }
 
 // The last prefix group g with cu[g] <= b, if b < cu[g + 1] (else -1).
-__device__ __forceinline__ int group_of(const volatile int* cu, int P, int b) {
+__device__ __forceinline__ int group_of(const volatile uint16_t* cu, int P, int b) {
   int lo = 0, hi = P + 1;  // first g with cu[g] > b
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -317,16 +334,16 @@ __device__ __forceinline__ int group_of(const volatile int* cu, int P, int b) {
 struct Own {
   int L, first_tok, first_page, n;
 };
-__device__ __forceinline__ Own own_part(const Params& p, int b, int shared_pages) {
+__device__ __forceinline__ Own own_part(const Params& p, int len, int shared_pages) {
   Own o;
-  o.L = context_len(p, b);
+  o.L = len;
   o.first_tok = p.window > 0 && o.L > p.window ? o.L - p.window : 0;
-  o.first_page = o.first_tok / p.block_size;
+  o.first_page = o.first_tok >> p.bs_log;
   if (shared_pages > 0) {
     o.first_page = shared_pages;
-    o.first_tok = shared_pages * p.block_size;
+    o.first_tok = shared_pages << p.bs_log;
   }
-  const int first = o.first_page * p.block_size;
+  const int first = o.first_page << p.bs_log;
   o.n = o.L > first ? (o.L - first + kT - 1) / kT : 0;
   return o;
 }
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int small_rows = p.G > 8 ? 16 : 8, n_small = 32 / small_rows;
   volatile int* seg_ring = reinterpret_cast<volatile int*>(base + L::kOffSeg);
   volatile int* scan = reinterpret_cast<volatile int*>(base + L::kOffScan);
-  volatile int* cu = reinterpret_cast<volatile int*>(base + L::kOffCu);
+  volatile uint16_t* cu = reinterpret_cast<volatile uint16_t*>(base + L::kOffCu);
   int* shared_pages = reinterpret_cast<int*>(base + L::kOffShared);  // of each group
   int* shared_row = reinterpret_cast<int*>(base + L::kOffRow);       // a sequence that holds them
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
@@ -414,47 +431,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) griddep_launch_dependents();
 
   // ------------------------------- the plan -------------------------------
-  // Chunks of every element (the groups, then the sequences) and their running sum; the
-  // ring's memory holds them.
+  // What every element (the groups, then the sequences) costs, and the running sum; the
+  // ring's memory holds them. What a thread needs of the inputs it loads at once.
   int P = p.P;
   int* sum = reinterpret_cast<int*>(base);
+  const int my_len = tid < p.B ? context_len(p, tid) : 0;
+  int my_prefix = 0;
   if (P > 0) {
-    for (int g = tid; g <= P; g += kThreads) cu[g] = __ldg(p.cu_seqs + g);
-    for (int g = tid; g < P; g += kThreads) shared_pages[g] = shared_row[g] = 0x7fffffff;
-    __syncthreads();
-    bool bad = false;
-    for (int g = tid; g < P; g += kThreads) bad |= cu[g] > cu[g + 1];
-    if (tid == 0) bad |= cu[0] < 0 || cu[P] > p.B;
-    if (__syncthreads_or(bad)) {  // no grouping: every sequence reads its own table row
-      P = 0;
+    const int mine = tid <= P ? __ldg(p.cu_seqs + tid) : 0, next = tid < P ? __ldg(p.cu_seqs + tid + 1) : mine;
+    my_prefix = tid < P ? max(0, __ldg(p.prefix_lens + tid)) : 0;
+    if (tid <= P) cu[tid] = (uint16_t)mine;
+    if (tid < P) shared_pages[tid] = shared_row[tid] = 0x7fffffff;
+    if (__syncthreads_or(mine > next || mine < 0 || mine > p.B)) {
+      P = 0;  // no grouping: every sequence reads its own table row
       if (tid == 0 && blockIdx.x == 0 && atomicCAS(p.err, 0, kErrCuSeqs) == 0) p.err[1] = 0;
     }
   }
+  auto len_of = [&](int b) { return b == tid ? my_len : context_len(p, b); };
   if (P > 0) {
     for (int b = tid; b < p.B; b += kThreads) {
       // an empty sequence (a padded batch) has no say, and its table row is not read
-      const int g = group_of(cu, P, b), n = context_len(p, b);
+      const int g = group_of(cu, P, b), n = len_of(b);
       if (g >= 0 && n > 0) {
         atomicMin(shared_pages + g, n);
         atomicMin(shared_row + g, b);
       }
     }
     __syncthreads();
-    for (int g = tid; g < P; g += kThreads) {
-      const int n = min(shared_pages[g], max(0, __ldg(p.prefix_lens + g)));
-      shared_pages[g] = cu[g + 1] - cu[g] > 1 && shared_row[g] < p.B ? n / p.block_size : 0;
+    if (tid < P) {
+      const int n = min(shared_pages[tid], my_prefix);
+      shared_pages[tid] = cu[tid + 1] - cu[tid] > 1 && shared_row[tid] < p.B ? n >> p.bs_log : 0;
     }
     __syncthreads();
   }
   auto tiles_of = [&](int g) { return (cu[g + 1] - cu[g] + 2 * spt - 1) / (2 * spt); };
-  auto group_chunks = [&](int g) { return (shared_pages[g] * p.block_size + kT - 1) / kT; };
+  auto group_chunks = [&](int g) { return ((shared_pages[g] << p.bs_log) + kT - 1) / kT; };
+  // the last tile of a group may be narrow, the others are wide
+  auto last_kind = [&](int g, int tiles) { return cu[g + 1] - cu[g] - (tiles - 1) * 2 * spt > spt ? kWideItem : kTileItem; };
+  auto group_cost = [&](int g) {  // of one kv head
+    const int n = group_chunks(g), tiles = tiles_of(g);
+    return (tiles - 1) * item_cost(kWideItem, n) + item_cost(last_kind(g, tiles), n);
+  };
   auto seq_shared = [&](int b) {
     const int g = P > 0 ? group_of(cu, P, b) : -1;
     return g >= 0 ? shared_pages[g] : 0;
   };
   const int n_elem = P + p.B;
-  for (int e = tid; e < n_elem; e += kThreads)
-    sum[e] = p.Hkv * (e < P ? tiles_of(e) * group_chunks(e) : own_part(p, e - P, seq_shared(e - P)).n);
+  if (tid < P) sum[tid] = tiles_of(tid) > 0 ? p.Hkv * group_cost(tid) : 0;
+  for (int b = tid; b < p.B; b += kThreads)
+    sum[P + b] = p.Hkv * item_cost(kOwnItem, own_part(p, len_of(b), seq_shared(b)).n);
   __syncthreads();
   const int per_thread = (n_elem + kThreads - 1) / kThreads;
   const int e0 = min(n_elem, tid * per_thread), e1 = min(n_elem, e0 + per_thread);
@@ -469,22 +494,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += scan[w];
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int v = scan[w];
+      all += v;
+      if (w < warp) before += v;
+    }
     int at = before + incl - mine;
     for (int e = e0; e < e1; ++e) {
       const int n = sum[e];
       sum[e] = at;
       at += n;
     }
-    if (tid == kThreads - 1) scan[10] = at;
+    if (tid == 0) scan[10] = all;
     __syncthreads();
   }
   const int total = scan[10];
-  const int per = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  // no less than a chunk each: finer cuts would only leave empty ranges
+  const int per = max(item_chunk(kOwnItem), (total + (int)gridDim.x - 1) / (int)gridDim.x);
   const int r0 = min((int64_t)total, (int64_t)blockIdx.x * per);
-  const int r1 = min(total, r0 + per);
-  // the element that holds chunk r0
+  const int r1 = min((int64_t)total, (int64_t)r0 + per);
+  // the element that r0 falls into
   for (int e = e0; e < e1; ++e) {
     const int next = e + 1 < n_elem ? sum[e + 1] : total;
     if (r0 >= sum[e] && r0 < next) {
@@ -492,22 +523,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       scan[12] = r0 - sum[e];
     }
   }
-  if (blockIdx.x == 0) {  // for the merge
+  if (blockIdx.x == gridDim.x - 1) {  // for the merge, by the CTA with the least left to do
     if (tid == 0) p.plan[0] = per;
     SeqPlan* plan = reinterpret_cast<SeqPlan*>(p.plan + kPlanInts);
     for (int b = tid; b < p.B; b += kThreads) {
       SeqPlan s = {};
-      const int g = P > 0 ? group_of(cu, P, b) : -1;
-      if (g >= 0 && shared_pages[g] > 0 && context_len(p, b) > 0) {
+      const int g = P > 0 ? group_of(cu, P, b) : -1, len = len_of(b);
+      if (g >= 0 && shared_pages[g] > 0 && len > 0) {
         const int i = b - cu[g], tile = i / (2 * spt), r = i - tile * 2 * spt;
         const int n_seq = min(2 * spt, cu[g + 1] - cu[g] - tile * 2 * spt);
         s.pre_n = group_chunks(g);
-        s.pre_start = sum[g] + tile * s.pre_n;
-        s.pre_stride = tiles_of(g) * s.pre_n;
+        s.pre_start = sum[g] + tile * item_cost(kWideItem, s.pre_n);
+        s.pre_stride = group_cost(g);
         s.pre_row = (r >= spt ? kT + (r - spt) * G : r * G) + (n_seq > spt ? kWide : 0);
       }
       s.own_start = sum[P + b];
-      s.own_n = own_part(p, b, g >= 0 ? shared_pages[g] : 0).n;
+      s.own_n = own_part(p, len, g >= 0 ? shared_pages[g] : 0).n;
       plan[b] = s;
     }
   }
@@ -522,23 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (r0 < r1) {
     if (warp == kWarpLoad) {
       // ------------------------- segments and loads -------------------------
-      const int PPS = kT / p.block_size;
+      const int PPS = kT >> p.bs_log;
       const int out_of_range = (int)(p.num_blocks * p.block_size);  // rows there read as zeros
-      int e = scan[11], off = scan[12];
-      int fill = 0, qfill = 0, qsmall = 0, k = 0, cc = 0, par = 0, left = r1 - r0;
-      int n_item, shared = 0;
-      Own own = {};
-      auto load_elem = [&]() {  // n_item and the like of element e
-        if (e < P) {
-          n_item = group_chunks(e);
-        } else {
-          shared = seq_shared(e - P);
-          own = own_part(p, e - P, shared);
-          n_item = own.n;
-        }
-      };
-      load_elem();
-      int item = off / n_item, chunk = off - item * n_item;  // item: (h, tile) of a group, h of a sequence
+      const int my_page = lane % PPS, my_half = lane / PPS;  // PPS * NB <= 32: a box per lane
+      int fill = 0, qfill = 0, qsmall = 0, k = 0, cc = 0, par = 0;
       auto wait = [&](uint32_t bar, uint32_t parity) {
         const bool ok = mbar_wait(bar, parity);
         if (!__all_sync(kFull, ok)) failed = true;
@@ -555,45 +573,92 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++k;
         return true;
       };
-      while (left > 0 && !failed) {
+      // Sequences in order, with the own part and the first table entries of the next one and
+      // the length of the one after it on their way, so that a change of sequence waits for
+      // neither.
+      auto len_at = [&](int b) { return b < p.B ? context_len(p, b) : 0; };
+      auto own_at = [&](int b, int len) { return b < p.B ? own_part(p, len, seq_shared(b)) : Own{}; };
+      auto page_end_of = [&](const Own& o) { return (o.L + p.block_size - 1) >> p.bs_log; };
+      auto first_ids = [&](int b, const Own& o) {
+        return o.n > 0 && o.first_page + my_page < page_end_of(o)
+                   ? __ldg(p.block_table + (int64_t)b * p.max_blocks + o.first_page + my_page) : 0;
+      };
+      int e = scan[11], at = r0 - scan[12];  // the element, and where it begins
+      Own own = {}, own1 = {};
+      int ids = 0, ids1 = 0, len2 = 0;
+      auto prime = [&](int b) {  // sequence b becomes the current one
+        const int l0 = len_at(b), l1 = len_at(b + 1);
+        len2 = len_at(b + 2);
+        own = own_at(b, l0);
+        ids = first_ids(b, own);
+        own1 = own_at(b + 1, l1);
+        ids1 = first_ids(b + 1, own1);
+      };
+      auto shift = [&]() {  // the next sequence becomes the current one
+        ++e;
+        own = own1;
+        ids = ids1;
+        own1 = own_at(e - P + 1, len2);
+        ids1 = first_ids(e - P + 1, own1);
+        len2 = len_at(e - P + 2);
+      };
+      if (e >= P) prime(e - P);
+      // (h, tile) or h of the item that r0 falls into
+      int h, tile = 0;
+      {
+        const int off = r0 - at;
+        if (e >= P) {
+          const int c = item_cost(kOwnItem, own.n);
+          h = off / c;
+          at += h * c;
+        } else {
+          const int c = group_cost(e), w = item_cost(kWideItem, group_chunks(e));
+          h = off / c;
+          tile = min((off - h * c) / w, tiles_of(e) - 1);
+          at += h * c + tile * w;
+        }
+      }
+      while (at < r1 && !failed) {
         const bool is_own = e >= P;
-        const int n = min(left, n_item - chunk);
         Seg s;
-        s.n = n;
         s.cc = cc;
-        s.first = chunk == 0;
         s.own = is_own;
-        int page, page_end, n_items;
+        s.h = h;
+        s.par = par;
+        int page, page_end, n_item, kind, tiles = 1;
         if (is_own) {
           s.b0 = e - P;
           s.n_seq = 1;
-          s.h = item;
           s.t_end = own.L;
           s.t_lo = own.first_tok;
           page = own.first_page;
-          page_end = (own.L + p.block_size - 1) / p.block_size;
-          n_items = p.Hkv;
+          page_end = page_end_of(own);
+          n_item = own.n;
+          kind = kOwnItem;
         } else {
-          const int tiles = tiles_of(e);
-          s.h = item / tiles;
-          const int tile = item - s.h * tiles;
+          tiles = tiles_of(e);
           s.b0 = cu[e] + tile * 2 * spt;
           s.n_seq = min(2 * spt, cu[e + 1] - s.b0);
-          s.t_end = shared_pages[e] * p.block_size;
+          s.t_end = shared_pages[e] << p.bs_log;
           s.t_lo = 0;
           page = 0;
           page_end = shared_pages[e];
-          n_items = p.Hkv * tiles;
+          n_item = group_chunks(e);
+          kind = s.n_seq > spt ? kWideItem : kTileItem;
         }
-        s.wide = s.n_seq > spt;
-        s.par = par;
-        if (!s.wide) par ^= n & 1;
-        page += chunk * PPS;
-        s.t0 = page * p.block_size;
-        if (!publish(s)) break;
+        const int chunk = chunk_at(kind, n_item, r0 - at);
+        const int n = chunk_at(kind, n_item, r1 - at) - chunk;
         const int32_t* table = p.block_table + (int64_t)(is_own ? e - P : shared_row[e]) * p.max_blocks;
-        const int my_page = lane % PPS, my_half = lane / PPS;  // PPS * NB <= 32: a box per lane
-        int id = page + my_page < page_end ? __ldg(table + page + my_page) : 0;
+        page += chunk * PPS;
+        int id = ids;
+        if (!is_own || chunk > 0) id = page + my_page < page_end ? __ldg(table + page + my_page) : 0;
+        s.n = n;
+        s.first = chunk == 0;
+        s.wide = kind == kWideItem;
+        s.t0 = page << p.bs_log;
+        if (n > 0) {
+          if (!s.wide) par ^= n & 1;
+          if (!publish(s)) break;
         // the queries
         if (is_own) {
           if (qsmall == 0)  // the tile that the small places are in
@@ -625,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (failed) break;
         for (int c = 0; c < n; ++c) {
           const int np = min(PPS, page_end - page);
-          const int row = (unsigned)id < (unsigned long long)p.num_blocks ? id * p.block_size : out_of_range;
+          const int row = (unsigned)id < (unsigned long long)p.num_blocks ? id << p.bs_log : out_of_range;
           page += PPS;
           if (c + 1 < n) id = page + my_page < page_end ? __ldg(table + page + my_page) : 0;
 #pragma unroll
@@ -642,12 +707,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (failed) break;
         }
+        }
         cc += n;
-        left -= n;
-        chunk = 0;
-        if (left > 0 && ++item == n_items) {
-          item = 0;
-          do { ++e; load_elem(); } while (n_item == 0);
+        // on to the next item
+        at += item_cost(kind, n_item);
+        if (++tile >= tiles) {
+          tile = 0;
+          if (++h == p.Hkv) {
+            h = 0;
+            if (is_own) {
+              shift();
+            } else {
+              while (++e < P && group_chunks(e) * tiles_of(e) == 0) {}
+              if (e == P) prime(0);
+            }
+            while (e >= P && e < n_elem && own.n == 0) shift();
+          }
         }
       }
       Seg end = {};
@@ -949,13 +1024,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // V rows of masked tokens are zeros: 0 times whatever they hold would be no zero
             const int f = 2 * (s.cc + i) + 1, slot = f % kSlots;
             if (!wait(kv_full(slot), (f / kSlots) & 1)) break;
-            if (r < lo || r >= hi) {
 #pragma unroll
-              for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  *reinterpret_cast<uint4*>(base + slot * L::kTile + j * kHalf + r * 128 + q * 16) =
-                      make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < NB; ++j) {
+              uint4* v = reinterpret_cast<uint4*>(base + slot * L::kTile + j * kHalf);
+              for (int q = r; q < lo * 8; q += kT) v[q] = make_uint4(0, 0, 0, 0);
+              for (int q = hi * 8 + r; q < kT * 8; q += kT) v[q] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
@@ -977,52 +1050,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++outs;
         tc_fence_after();
         if (s.own) {
-          // the four warps' parts, 32 dims at a time; every step of it between two meetings
-          float4* part4 = reinterpret_cast<float4*>(base + L::kOffJoin + t * kJoinBytes);  // [4][16][8]
-          float2* ml = reinterpret_cast<float2*>(part4 + 4 * 16 * 8);                      // [4][16]
+          // the four warps' parts, all dims at once (G <= 8) or half of them at a time
+          const int heads = small_rows, dims4 = G > 8 ? D / 8 : D / 4;  // rows and float4s of a round
+          float4* part4 = reinterpret_cast<float4*>(base + L::kOffJoin + t * kJoinBytes);  // [4][heads][dims4]
+          float2* ml = reinterpret_cast<float2*>(base + L::kOffMl) + t * 64;               // [4][16]
           if (row_ok) ml[wq * 16 + lane] = make_float2(m, l);
-          if (!meet()) break;
-          float M = -INFINITY, sum = 0.f;
-          if (row_ok) {
-            float2 v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              v[q] = ml[q * 16 + lane];
-              M = fmaxf(M, v[q].x);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sum += v[q].x == -INFINITY ? 0.f : ex2_ftz(v[q].x - M) * v[q].y;
-          }
-          const float f = m == -INFINITY ? 0.f : ex2_ftz(m - M) / sum;
           const int64_t w0 = s.first ? ws_first(p, true, (int64_t)s.b0 * p.Hq + s.h * G, t)
                                      : ws_next(p, blockIdx.x, cap_rows, t, 0);
           const int w_step = s.first ? 2 : 1;  // workspace rows from one head's to the next one's
-          const int out_r = r >> 3, out_c = r & 7;
 #pragma unroll 1
-          for (int j = 0; j < D / 32; ++j) {
-            float o[32];
-            tmem_ld32(o_addr + j * 32, o);
-            tmem_ld_wait();
-            if (row_ok) {
+          for (int d0 = 0; d0 < D / 4; d0 += dims4) {
+            if (d0 > 0 && !meet()) break;  // the round before is read
+#pragma unroll 1
+            for (int j = 0; j < dims4; j += 8) {
+              float o[32];
+              tmem_ld32(o_addr + (d0 + j) * 4, o);
+              tmem_ld_wait();
+              if (row_ok) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                part4[(wq * 16 + lane) * 8 + (q ^ (lane & 7))] =
-                    make_float4(o[4 * q] * f, o[4 * q + 1] * f, o[4 * q + 2] * f, o[4 * q + 3] * f);
-            }
-            if (!meet()) break;
-            if (out_r < G) {
-              float4 a = part4[out_r * 8 + (out_c ^ (out_r & 7))];
-#pragma unroll
-              for (int q = 1; q < 4; ++q) {
-                const float4 c = part4[(q * 16 + out_r) * 8 + (out_c ^ (out_r & 7))];
-                a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+                for (int q = 0; q < 8; ++q)
+                  part4[(wq * heads + lane) * dims4 + j + (q ^ (lane & 7))] =
+                      make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
               }
-              *reinterpret_cast<float4*>(p.ws_o + (w0 + (int64_t)out_r * w_step) * D + j * 32 + out_c * 4) = a;
             }
             if (!meet()) break;
+            for (int i = r; i < G * dims4; i += kT) {
+              const int g = i / dims4, c = i - g * dims4;
+              float2 v[4];
+              float M = -INFINITY, sum = 0.f;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[q] = ml[q * 16 + g];
+                M = fmaxf(M, v[q].x);
+              }
+              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (v[q].x != -INFINITY) {  // the warp saw tokens
+                  const float f = ex2_ftz(v[q].x - M);
+                  const float4 o = part4[(q * heads + g) * dims4 + (c ^ (g & 7))];
+                  sum = fmaf(f, v[q].y, sum);
+                  a.x = fmaf(f, o.x, a.x), a.y = fmaf(f, o.y, a.y);
+                  a.z = fmaf(f, o.z, a.z), a.w = fmaf(f, o.w, a.w);
+                }
+              }
+              const float inv = 1.f / sum;
+              const int64_t at = w0 + (int64_t)g * w_step;
+              *reinterpret_cast<float4*>(p.ws_o + at * D + (d0 + c) * 4) =
+                  make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+              if (d0 + c == 0) p.ws_lse[at] = M - kShift + log2f(sum);
+            }
           }
           if (failed) break;
-          if (row_ok && wq == 0) p.ws_lse[w] = M - kShift + log2f(sum);
+          // (The next segment's parts are written once its O is complete, which takes all
+          // four warps' weights and so comes after their reads here.)
         } else if (warp_ok) {
           const float inv = 1.f / l;
           float* dst = p.ws_o + w * D;
