@@ -17,18 +17,20 @@
 //
 // Inside a CTA two pipes, each a softmax warpgroup with one TMEM score tile S (128 rows x
 // 128 tokens, fp32), whose columns then hold the weights P (16 bits), and one output tile O:
-//   S = Q . K^T  (Q 128 x D from shared memory, K chunk 128 x D)       tcgen05 kind::f16
+//   S = Q . K^T  (Q 128 x D from shared memory, K 64 or 128 tokens x D)  tcgen05 kind::f16
 //   O += P . V   (P from TMEM, V chunk as an MN-major operand)
 // A wide segment (more than 128 rows) gives each pipe one of its two row tiles, and both
-// read every chunk; in a narrow one the pipes take alternate chunks. A sequence's own item has
-// only G rows: they stand in Q four times, once for the TMEM lanes of each warp of a pipe,
-// and each warp takes a quarter of the chunk's tokens (its P is zero elsewhere), with a
-// maximum and a sum of its own; at the segment's end the four parts are joined through
-// shared memory. The tensor pipe works
-// for one pipe while the other's warpgroup does its softmax: QK^T of step n + 1 is issued
-// before PV of step n, which belongs to the other pipe. One thread owns one row, so maxima and sums need no exchange. The
-// running maximum is only followed when it grows by more than a threshold (2^8 in bf16,
-// 2 in fp16), which spares nearly every rescaling of O; the final division makes up for it.
+// read every chunk; in a narrow one the pipes take alternate chunks. Both work on S in
+// halves of 64 tokens: while the warpgroup turns one half into weights, the tensor pipe
+// multiplies those of the other with V and fills it with the next chunk's scores. (With
+// whole tiles a pipe's chain QK, softmax, PV took 3970 cycles a chunk where its MMAs take
+// 1024.) A sequence's own item has only G rows: they stand in Q four times, once for the
+// TMEM lanes of each warp of a pipe, and each warp takes a quarter of the chunk's tokens (its
+// P is zero elsewhere), with a maximum and a sum of its own; at the segment's end the four
+// parts are joined through shared memory. One thread owns one row, so maxima and sums need
+// no exchange. The running maximum is only followed when it grows by more than a threshold
+// (2^8 in bf16, 2 in fp16), which spares nearly every rescaling of O; the final division
+// makes up for it.
 // In a wide segment P is rounded to 16 bits once: a weight is off by at most 2^-8 (bf16) or
 // 2^-11 (fp16) of itself, as much as the output's own rounding, and the denominator adds
 // the rounded weights, so that they still sum to one and an error is only ever relative to
@@ -113,7 +115,7 @@ struct Layout {
   // segment follows no wide one that still needs it), or at D 64 memory of its own
   static constexpr int kOffJoin = D == 128 ? kOffQ + kTile : kOffQ + 2 * kTile;
   static constexpr int kOffBar = kOffJoin + 2 * kJoinBytes;
-  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 10;
+  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 16;
   static constexpr int kOffMl = kOffBar + kBars * 8;  // [pipe][4 warps][16 rows] maximum and sum
   static constexpr int kOffTmem = kOffMl + 2 * 4 * 16 * 8;
   static constexpr int kOffSeg = kOffTmem + 16;
@@ -182,6 +184,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Whether the phase with the given parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // One lane of the (converged) warp. The compiler knows of elect.sync that a single thread is
@@ -380,11 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBar1 = 2 * kSlots + 2 * kQBars;
   auto seg_full = [&](int s) { return bar0 + 8u * (kBar1 + s); };
   auto seg_empty = [&](int s) { return bar0 + 8u * (kBar1 + kSegRing + s); };
-  auto s_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + t); };
-  auto p_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 + t); };
-  auto o_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 4 + t); };
-  auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 6 + t); };
-  auto joint = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 8 + t); };
+  // of pipe t and half h of its score tile
+  auto s_full = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 * t + h); };
+  auto p_full = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 4 + 2 * t + h); };
+  auto pv_done = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 8 + 2 * t + h); };
+  auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 12 + t); };
+  auto joint = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 14 + t); };
   // small segments' queries: rows 32 w .. 32 w + G - 1 of a tile for w < 4, so that tiles 8
   // (16) rows further in the same memory hold those of four (two) segments
   const int small_rows = p.G > 8 ? 16 : 8, n_small = 32 / small_rows;
@@ -408,9 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(joint(s), 4);
-      mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);
-      mbar_init(o_full(s), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(s_full(s, h), 1);
+        mbar_init(p_full(s, h), 4);
+        mbar_init(pv_done(s, h), 1);
+      }
       mbar_init(o_free(s), 4);
     }
     for (int s = 0; s < kSegRing; ++s) {
@@ -735,128 +752,230 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpMma) {
       // -------------------------------- MMAs --------------------------------
       // One thread does all of it: what it does between two MMAs the tensor pipe, whose queue
-      // is short, waits for.
+      // is short, waits for. So each kind of segment has a loop of its own with little in it.
+      // (One loop over steps of any kind spent 1100 cycles a step on finding out which.)
       if (elect_one()) {
         constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
+        constexpr uint32_t idesc_qk2 = idesc_f16(kT, kT / 2, !FP16, false, false);
         constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
-        // descriptors of the ring's first slot; another place is 16 bytes a unit further
+        constexpr uint32_t kTileU = L::kTile >> 4, kHalfTileU = kHalf / 2 >> 4;  // in descriptor units
+        // descriptors of the ring's first slot and of the first Q tile
         const uint64_t k_desc = sdesc_sw128(base_u32, 16, 1024);
         const uint64_t v_desc = sdesc_sw128(base_u32, kHalf, 1024);
         const uint64_t q_desc = sdesc_sw128(base_u32 + L::kOffQ, 16, 1024);
-        struct Step {
-          int t, kslot, vslot, qslot;
-          uint32_t qoff;         // place of the queries, in descriptor units
-          uint32_t kphase, vphase, qphase;
-          bool start, last;      // first and last step of pipe t in the segment
-          bool q_wait, q_done;   // first and last use of the Q tile
-          bool kv_done;          // last use of the chunk
-          bool two;              // P has two terms
-        };
-        Seg s = {};
-        int i = 0, k = 0, qfill = 0, qsmall = -1;
-        bool second = false;                      // the next step is a wide chunk's second one
-        int kslot = -2;                           // ring slot of the chunk's K
-        uint32_t kphase = 0;
-        int steps[2] = {0, 0}, outs[2] = {0, 0};  // steps and segments of each pipe
+        int slot = 0;             // ring slot of the next chunk's K
+        uint32_t phase = 0;       // and its phase
+        int qfill = 0;            // Q tiles used
+        uint32_t p_phase = 0;     // phases of p_full, bit 2 t + h
+        uint32_t o_used = 0, o_phase = 0;  // bit t: the pipe had a segment; phase of o_free
+        int k = 0;                // segments
+        int par = 0;
         auto wait = [&](uint32_t bar, uint32_t parity) {
           if (!mbar_wait(bar, parity)) failed = true;
           return !failed;
         };
-        auto next = [&](Step& st) {
-          if (i == s.n) {  // the next segment
-            if (!s.own) qfill += s.n == 0 ? 0 : s.wide ? 2 : 1;
-            const int slot = k % kSegRing;
-            if (!wait(seg_full(slot), (k / kSegRing) & 1)) return false;
-            seg_get(seg_ring + slot * kSegInts, s);
-            mbar_arrive(seg_empty(slot));
-            ++k;
-            i = 0;
-            if (s.n == 0) return false;
-            if (s.own) ++qsmall;
+        auto next_slot = [](int& sl, uint32_t& ph) {
+          sl += 2;
+          if (sl >= kSlots) sl -= kSlots, ph ^= 1;
+        };
+        // scores of a half (64 tokens) or all of a chunk
+        auto qk = [&](int t, int h, uint32_t q_off, int sl, uint32_t idesc) {
+          const uint64_t qa = q_desc + q_off, kb = k_desc + (uint32_t)(sl * kTileU + h * kHalfTileU);
+          const uint32_t d = tS(t) + h * (kT / 2);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+            mma_f16_ss(d, qa + o, kb + o, idesc, i > 0 ? 1u : 0u);
           }
-          if (!second) {  // a new chunk
-            kslot += 2;
-            if (kslot >= kSlots) {
-              kslot -= kSlots;
-              kphase ^= 1;
-            }
+          mma_commit(s_full(t, h));
+        };
+        auto v_slot = [&](int sl) { return sl + 1 == kSlots ? 0 : sl + 1; };
+        auto v_wait = [&](int sl, uint32_t ph) {
+          return sl + 1 == kSlots ? wait(kv_full(0), ph ^ 1) : wait(kv_full(sl + 1), ph);
+        };
+        // Pipe t's output tile is free for another segment.
+        auto o_wait = [&](int t) {
+          if ((o_used >> t) & 1) {
+            if (!wait(o_free(t), (o_phase >> t) & 1)) return false;
+            o_phase ^= 1u << t;
           }
-          st.t = (s.par + (s.wide ? (second ? 1 : 0) : i)) & 1;
-          st.start = i < (s.wide ? 1 : 2);
-          st.last = i >= s.n - (s.wide ? 1 : 2);
-          if (s.own) {
-            const int slot = qsmall % n_small;
-            st.qslot = 2 + slot;
-            st.qphase = (qsmall / n_small) & 1;
-            st.qoff = (uint32_t)(slot * small_rows * 128 >> 4);
-          } else {
-            const int q = qfill + (s.wide ? st.t : 0);
-            st.qslot = q & 1;
-            st.qphase = (q >> 1) & 1;
-            st.qoff = (uint32_t)(st.qslot * (L::kTile >> 4));
-          }
-          st.kslot = kslot;
-          st.kphase = kphase;
-          st.vslot = kslot + 1 == kSlots ? 0 : kslot + 1;
-          st.vphase = kslot + 1 == kSlots ? kphase ^ 1 : kphase;
-          st.q_wait = i == 0;
-          st.q_done = i == s.n - 1;
-          st.kv_done = !s.wide || second;
-          st.two = !s.wide;
-          if (s.wide && !second) {
-            second = true;
-          } else {
-            second = false;
-            ++i;
-          }
+          o_used |= 1u << t;
           return true;
         };
-        auto issue_qk = [&](const Step& st) {
-          if (st.q_wait && !wait(q_full(st.qslot), st.qphase)) return;
-          if (!wait(kv_full(st.kslot), st.kphase)) return;
-          tc_fence_after();
-          const uint64_t qa = q_desc + st.qoff;
-          const uint64_t kb = k_desc + (uint32_t)(st.kslot * (L::kTile >> 4));
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            const uint32_t o = ((d >> 2) * kHalf + (d & 3) * 32) >> 4;
-            mma_f16_ss(tS(st.t), qa + o, kb + o, idesc_qk, d > 0 ? 1u : 0u);
-          }
-          mma_commit(s_full(st.t));
-          if (st.kv_done) mma_commit(kv_empty(st.kslot));
-          if (st.q_done) mma_commit(q_empty(st.qslot));
+        auto p_wait = [&](int t, int h) {
+          const int x = 2 * t + h;
+          if (!wait(p_full(t, h), (p_phase >> x) & 1)) return false;
+          p_phase ^= 1u << x;
+          return true;
         };
-        auto issue_pv = [&](const Step& st) {
-          if (!wait(kv_full(st.vslot), st.vphase)) return;
-          if (st.start) {
-            if (outs[st.t] > 0 && !wait(o_free(st.t), (outs[st.t] - 1) & 1)) return;
-            ++outs[st.t];
-          }
-          if (!wait(p_full(st.t), steps[st.t]++ & 1)) return;
-          tc_fence_after();
-          const uint64_t vb = v_desc + (uint32_t)(st.vslot * (L::kTile >> 4));
-          const uint32_t pa = tS(st.t), o = tO(st.t);
+        // kSteps x 16 tokens from half h on, kTerms terms of the weights
+        auto pv = [&](auto steps, auto terms, int t, int h, int vs, bool start) {
+          const uint64_t vb = v_desc + (uint32_t)(vs * kTileU + h * kHalfTileU);
+          const uint32_t pa = tS(t) + h * (kT / 2), o = tO(t);
 #pragma unroll
-          for (int j = 0; j < kT / 16; ++j)
-            mma_f16_ts(o, pa + (j >> 1) * 32 + (j & 1) * 8, vb + (uint32_t)(j * 2048 >> 4), idesc_pv,
-                       st.start && j == 0 ? 0u : 1u);
-          if (st.two) {
+          for (int u = 0; u < decltype(terms)::value; ++u) {
 #pragma unroll
-            for (int j = 0; j < kT / 16; ++j)
-              mma_f16_ts(o, pa + (j >> 1) * 32 + 16 + (j & 1) * 8, vb + (uint32_t)(j * 2048 >> 4), idesc_pv, 1u);
+            for (int j = 0; j < decltype(steps)::value; ++j)
+              mma_f16_ts(o, pa + (j >> 1) * 32 + u * 16 + (j & 1) * 8, vb + (uint32_t)(j * 2048 >> 4), idesc_pv,
+                         u == 0 && j == 0 && start ? 0u : 1u);
           }
-          if (st.last) mma_commit(o_full(st.t));
-          if (st.kv_done) mma_commit(kv_empty(st.vslot));
+          mma_commit(pv_done(t, h));
         };
-        Step st, pend;
-        bool have = false;
-        while (!failed && next(st)) {
-          issue_qk(st);
-          if (have && !failed) issue_pv(pend);
-          pend = st;
-          have = true;
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        using Half = std::integral_constant<int, kT / 32>;
+        using Whole = std::integral_constant<int, kT / 16>;
+        int n = 0;
+        bool own = false;
+        // shared segments, one after the other
+        while (!failed) {
+          const int e = k % kSegRing;
+          if (!wait(seg_full(e), (k / kSegRing) & 1)) break;
+          Seg s;
+          seg_get(seg_ring + e * kSegInts, s);
+          n = s.n, own = s.own, par = s.par;
+          if (n == 0 || own) break;
+          mbar_arrive(seg_empty(e));
+          ++k;
+          if (s.wide) {
+            // steps (pipe, half) in the order (0, 0) (1, 0) (0, 1) (1, 1)
+            const uint32_t q0 = (qfill & 1) * kTileU, q1 = ((qfill + 1) & 1) * kTileU;
+            const int f0 = qfill & 1, f1 = f0 ^ 1;
+            if (!wait(q_full(f0), (qfill >> 1) & 1) || !wait(q_full(f1), ((qfill + 1) >> 1) & 1)) break;
+            qfill += 2;
+            int pslot = slot;
+            uint32_t pphase = phase;
+            if (!wait(kv_full(slot), phase)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) qk(x & 1, x >> 1, x & 1 ? q1 : q0, slot, idesc_qk2);
+            mma_commit(kv_empty(slot));
+            next_slot(slot, phase);
+            for (int i = 0; i < n && !failed; ++i) {
+              const int vs = v_slot(pslot);
+              if (!v_wait(pslot, pphase)) break;
+              const bool more = i + 1 < n;
+#pragma unroll 1
+              for (int x = 0; x < 4; ++x) {
+                const int t = x & 1, h = x >> 1;
+                if (i == 0 && h == 0 && !o_wait(t)) break;
+                if (!p_wait(t, h)) break;
+                tc_fence_after();
+                pv(Half{}, One{}, t, h, vs, i == 0 && h == 0);
+                if (more) {
+                  if (x == 0) {
+                    if (!wait(kv_full(slot), phase)) break;
+                    tc_fence_after();
+                  }
+                  qk(t, h, t ? q1 : q0, slot, idesc_qk2);
+                }
+              }
+              if (failed) break;
+              mma_commit(kv_empty(vs));
+              next_slot(pslot, pphase);
+              if (more) {
+                mma_commit(kv_empty(slot));
+                next_slot(slot, phase);
+              }
+            }
+            mma_commit(q_empty(f0));
+            mma_commit(q_empty(f1));
+          } else {
+            // chunks take the pipes in turns, each in two halves; scores two chunks ahead
+            const int f = qfill & 1;
+            const uint32_t q0 = f * kTileU;
+            if (!wait(q_full(f), (qfill >> 1) & 1)) break;
+            ++qfill;
+            int pslot = slot;
+            uint32_t pphase = phase;
+            for (int i = -2; i < n && !failed; ++i) {
+              const int t = (par + i) & 1, vs = v_slot(pslot);
+              const bool more = i + 2 < n;
+              if (i >= 0 && !v_wait(pslot, pphase)) break;
+              if (i >= 0 && i < 2 && !o_wait(t)) break;
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                if (i >= 0) {
+                  if (!p_wait(t, h)) break;
+                  tc_fence_after();
+                  pv(Half{}, Two{}, t, h, vs, i < 2 && h == 0);
+                }
+                if (more) {
+                  if (h == 0) {
+                    if (!wait(kv_full(slot), phase)) break;
+                    tc_fence_after();
+                  }
+                  qk(t, h, q0, slot, idesc_qk2);
+                }
+              }
+              if (failed) break;
+              if (i >= 0) {
+                mma_commit(kv_empty(vs));
+                next_slot(pslot, pphase);
+              }
+              if (more) {
+                mma_commit(kv_empty(slot));
+                next_slot(slot, phase);
+              }
+            }
+            mma_commit(q_empty(f));
+          }
         }
-        if (have && !failed) issue_pv(pend);
+        // Own segments: whole chunks, the pipes in turns, scores up to two chunks ahead,
+        // beyond the segment's end too (it may have one chunk only). Where the next segment
+        // or its K is not there yet, PV goes first.
+        if (own && !failed) {
+          int kp = k, qleft = 0, vleft = 0, vi = 0, place = -1, pending = 0, tq = par, tp = par;
+          uint32_t place_phase = 0;
+          int pslot = slot;
+          uint32_t pphase = phase;
+          bool end = false;
+          while (!failed) {
+            while (!end && pending < 2) {
+              if (qleft == 0) {
+                const int e = k % kSegRing;
+                const uint32_t parity = (k / kSegRing) & 1;
+                if (pending > 0 ? !mbar_test(seg_full(e), parity) : !wait(seg_full(e), parity)) break;
+                qleft = seg_ring[e * kSegInts];
+                ++k;
+                end = qleft == 0;
+                if (end) break;
+                if (++place == n_small) place = 0, place_phase ^= 1;
+                if (!wait(q_full(2 + place), place_phase)) break;
+              }
+              if (pending > 0 && !mbar_test(kv_full(slot), phase)) break;
+              if (!wait(kv_full(slot), phase)) break;
+              tc_fence_after();
+              qk(tq, 0, (uint32_t)(place * small_rows * 128 >> 4), slot, idesc_qk);
+              mma_commit(kv_empty(slot));
+              if (--qleft == 0) mma_commit(q_empty(2 + place));
+              next_slot(slot, phase);
+              tq ^= 1;
+              ++pending;
+            }
+            if (failed || pending == 0) break;
+            if (vleft == 0) {
+              const int e = kp % kSegRing;
+              vleft = seg_ring[e * kSegInts];
+              mbar_arrive(seg_empty(e));
+              ++kp;
+              vi = 0;
+            }
+            const int vs = v_slot(pslot);
+            if (!v_wait(pslot, pphase)) break;
+            if (vi < 2 && !o_wait(tp)) break;
+            if (!p_wait(tp, 0)) break;
+            tc_fence_after();
+            pv(Whole{}, Two{}, tp, 0, vs, vi < 2);
+            mma_commit(kv_empty(vs));
+            next_slot(pslot, pphase);
+            tp ^= 1;
+            ++vi;
+            --vleft;
+            --pending;
+          }
+        }
+        // (nobody waits for the last descriptor to be read)
       }
       failed = __any_sync(kFull, failed);
     } else {
@@ -868,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr float kGrow = FP16 ? 1.f : 8.f;     // log2 of the growth that is let pass
       constexpr float kShift = FP16 ? 14.f : 0.f;   // log2 of the weights' factor
       const int cap_rows = ws_cap(p);
-      int steps = 0, outs = 0;
+      uint32_t s_phase[2] = {0, 0};  // of the halves of S; PV of the same steps completes in them too
       auto wait = [&](uint32_t bar, uint32_t parity) {
         const bool ok = mbar_wait(bar, parity);
         if (!__all_sync(kFull, ok)) failed = true;
@@ -918,124 +1037,105 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         int done = 0;  // steps of this pipe in the segment
-        for (int i = s.wide ? 0 : s.par ^ t; i < s.n; i += s.wide ? 1 : 2) {
+        // Follows the running maximum once the largest score has outgrown it.
+        auto follow = [&](float top) {
+          if (__any_sync(kFull, row_ok && top > m + kGrow)) {
+            const float mn = fmaxf(m, top);
+            const float alpha = m == mn ? 1.f : ex2_ftz(m - mn);
+            m = mn;
+            l *= alpha;
+            if (done > 0) {  // O has to be complete: PV of the step before
+              const int h = s.own ? 0 : (done - 1) & 1;
+              if (!wait(pv_done(t, h), s_phase[h] ^ 1)) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int j = 0; j < D / 32; ++j) {
+                float o[32];
+                tmem_ld32(o_addr + j * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 32; ++q) o[q] *= alpha;
+                tmem_st32(o_addr + j * 32, o);
+              }
+            }
+          }
+        };
+        for (int i = s.wide ? 0 : s.par ^ t; i < s.n && !failed; i += s.wide ? 1 : 2) {
           const int t0 = s.t0 + i * kT;
           const int lo = max(0, s.t_lo - t0), hi = min(kT, s.t_end - t0);  // valid tokens of the chunk
           const bool part = lo > 0 || hi < kT;
-          if (!wait(s_full(t), steps & 1)) break;
-          ++steps;
-          tc_fence_after();
-          // Follows the running maximum once the chunk's largest score has outgrown it.
-          auto follow = [&](float top) {
-            if (__any_sync(kFull, row_ok && top > m + kGrow)) {
-              const float mn = fmaxf(m, top);
-              const float alpha = m == mn ? 1.f : ex2_ftz(m - mn);
-              m = mn;
-              l *= alpha;
-              if (done > 0) {  // O of the steps before is complete: its MMAs precede this S
+          const float far = far0 + (float)(i * kT);
 #pragma unroll 1
-                for (int j = 0; j < D / 32; ++j) {
-                  float o[32];
-                  tmem_ld32(o_addr + j * 32, o);
-                  tmem_ld_wait();
+          for (int h = 0; h < (s.own ? 1 : 2); ++h) {
+            if (!wait(s_full(t, h), s_phase[h])) break;
+            tc_fence_after();
+            if (s.own) {
+              // All 128 columns at once, 32 of them here.
+              const int j = wq * 32;
+              float x[32];
+              tmem_ld32(s_addr + j, x);
+              tmem_ld_wait();
+              scores(x, far + (float)j, part, lo - j, hi - j);
+              follow(max32(x));
+              uint64_t sum2 = f32x2(0.f, 0.f);
+              weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum2);
 #pragma unroll
-                  for (int q = 0; q < 32; ++q) o[q] *= alpha;
-                  tmem_st32(o_addr + j * 32, o);
-                }
-              }
-            }
-          };
-          if (s.own) {
-            const int j = wq * 32;
-            float x[32];
-            tmem_ld32(s_addr + j, x);
-            tmem_ld_wait();
-            scores(x, far0 + (float)(i * kT + j), part, lo - j, hi - j);
-            follow(max32(x));
-            uint64_t sum2 = f32x2(0.f, 0.f);
-            weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum2);
-#pragma unroll
-            for (int q = 0; q < 32; ++q) x[q] = 0.f;
+              for (int q = 0; q < 32; ++q) x[q] = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < kT; c += 32)
-              if (c != j) tmem_st32(s_addr + c, x);
-            l += f32x2_sum(sum2);
-            tmem_st_wait();
-          } else if (warp_ok) {
-            // Two passes over S in TMEM, in blocks of 32 columns: the maximum, then the
-            // weights. (All 128 columns in registers unrolled to 30 KB of code, and eight
-            // warps on their own ways through it waited for instructions: 173 us for 128
-            // sequences of 64/8 heads behind 16384 tokens.)
-            float qs = p.qscale;
-            float top = -INFINITY;
-            if (MOD || part) {
-              // scores in base-2 units, masked tokens -inf, back into TMEM
-#pragma unroll 1
-              for (int j = 0; j < kT; j += 32) {
-                float x[32];
-                tmem_ld32(s_addr + j, x);
-                tmem_ld_wait();
-                scores(x, far0 + (float)(i * kT + j), part, lo - j, hi - j);
-                tmem_st32(s_addr + j, x);
-                top = fmaxf(top, max32(x));
-              }
+              for (int c = 0; c < kT; c += 32)
+                if (c != j) tmem_st32(s_addr + c, x);
+              l += f32x2_sum(sum2);
               tmem_st_wait();
-              qs = 1.f;
-            } else {
-              // of the scaled scores: a negative scale turns the order around
-              const float sign = qs < 0.f ? -1.f : 1.f;
-#pragma unroll 1
-              for (int j = 0; j < kT; j += 64) {
-                float x[64];
-                tmem_ld32(s_addr + j, x);
-                tmem_ld32(s_addr + j + 32, x + 32);
-                tmem_ld_wait();
-                if (sign < 0.f) {
+            } else if (warp_ok) {
+              // Half the columns. (All 128 in registers, with the code that this unrolls to,
+              // left eight warps waiting for instructions.)
+              const int j = h * (kT / 2);
+              float x[64];
+              tmem_ld32(s_addr + j, x);
+              tmem_ld32(s_addr + j + 32, x + 32);
+              tmem_ld_wait();
+              float qs = p.qscale, top;
+              if (MOD || part) {
+                scores(x, far + (float)j, part, lo - j, hi - j);
+                scores(x + 32, far + (float)(j + 32), part, lo - j - 32, hi - j - 32);
+                qs = 1.f;
+              } else if (qs < 0.f) {  // the largest scaled score is the least product's
 #pragma unroll
-                  for (int q = 0; q < 64; ++q) x[q] = -x[q];
-                }
-                top = fmaxf(top, fmaxf(max32(x), max32(x + 32)));
+                for (int q = 0; q < 64; ++q) x[q] = -x[q];
+                qs = -qs;
               }
-              top *= sign * qs;
+              top = fmaxf(max32(x), max32(x + 32)) * qs;
+              follow(top);
+              const uint64_t qs2 = f32x2(qs, qs), neg2 = shift(m);
+              uint64_t sum2 = f32x2(0.f, 0.f);
+              if (s.wide) {
+                weights<FP16, false>(s_addr + j, x, qs2, neg2, sum2);
+                weights<FP16, false>(s_addr + j + 32, x + 32, qs2, neg2, sum2);
+              } else {
+                weights<FP16, true>(s_addr + j, x, qs2, neg2, sum2);
+                weights<FP16, true>(s_addr + j + 32, x + 32, qs2, neg2, sum2);
+              }
+              l += f32x2_sum(sum2);
+              tmem_st_wait();
             }
-            follow(top);
-            const uint64_t qs2 = f32x2(qs, qs), neg2 = shift(m);
-            uint64_t sum2 = f32x2(0.f, 0.f);
-            auto all_weights = [&](auto two) {
-              constexpr bool kTwo = decltype(two)::value;
-              float xa[32], xb[32];
-              tmem_ld32(s_addr, xa);
-#pragma unroll 1
-              for (int j = 0; j < kT; j += 64) {
-                tmem_ld_wait();
-                tmem_ld32(s_addr + j + 32, xb);
-                weights<FP16, kTwo>(s_addr + j, xa, qs2, neg2, sum2);
-                tmem_ld_wait();
-                if (j == 0) tmem_ld32(s_addr + 64, xa);
-                weights<FP16, kTwo>(s_addr + j + 32, xb, qs2, neg2, sum2);
-              }
-            };
-            if (s.wide) all_weights(std::false_type{});
-            else all_weights(std::true_type{});
-            l += f32x2_sum(sum2);
-            tmem_st_wait();
-          }
-          if (part && (!s.wide || t == s.par)) {
-            // V rows of masked tokens are zeros: 0 times whatever they hold would be no zero
-            const int f = 2 * (s.cc + i) + 1, slot = f % kSlots;
-            if (!wait(kv_full(slot), (f / kSlots) & 1)) break;
+            if (part && h == 0 && (!s.wide || t == 0)) {
+              // V rows of masked tokens are zeros: 0 times whatever they hold would be no zero
+              const int f = 2 * (s.cc + i) + 1, slot = f % kSlots;
+              if (!wait(kv_full(slot), (f / kSlots) & 1)) break;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              uint4* v = reinterpret_cast<uint4*>(base + slot * L::kTile + j * kHalf);
-              for (int q = r; q < lo * 8; q += kT) v[q] = make_uint4(0, 0, 0, 0);
-              for (int q = hi * 8 + r; q < kT * 8; q += kT) v[q] = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < NB; ++j) {
+                uint4* v = reinterpret_cast<uint4*>(base + slot * L::kTile + j * kHalf);
+                for (int q = r; q < lo * 8; q += kT) v[q] = make_uint4(0, 0, 0, 0);
+                for (int q = hi * 8 + r; q < kT * 8; q += kT) v[q] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(t, h));
+            s_phase[h] ^= 1;
+            ++done;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(t));
-          ++done;
         }
         if (failed) break;
         // the segment's partial of this row
@@ -1046,8 +1146,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok && (!s.own || wq == 0)) p.ws_lse[w] = -INFINITY;
           continue;
         }
-        if (!wait(o_full(t), outs & 1)) break;
-        ++outs;
+        {
+          const int h = s.own ? 0 : 1;  // of the last step
+          if (!wait(pv_done(t, h), s_phase[h] ^ 1)) break;
+        }
         tc_fence_after();
         if (s.own) {
           // the four warps' parts, all dims at once (G <= 8) or half of them at a time
