@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cc += n;
         // on to the next item
         at += item_cost(kind, n_item);
-        if (++tile >= tiles) {
+        if (at < r1 && ++tile >= tiles) {
           tile = 0;
           if (++h == p.Hkv) {
             h = 0;
@@ -738,7 +738,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               while (++e < P && group_chunks(e) * tiles_of(e) == 0) {}
               if (e == P) prime(0);
             }
-            while (e >= P && e < n_elem && own.n == 0) shift();
+            if (e >= P && own.n == 0) {  // the first sequence from here on that has chunks
+              int b = e - P;
+              unsigned some;
+              do {
+                ++b;
+                some = __ballot_sync(kFull, own_at(b + lane, len_at(b + lane)).n > 0);
+                b += some ? __ffs(some) - 1 : 31;
+              } while (!some && b + 1 < p.B);
+              e = P + b;
+              prime(b);
+            }
           }
         }
       }
@@ -751,67 +761,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(q_empty(2 + i % n_small), (i / n_small) & 1);
     } else if (warp == kWarpMma) {
       // -------------------------------- MMAs --------------------------------
-      // One thread does all of it: what it does between two MMAs the tensor pipe, whose queue
-      // is short, waits for. So each kind of segment has a loop of its own with little in it.
-      // (One loop over steps of any kind spent 1100 cycles a step on finding out which.)
-      if (elect_one()) {
-        constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
-        constexpr uint32_t idesc_qk2 = idesc_f16(kT, kT / 2, !FP16, false, false);
-        constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
-        constexpr uint32_t kTileU = L::kTile >> 4, kHalfTileU = kHalf / 2 >> 4;  // in descriptor units
-        // descriptors of the ring's first slot and of the first Q tile
-        const uint64_t k_desc = sdesc_sw128(base_u32, 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(base_u32, kHalf, 1024);
-        const uint64_t q_desc = sdesc_sw128(base_u32 + L::kOffQ, 16, 1024);
-        int slot = 0;             // ring slot of the next chunk's K
-        uint32_t phase = 0;       // and its phase
-        int qfill = 0;            // Q tiles used
-        uint32_t p_phase = 0;     // phases of p_full, bit 2 t + h
-        uint32_t o_used = 0, o_phase = 0;  // bit t: the pipe had a segment; phase of o_free
-        int k = 0;                // segments
-        int par = 0;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (!mbar_wait(bar, parity)) failed = true;
-          return !failed;
-        };
-        auto next_slot = [](int& sl, uint32_t& ph) {
-          sl += 2;
-          if (sl >= kSlots) sl -= kSlots, ph ^= 1;
-        };
-        // scores of a half (64 tokens) or all of a chunk
-        auto qk = [&](int t, int h, uint32_t q_off, int sl, uint32_t idesc) {
-          const uint64_t qa = q_desc + q_off, kb = k_desc + (uint32_t)(sl * kTileU + h * kHalfTileU);
-          const uint32_t d = tS(t) + h * (kT / 2);
+      // What the warp does between two MMAs the tensor pipe, whose queue is short, waits for.
+      // So each kind of segment has a loop of its own with little in it, and everything that
+      // ends up in an MMA's operands is the same for the whole warp in the compiler's eyes too
+      // (uniform registers, no branch on the outcome of a wait): a thread's own descriptors
+      // cost 650 cycles a step on their way to the tensor pipe. After a wait that ran out,
+      // the rest is walked through without waiting.
+      constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
+      constexpr uint32_t idesc_qk2 = idesc_f16(kT, kT / 2, !FP16, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
+      constexpr uint32_t kTileU = L::kTile >> 4, kHalfTileU = kHalf / 2 >> 4;  // in descriptor units
+      // descriptors of the ring's first slot and of the first Q tile
+      const uint64_t k_desc = sdesc_sw128(base_u32, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(base_u32, kHalf, 1024);
+      const uint64_t q_desc = sdesc_sw128(base_u32 + L::kOffQ, 16, 1024);
+      int slot = 0;             // ring slot of the next chunk's K
+      uint32_t phase = 0;       // and its phase
+      int qfill = 0;            // Q tiles used
+      uint32_t p_phase = 0;     // phases of p_full, bit 2 t + h
+      uint32_t o_used = 0, o_phase = 0;  // bit t: the pipe had a segment; phase of o_free
+      int k = 0;                // segments
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!failed && !mbar_wait(bar, parity)) failed = true;
+      };
+      auto next_slot = [](int& sl, uint32_t& ph) {
+        const int up = sl + 2 >= kSlots;
+        sl += 2 - up * kSlots;
+        ph ^= (uint32_t)up;
+      };
+      auto commit = [&](uint32_t bar) {
+        if (elect_one()) mma_commit(bar);
+      };
+      // scores of a half (64 tokens) or all of a chunk
+      auto qk = [&](int t, int h, uint32_t q_off, int sl, uint32_t idesc) {
+        const uint64_t qa = q_desc + q_off, kb = k_desc + (uint32_t)(sl * kTileU + h * kHalfTileU);
+        const uint32_t d = tS(t) + h * (kT / 2);
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
             mma_f16_ss(d, qa + o, kb + o, idesc, i > 0 ? 1u : 0u);
           }
           mma_commit(s_full(t, h));
-        };
-        auto v_slot = [&](int sl) { return sl + 1 == kSlots ? 0 : sl + 1; };
-        auto v_wait = [&](int sl, uint32_t ph) {
-          return sl + 1 == kSlots ? wait(kv_full(0), ph ^ 1) : wait(kv_full(sl + 1), ph);
-        };
-        // Pipe t's output tile is free for another segment.
-        auto o_wait = [&](int t) {
-          if ((o_used >> t) & 1) {
-            if (!wait(o_free(t), (o_phase >> t) & 1)) return false;
-            o_phase ^= 1u << t;
-          }
-          o_used |= 1u << t;
-          return true;
-        };
-        auto p_wait = [&](int t, int h) {
-          const int x = 2 * t + h;
-          if (!wait(p_full(t, h), (p_phase >> x) & 1)) return false;
-          p_phase ^= 1u << x;
-          return true;
-        };
-        // kSteps x 16 tokens from half h on, kTerms terms of the weights
-        auto pv = [&](auto steps, auto terms, int t, int h, int vs, bool start) {
-          const uint64_t vb = v_desc + (uint32_t)(vs * kTileU + h * kHalfTileU);
-          const uint32_t pa = tS(t) + h * (kT / 2), o = tO(t);
+        }
+      };
+      auto v_slot = [&](int sl) { return sl + 1 == kSlots ? 0 : sl + 1; };
+      auto v_wait = [&](int sl, uint32_t ph) {
+        wait(kv_full(v_slot(sl)), sl + 1 == kSlots ? ph ^ 1 : ph);
+      };
+      // Pipe t's output tile is free for another segment.
+      auto o_wait = [&](int t) {
+        if ((o_used >> t) & 1) {
+          wait(o_free(t), (o_phase >> t) & 1);
+          o_phase ^= 1u << t;
+        }
+        o_used |= 1u << t;
+      };
+      auto p_wait = [&](int t, int h) {
+        const int x = 2 * t + h;
+        wait(p_full(t, h), (p_phase >> x) & 1);
+        p_phase ^= 1u << x;
+      };
+      // steps x 16 tokens from half h on, `terms` terms of the weights
+      auto pv = [&](auto steps, auto terms, int t, int h, int vs, bool start) {
+        const uint64_t vb = v_desc + (uint32_t)(vs * kTileU + h * kHalfTileU);
+        const uint32_t pa = tS(t) + h * (kT / 2), o = tO(t);
+        if (elect_one()) {
 #pragma unroll
           for (int u = 0; u < decltype(terms)::value; ++u) {
 #pragma unroll
@@ -820,162 +835,165 @@ __global__ void __launch_bounds__(kThreads, 1)
                          u == 0 && j == 0 && start ? 0u : 1u);
           }
           mma_commit(pv_done(t, h));
-        };
-        using One = std::integral_constant<int, 1>;
-        using Two = std::integral_constant<int, 2>;
-        using Half = std::integral_constant<int, kT / 32>;
-        using Whole = std::integral_constant<int, kT / 16>;
-        int n = 0;
-        bool own = false;
-        // shared segments, one after the other
-        while (!failed) {
-          const int e = k % kSegRing;
-          if (!wait(seg_full(e), (k / kSegRing) & 1)) break;
-          Seg s;
-          seg_get(seg_ring + e * kSegInts, s);
-          n = s.n, own = s.own, par = s.par;
-          if (n == 0 || own) break;
-          mbar_arrive(seg_empty(e));
-          ++k;
-          if (s.wide) {
-            // steps (pipe, half) in the order (0, 0) (1, 0) (0, 1) (1, 1)
-            const uint32_t q0 = (qfill & 1) * kTileU, q1 = ((qfill + 1) & 1) * kTileU;
-            const int f0 = qfill & 1, f1 = f0 ^ 1;
-            if (!wait(q_full(f0), (qfill >> 1) & 1) || !wait(q_full(f1), ((qfill + 1) >> 1) & 1)) break;
-            qfill += 2;
-            int pslot = slot;
-            uint32_t pphase = phase;
-            if (!wait(kv_full(slot), phase)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < 4; ++x) qk(x & 1, x >> 1, x & 1 ? q1 : q0, slot, idesc_qk2);
-            mma_commit(kv_empty(slot));
-            next_slot(slot, phase);
-            for (int i = 0; i < n && !failed; ++i) {
-              const int vs = v_slot(pslot);
-              if (!v_wait(pslot, pphase)) break;
-              const bool more = i + 1 < n;
-#pragma unroll 1
-              for (int x = 0; x < 4; ++x) {
-                const int t = x & 1, h = x >> 1;
-                if (i == 0 && h == 0 && !o_wait(t)) break;
-                if (!p_wait(t, h)) break;
-                tc_fence_after();
-                pv(Half{}, One{}, t, h, vs, i == 0 && h == 0);
-                if (more) {
-                  if (x == 0) {
-                    if (!wait(kv_full(slot), phase)) break;
-                    tc_fence_after();
-                  }
-                  qk(t, h, t ? q1 : q0, slot, idesc_qk2);
-                }
-              }
-              if (failed) break;
-              mma_commit(kv_empty(vs));
-              next_slot(pslot, pphase);
-              if (more) {
-                mma_commit(kv_empty(slot));
-                next_slot(slot, phase);
-              }
-            }
-            mma_commit(q_empty(f0));
-            mma_commit(q_empty(f1));
-          } else {
-            // chunks take the pipes in turns, each in two halves; scores two chunks ahead
-            const int f = qfill & 1;
-            const uint32_t q0 = f * kTileU;
-            if (!wait(q_full(f), (qfill >> 1) & 1)) break;
-            ++qfill;
-            int pslot = slot;
-            uint32_t pphase = phase;
-            for (int i = -2; i < n && !failed; ++i) {
-              const int t = (par + i) & 1, vs = v_slot(pslot);
-              const bool more = i + 2 < n;
-              if (i >= 0 && !v_wait(pslot, pphase)) break;
-              if (i >= 0 && i < 2 && !o_wait(t)) break;
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                if (i >= 0) {
-                  if (!p_wait(t, h)) break;
-                  tc_fence_after();
-                  pv(Half{}, Two{}, t, h, vs, i < 2 && h == 0);
-                }
-                if (more) {
-                  if (h == 0) {
-                    if (!wait(kv_full(slot), phase)) break;
-                    tc_fence_after();
-                  }
-                  qk(t, h, q0, slot, idesc_qk2);
-                }
-              }
-              if (failed) break;
-              if (i >= 0) {
-                mma_commit(kv_empty(vs));
-                next_slot(pslot, pphase);
-              }
-              if (more) {
-                mma_commit(kv_empty(slot));
-                next_slot(slot, phase);
-              }
-            }
-            mma_commit(q_empty(f));
-          }
         }
-        // Own segments: whole chunks, the pipes in turns, scores up to two chunks ahead,
-        // beyond the segment's end too (it may have one chunk only). Where the next segment
-        // or its K is not there yet, PV goes first.
-        if (own && !failed) {
-          int kp = k, qleft = 0, vleft = 0, vi = 0, place = -1, pending = 0, tq = par, tp = par;
-          uint32_t place_phase = 0;
-          int pslot = slot;
-          uint32_t pphase = phase;
-          bool end = false;
-          while (!failed) {
-            while (!end && pending < 2) {
-              if (qleft == 0) {
-                const int e = k % kSegRing;
-                const uint32_t parity = (k / kSegRing) & 1;
-                if (pending > 0 ? !mbar_test(seg_full(e), parity) : !wait(seg_full(e), parity)) break;
-                qleft = seg_ring[e * kSegInts];
-                ++k;
-                end = qleft == 0;
-                if (end) break;
-                if (++place == n_small) place = 0, place_phase ^= 1;
-                if (!wait(q_full(2 + place), place_phase)) break;
-              }
-              if (pending > 0 && !mbar_test(kv_full(slot), phase)) break;
-              if (!wait(kv_full(slot), phase)) break;
-              tc_fence_after();
-              qk(tq, 0, (uint32_t)(place * small_rows * 128 >> 4), slot, idesc_qk);
-              mma_commit(kv_empty(slot));
-              if (--qleft == 0) mma_commit(q_empty(2 + place));
-              next_slot(slot, phase);
-              tq ^= 1;
-              ++pending;
-            }
-            if (failed || pending == 0) break;
-            if (vleft == 0) {
-              const int e = kp % kSegRing;
-              vleft = seg_ring[e * kSegInts];
-              mbar_arrive(seg_empty(e));
-              ++kp;
-              vi = 0;
-            }
+      };
+      using One = std::integral_constant<int, 1>;
+      using Two = std::integral_constant<int, 2>;
+      using Half = std::integral_constant<int, kT / 32>;
+      using Whole = std::integral_constant<int, kT / 16>;
+      int n = 0, own = 0, par = 0;
+      auto seg_int = [&](int e, int i) { return __shfl_sync(kFull, seg_ring[e * kSegInts + i], 0); };
+      // shared segments, one after the other
+      while (true) {
+        const int e = k % kSegRing;
+        wait(seg_full(e), (k / kSegRing) & 1);
+        if (__any_sync(kFull, failed)) break;
+        n = seg_int(e, 0), own = seg_int(e, 9), par = seg_int(e, 11);
+        const int wide = seg_int(e, 1);
+        if (n == 0 || own) break;
+        if (lane == 0) mbar_arrive(seg_empty(e));
+        __syncwarp();
+        ++k;
+        int pslot = slot;
+        uint32_t pphase = phase;
+        if (wide) {
+          // steps (pipe, half) in the order (0, 0) (1, 0) (0, 1) (1, 1)
+          const int f0 = qfill & 1, f1 = f0 ^ 1;
+          const uint32_t q0 = f0 * kTileU, q1 = f1 * kTileU;
+          wait(q_full(f0), (qfill >> 1) & 1);
+          wait(q_full(f1), ((qfill + 1) >> 1) & 1);
+          qfill += 2;
+          wait(kv_full(slot), phase);
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) qk(x & 1, x >> 1, x & 1 ? q1 : q0, slot, idesc_qk2);
+          commit(kv_empty(slot));
+          next_slot(slot, phase);
+          for (int i = 0; i < n; ++i) {
             const int vs = v_slot(pslot);
-            if (!v_wait(pslot, pphase)) break;
-            if (vi < 2 && !o_wait(tp)) break;
-            if (!p_wait(tp, 0)) break;
-            tc_fence_after();
-            pv(Whole{}, Two{}, tp, 0, vs, vi < 2);
-            mma_commit(kv_empty(vs));
+            v_wait(pslot, pphase);
+            const bool more = i + 1 < n;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int t = x & 1, h = x >> 1;
+              if (i == 0 && h == 0) o_wait(t);
+              p_wait(t, h);
+              tc_fence_after();
+              pv(Half{}, One{}, t, h, vs, i == 0 && h == 0);
+              if (more) {
+                if (x == 0) {
+                  wait(kv_full(slot), phase);
+                  tc_fence_after();
+                }
+                qk(t, h, t ? q1 : q0, slot, idesc_qk2);
+              }
+            }
+            commit(kv_empty(vs));
             next_slot(pslot, pphase);
-            tp ^= 1;
-            ++vi;
-            --vleft;
-            --pending;
+            if (more) {
+              commit(kv_empty(slot));
+              next_slot(slot, phase);
+            }
           }
+          commit(q_empty(f0));
+          commit(q_empty(f1));
+        } else {
+          // chunks take the pipes in turns, each in two halves; scores two chunks ahead
+          const int f = qfill & 1;
+          const uint32_t q0 = f * kTileU;
+          wait(q_full(f), (qfill >> 1) & 1);
+          ++qfill;
+          for (int i = -2; i < n; ++i) {
+            const int t = (par + i) & 1, vs = v_slot(pslot);
+            const bool more = i + 2 < n;
+            if (i >= 0) v_wait(pslot, pphase);
+            if (i >= 0 && i < 2) o_wait(t);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (i >= 0) {
+                p_wait(t, h);
+                tc_fence_after();
+                pv(Half{}, Two{}, t, h, vs, i < 2 && h == 0);
+              }
+              if (more) {
+                if (h == 0) {
+                  wait(kv_full(slot), phase);
+                  tc_fence_after();
+                }
+                qk(t, h, q0, slot, idesc_qk2);
+              }
+            }
+            if (i >= 0) {
+              commit(kv_empty(vs));
+              next_slot(pslot, pphase);
+            }
+            if (more) {
+              commit(kv_empty(slot));
+              next_slot(slot, phase);
+            }
+          }
+          commit(q_empty(f));
         }
-        // (nobody waits for the last descriptor to be read)
+      }
+      // Own segments: whole chunks, the pipes in turns, scores up to two chunks ahead,
+      // beyond the segment's end too (it may have one chunk only). Where the next segment
+      // or its K is not there yet, PV goes first.
+      if (own && !__any_sync(kFull, failed)) {
+        int kp = k, qleft = 0, vleft = 0, vi = 0, place = -1, pending = 0, tq = par, tp = par;
+        uint32_t place_phase = 0;
+        int pslot = slot;
+        uint32_t pphase = phase;
+        bool end = false;
+        auto ready = [&](uint32_t bar, uint32_t parity) {  // waits if there is nothing else to do
+          if (pending > 0) return (bool)__all_sync(kFull, mbar_test(bar, parity));
+          wait(bar, parity);
+          return true;
+        };
+        while (true) {
+          while (!end && pending < 2) {
+            if (qleft == 0) {
+              const int e = k % kSegRing;
+              if (!ready(seg_full(e), (k / kSegRing) & 1) || __any_sync(kFull, failed)) break;
+              qleft = seg_int(e, 0);
+              ++k;
+              end = qleft == 0;
+              if (end) break;
+              if (++place == n_small) place = 0, place_phase ^= 1;
+              wait(q_full(2 + place), place_phase);
+            }
+            if (!ready(kv_full(slot), phase)) break;
+            tc_fence_after();
+            const int sl = __shfl_sync(kFull, slot, 0), t = __shfl_sync(kFull, tq, 0);
+            const int at = __shfl_sync(kFull, place * small_rows * 128 >> 4, 0);
+            qk(t, 0, (uint32_t)at, sl, idesc_qk);
+            commit(kv_empty(sl));
+            if (--qleft == 0) commit(q_empty(2 + place));
+            next_slot(slot, phase);
+            tq ^= 1;
+            ++pending;
+          }
+          if (pending == 0 || __any_sync(kFull, failed)) break;
+          if (vleft == 0) {
+            const int e = kp % kSegRing;
+            vleft = seg_int(e, 0);
+            if (lane == 0) mbar_arrive(seg_empty(e));
+            __syncwarp();
+            ++kp;
+            vi = 0;
+          }
+          v_wait(pslot, pphase);
+          if (vi < 2) o_wait(tp);
+          p_wait(tp, 0);
+          tc_fence_after();
+          const int vs = __shfl_sync(kFull, v_slot(pslot), 0), t = __shfl_sync(kFull, tp, 0);
+          pv(Whole{}, Two{}, t, 0, vs, vi < 2);
+          commit(kv_empty(vs));
+          next_slot(pslot, pphase);
+          tp ^= 1;
+          ++vi;
+          --vleft;
+          --pending;
+        }
       }
       failed = __any_sync(kFull, failed);
     } else {
