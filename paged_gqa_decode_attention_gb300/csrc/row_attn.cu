@@ -6,8 +6,9 @@
 // log-sum-exps lse_i,
 //   M = max_i lse_i,  out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M)
 // (an empty partial has lse_i = -inf and is not read). Which ones those are follows from
-// the plan that the first kernel left (SeqPlan). One warp a row while there are many rows;
-// four that take the partials in turns where a warp each would leave the GPU empty.
+// the plan that the first kernel left (SeqPlan): a lane each works out where one is. One warp
+// a row while there are many rows; four that take the partials in turns where a warp each
+// would leave the GPU empty.
 #include "row_attn_kernel.cuh"
 
 namespace pda {
@@ -57,7 +58,7 @@ __device__ __forceinline__ Part part_of(const Params& p, int64_t row, int kind, 
 template <int D, bool FP16, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Params p) {
   constexpr int V = D / 32;   // dims of a lane
-  constexpr int U = 4;        // partials in flight
+  constexpr int U = 8;        // partials in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.B * p.Hq;
   const int row = WPR == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x;
@@ -78,43 +79,54 @@ __global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Param
   float M = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int i0 = sub * U; i0 < n; i0 += WPR * U) {
-    float l[U], o[U][V];
+  // 32 partials at a time, one a lane: where it is and what it weighs
+  for (int i0 = sub; i0 < n; i0 += 32 * WPR) {
+    const int i = i0 + lane * WPR;
+    int64_t at = -1;
+    if (i < n) at = i < pre.n ? pre.at(i) : own.at(i - pre.n);
+    const float l = at >= 0 ? __ldcg(p.ws_lse + at) : -INFINITY;
+    unsigned used = __ballot_sync(kFull, l != -INFINITY);
+    if (used == 0) continue;
+    float top = l;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      l[u] = -INFINITY;
-      if (i0 + u < n) {
-        const int i = i0 + u;
-        const int64_t at = i < pre.n ? pre.at(i) : own.at(i - pre.n);
-        if (at < 0) continue;
-        l[u] = __ldcg(p.ws_lse + at);
-        const float* src = p.ws_o + at * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-          o[u][0] = f.x, o[u][1] = f.y, o[u][2] = f.z, o[u][3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-          o[u][0] = f.x, o[u][1] = f.y;
-        }
-      }
-    }
-    float Mn = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, l[u]);
-    if (Mn == -INFINITY) Mn = 0.f;  // only empty partials (or NaN) so far
-    const float a = exp2f(M - Mn);
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    const float Mn = fmaxf(M, top);
+    const float a = M == Mn ? 1.f : exp2f(M - Mn);
     sum *= a;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= a;
     M = Mn;
+    const float w = l == -INFINITY ? 0.f : exp2f(l - M);
+    float ws = w;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (l[u] != -INFINITY) {
-        const float w = exp2f(l[u] - M);
-        sum += w;
+    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(kFull, ws, off);
+    sum += ws;
+    while (used) {
+      float o[U][V], wu[U];
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[u][v], acc[v]);
+      for (int u = 0; u < U; ++u) {
+        wu[u] = 0.f;
+        if (used) {
+          const int j = __ffs(used) - 1;
+          used &= used - 1;
+          wu[u] = __shfl_sync(kFull, w, j);
+          const float* src = p.ws_o + __shfl_sync(kFull, at, j) * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+            o[u][0] = f.x, o[u][1] = f.y, o[u][2] = f.z, o[u][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+            o[u][0] = f.x, o[u][1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[u][v] = 0.f;
+        }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(wu[u], o[u][v], acc[v]);
     }
   }
   if constexpr (WPR > 1) {
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Param
     float Mn = M;
 #pragma unroll
     for (int w = 1; w < kMergeWarps; ++w) Mn = fmaxf(Mn, sm[w][D]);
-    if (Mn == -INFINITY) Mn = 0.f;
+    if (Mn == -INFINITY) Mn = 0.f;  // no tokens
     float a = exp2f(M - Mn);
     sum *= a;
 #pragma unroll

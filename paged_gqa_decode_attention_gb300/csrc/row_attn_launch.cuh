@@ -18,7 +18,10 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  // Not behind shared prefixes: started while the merge before it leaves the SMs, the CTAs
+  // come to lie on them in any order, and a wide segment beside an own one on an SM pair
+  // slowed some of both (128 sequences of 64/8 heads behind 16384 tokens: 112 us for 97).
+  cfg.numAttrs = pdl_enabled() && p.P == 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, row_attn_kernel<D, FP16, MOD>, tk, tv, tq, tq1, p);
 }
 
