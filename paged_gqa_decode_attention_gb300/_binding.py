@@ -329,17 +329,18 @@ class PagedDecodeAttention:
                   alibi_slopes, out, stream, window=0, cu_seqs=None, prefix_lens=None):
         dt, dev = self.dtype, self.device
         Hq, Hkv, bs, D = self._geometry
-        B = len(q)
-        if q.shape != (B, Hq, D):
+        shape, cache = q.shape, k_cache.shape
+        B = shape[0]
+        if shape != (B, Hq, D):
             raise ValueError("q must be [batch, Hq, D] with the handle's sizes")
-        shape = k_cache.shape
-        if len(shape) != 4 or v_cache.shape != shape or shape[1:] != (bs, Hkv, D):
+        if cache != (cache[0], bs, Hkv, D) or v_cache.shape != cache:
             raise ValueError("caches must be [num_blocks, block_size, Hkv, D] with the handle's sizes")
-        if block_table.dim() != 2 or len(block_table) != B or context_lens.shape != (B,):
+        rows = block_table.shape
+        if len(rows) != 2 or rows[0] != B or context_lens.shape != (B,):
             raise ValueError("block_table must be [batch, max_blocks] and context_lens [batch]")
         if out is None:
             out = torch.empty_like(q)
-        elif out.shape != q.shape:
+        elif out.shape != shape:
             raise ValueError("out must have q's shape")
         kv = None if self.kv_fp8 else dt
         named = [("q", q, dt), ("k_cache", k_cache, kv), ("v_cache", v_cache, kv),
@@ -350,7 +351,7 @@ class PagedDecodeAttention:
                 raise ValueError("alibi_slopes must be [Hq]")
             named.append(("alibi_slopes", alibi_slopes, torch.float32))
         if cu_seqs is not None:
-            if prefix_lens.dim() != 1 or cu_seqs.shape != (len(prefix_lens) + 1,):
+            if prefix_lens.dim() != 1 or cu_seqs.shape != (prefix_lens.shape[0] + 1,):
                 raise ValueError("cu_seqs must be [P + 1] and prefix_lens [P]")
             named += [("cu_seqs", cu_seqs, torch.int32), ("prefix_lens", prefix_lens, torch.int32)]
         p = _pointers(dev, named)
@@ -358,13 +359,13 @@ class PagedDecodeAttention:
         if scale is None:
             scale = D ** -0.5
         stream = _raw_stream(dev) if stream is None else _stream_ptr(stream)
-        head = (self.handle, *p[:5], B, block_table.shape[1], shape[0])
+        head = (self.handle, *p[:5], B, rows[1], cache[0])
         if cu_seqs is None:
             status = self.lib.paged_decode_attn_run_scored(*head, scale, softcap, slopes,
                                                            int(window), p[5], stream)
         else:
             status = self.lib.paged_decode_attn_run_shared_prefix(
-                *head, p[-2], p[-1], len(prefix_lens), scale, softcap, slopes, p[5], stream)
+                *head, p[-2], p[-1], prefix_lens.shape[0], scale, softcap, slopes, p[5], stream)
         if status:
             _check(self.lib, status)
         return out
