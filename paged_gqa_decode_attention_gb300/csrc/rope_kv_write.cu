@@ -23,8 +23,10 @@
 //
 // With several position axes (time, height, width of image and video tokens) pair j of a
 // token turns by the angle of its position on axis a_j: its cosine and sine are entries j of
-// table row pos[a_j][t]. An item of 8 pairs on one axis reads one row as above; one whose
-// pairs differ (interleaved axes) reads the 8 entries of every axis in it and selects.
+// table row pos[a_j][t]. The mover warp gathers them into one row a token, beside the token's
+// data in the ring, by 4-byte asynchronous copies that complete with the bulk copies; all
+// heads then read that row. (Each item reading the rows of all its axes and selecting took
+// 147 us for 16384 tokens at 32/8 heads, D 128, where one axis takes 77.)
 //
 // Memory-bound: token rows move through shared memory by bulk asynchronous
 // copies (no registers hold data in flight), so a ring of up to six ~16 KB
@@ -79,19 +81,19 @@ struct RopeParams {
   int lag;          // a stage is refilled `lag` tiles after its stores were issued
   int fused;        // q, k, v are consecutive parts of one [T, row_elems] buffer
   int axes;         // position axes (kAxes kernels)
-  uint64_t pair_axis[64];  // axis of each pair, a byte each; entry u: the pairs of item u
+  uint64_t pair_axis[64];  // axis of each pair, a byte each
 };
 constexpr int kRopeMaxAxes = 4;
 
-// Position of token t on axis a, and whether all of them are inside the table.
+// Whether the positions of token t are inside the table, on every axis.
 template <bool kAxes>
-__device__ __forceinline__ bool load_positions(const RopeParams& p, int64_t t, int (&pos)[kRopeMaxAxes]) {
+__device__ __forceinline__ bool positions_ok(const RopeParams& p, int64_t t) {
   bool ok = true;
 #pragma unroll
   for (int a = 0; a < (kAxes ? kRopeMaxAxes : 1); ++a) {
-    pos[a] = 0;
-    if (!kAxes || a < p.axes) pos[a] = __ldg(p.positions + (int64_t)a * p.T + t);
-    ok &= pos[a] >= 0 && pos[a] < p.max_position;
+    if (kAxes && a >= p.axes) break;
+    const int pos = __ldg(p.positions + (int64_t)a * p.T + t);
+    ok &= pos >= 0 && pos < p.max_position;
   }
   return ok;
 }
@@ -114,44 +116,20 @@ constexpr int kRopeMaxTileTokens = 32;       // one lane of warp 0 per token
 // Rotates the pairs of one 32-byte item in shared memory: angles j = 8u ..
 // 8u + 7 of a head row, elements at offA and offB (16-byte vectors).
 template <typename F, bool kNeox, bool kAxes>
-__device__ __forceinline__ void rotate_item(uint16_t* row, const RopeParams& p,
-                                            const int (&pos)[kRopeMaxAxes], int half, int u) {
+__device__ __forceinline__ void rotate_item(uint16_t* row, const float* cs_row, int half, int u) {
   const int offA = kNeox ? 8 * u : 16 * u;
   const int offB = kNeox ? half + 8 * u : 16 * u + 8;
   uint4* pa = reinterpret_cast<uint4*>(row + offA);
   uint4* pb = reinterpret_cast<uint4*>(row + offB);
   const uint4 A = *pa, B = *pb;
-  float c[8], s[8];
-  auto read = [&](int at, float (&cc)[8], float (&ss)[8]) {
-    const float* cs = p.cos_sin + (int64_t)at * p.rot_dim + 8 * u;
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs));
-    const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(cs + half));
-    const float4 s1 = __ldg(reinterpret_cast<const float4*>(cs + half + 4));
-    cc[0] = c0.x, cc[1] = c0.y, cc[2] = c0.z, cc[3] = c0.w;
-    cc[4] = c1.x, cc[5] = c1.y, cc[6] = c1.z, cc[7] = c1.w;
-    ss[0] = s0.x, ss[1] = s0.y, ss[2] = s0.z, ss[3] = s0.w;
-    ss[4] = s1.x, ss[5] = s1.y, ss[6] = s1.z, ss[7] = s1.w;
+  const float* cs = cs_row + 8 * u;
+  auto load = [](const float* at) {  // the gathered row is in shared memory
+    if constexpr (kAxes) return *reinterpret_cast<const float4*>(at);
+    else return __ldg(reinterpret_cast<const float4*>(at));
   };
-  if constexpr (kAxes) {
-    const uint64_t codes = p.pair_axis[u];
-    const int a0 = (int)(codes & 255);
-    auto pos_of = [&](int a) { return a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3]; };
-    read(pos_of(a0), c, s);
-    if (codes != 0x0101010101010101ull * (uint64_t)a0) {
-      for (int a = 0; a < p.axes; ++a) {
-        if (a == a0) continue;
-        float c1[8], s1[8];
-        read(pos_of(a), c1, s1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if ((int)((codes >> (8 * i)) & 255) == a) c[i] = c1[i], s[i] = s1[i];
-        }
-      }
-    }
-  } else {
-    read(pos[0], c, s);
-  }
+  const float4 c0 = load(cs), c1 = load(cs + 4), s0 = load(cs + half), s1 = load(cs + half + 4);
+  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
   const uint32_t wa[4] = {A.x, A.y, A.z, A.w};
   const uint32_t wb[4] = {B.x, B.y, B.z, B.w};
   uint32_t oa[4], ob[4];
@@ -202,13 +180,14 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __
   uint16_t* data = reinterpret_cast<uint16_t*>(smem + kRopeDataOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_local = (p.num_tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int64_t stage_elems = (int64_t)p.tile_tokens * p.row_elems;
+  const int64_t tile_elems = (int64_t)p.tile_tokens * p.row_elems;  // rows, then (kAxes) gathered rows
+  const int64_t stage_elems = tile_elems + (kAxes ? (int64_t)p.tile_tokens * p.rot_dim * 2 : 0);
   const uint32_t row_bytes = (uint32_t)p.row_elems * 2;
   const uint32_t q_bytes = (uint32_t)(p.Hq * p.D) * 2, kv_bytes = (uint32_t)(p.Hkv * p.D) * 2;
 
   if (tid == 0) {
     for (int s = 0; s < K; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), kAxes ? 33 : 1);  // kAxes: every lane's gathered entries, too
       mbar_init(smem_u32(&done[s]), kRopeRotWarps);
     }
     fence_mbar_init();
@@ -220,6 +199,31 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __
 
   if (warp == kRopeRotWarps) {
     // ---------------- mover warp ----------------
+    int next_pos[kRopeMaxAxes];  // of the next tile to load, a token a lane
+    auto load_next = [&](int i) {
+      const int t = i < n_local ? first_token(i) + lane : p.T;
+#pragma unroll
+      for (int a = 0; a < kRopeMaxAxes; ++a)
+        next_pos[a] = lane < p.tile_tokens && t < p.T && a < p.axes ? __ldg(p.positions + (int64_t)a * p.T + t) : -1;
+    };
+    if constexpr (kAxes) load_next(0);
+    // Entry e of the gathered row of each of nt tokens from its axis's table row.
+    auto gather = [&](uint32_t dst, int nt, uint32_t bar) {
+      const int half = p.rot_dim >> 1;
+      for (int j = 0; j < nt; ++j) {
+        int pos[kRopeMaxAxes];
+#pragma unroll
+        for (int a = 0; a < kRopeMaxAxes; ++a) pos[a] = __shfl_sync(0xffffffffu, next_pos[a], j);
+        for (int e = lane; e < p.rot_dim; e += 32) {
+          const int pair = e < half ? e : e - half;
+          const int a = (int)(p.pair_axis[pair >> 3] >> (8 * (pair & 7))) & 255;
+          const int at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+          const bool in = at >= 0 && at < p.max_position;  // else zeros; the token is not stored
+          cp_async_4(dst + (uint32_t)(j * p.rot_dim + e) * 4, p.cos_sin + (int64_t)(in ? at : 0) * p.rot_dim + e, in);
+        }
+      }
+      cp_async_arrive(bar);
+    };
     auto issue_load = [&](int i, int s) {
       const int t0 = first_token(i), nt = tile_len(t0);
       const uint32_t bar = smem_u32(&full[s]);
@@ -236,6 +240,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __
         bulk_load(dst + q_bytes, p.k + t * p.k_stride, kv_bytes, bar);
         bulk_load(dst + q_bytes + kv_bytes, p.v + t * p.v_stride, kv_bytes, bar);
       }
+      if constexpr (kAxes) {
+        gather(dst0 + (uint32_t)tile_elems * 2, nt, bar);
+        load_next(i + 1);
+      }
     };
     for (int s = 0; s < K && s < n_local; ++s) issue_load(s, s);
     for (int i = 0; i < n_local; ++i) {
@@ -250,11 +258,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __
       }
       const int t0 = first_token(i), nt = tile_len(t0);
       const int64_t t = t0 + lane;
-      int pos[kRopeMaxAxes];
       bool pos_ok = false;
       int64_t slot = -1;
       if (lane < nt) {  // in flight while the stage is being rotated
-        pos_ok = load_positions<kAxes>(p, t, pos);
+        pos_ok = positions_ok<kAxes>(p, t);
         slot = __ldg(p.slots + t);
       }
       const bool ok = mbar_wait_sleep(smem_u32(&done[s]), (uint32_t)(i / K) & 1u);
@@ -300,15 +307,22 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __
     int rem = tid - j * per_token;
     int cur_j = -1;
     bool valid = false;
-    int pos[kRopeMaxAxes];
+    const float* cs_row = p.cos_sin;
     for (int it = tid; it < nt * per_token; it += kRopeRotThreads) {
       if (j != cur_j) {
         cur_j = j;
-        valid = load_positions<kAxes>(p, t0 + j, pos);
+        if constexpr (kAxes) {  // gathered; a token with a bad position is not stored
+          valid = true;
+          cs_row = reinterpret_cast<const float*>(st + tile_elems) + (int64_t)j * p.rot_dim;
+        } else {
+          const int pos = __ldg(p.positions + t0 + j);
+          valid = pos >= 0 && pos < p.max_position;
+          cs_row = p.cos_sin + (int64_t)(valid ? pos : 0) * p.rot_dim;
+        }
       }
       if (valid) {
         const int r = fast_div(rem, p.div_rot_mul, p.div_rot_shift);
-        rotate_item<F, kNeox, kAxes>(st + (int64_t)j * p.row_elems + r * p.D, p, pos, half,
+        rotate_item<F, kNeox, kAxes>(st + (int64_t)j * p.row_elems + r * p.D, cs_row, half,
                                      rem - r * rot_items);
       }
       rem += kRopeRotThreads;
@@ -472,8 +486,12 @@ int rope_call(const void* q, int64_t q_token_stride, const void* k, int64_t k_to
   const int64_t num_tiles = (T + n - 1) / n;
   const uint32_t per_token_items =
       std::max<uint32_t>(1, (uint32_t)(num_q_heads + num_kv_heads) * (uint32_t)(rot_dim / 16));
-  const int stage_bytes = n * (int)row_bytes;
-  const int stages = std::min(pda::kRopeMaxStages, pda::kRopeRingBytes / stage_bytes);
+  const int stage_bytes = n * ((int)row_bytes + (num_axes > 0 ? rot_dim * 4 : 0));
+  int stages = std::min(pda::kRopeMaxStages, pda::kRopeRingBytes / stage_bytes);
+  // the gathered rows must not cost the third CTA of an SM (16384 tokens at 32/8 heads, D 128:
+  // 118 us with two of six stages)
+  const int third = (233472 / 3 - 1024 - pda::kRopeDataOff) / stage_bytes;
+  if (num_axes > 0 && third >= 4 && third < stages) stages = third;
   const int lag = stages >= 5 ? 2 : 1;
   const int smem = pda::kRopeDataOff + stages * stage_bytes;
   const int per_sm = std::max(1, std::min(3, 233472 / (smem + 1024)));  // 3 by registers
