@@ -113,6 +113,12 @@ constexpr int kRopeRingBytes = 192 * 1024;   // at most, for the whole ring
 constexpr int kRopeMaxRowBytes = 48 * 1024;
 constexpr int kRopeMaxTileTokens = 32;       // one lane of warp 0 per token
 
+// Place of pair j's cosine (and, half further, sine) in a gathered row: the first four pairs of
+// every item of 8, then the second four, so that neighbouring items' float4s are neighbours.
+__device__ __forceinline__ int gathered_place(int pair, int half) {
+  return ((pair >> 2) & 1) * (half / 2) + (pair >> 3) * 4 + (pair & 3);
+}
+
 // Rotates the pairs of one 32-byte item in shared memory: angles j = 8u ..
 // 8u + 7 of a head row, elements at offA and offB (16-byte vectors).
 template <typename F, bool kNeox, bool kAxes>
@@ -122,12 +128,20 @@ __device__ __forceinline__ void rotate_item(uint16_t* row, const float* cs_row, 
   uint4* pa = reinterpret_cast<uint4*>(row + offA);
   uint4* pb = reinterpret_cast<uint4*>(row + offB);
   const uint4 A = *pa, B = *pb;
-  const float* cs = cs_row + 8 * u;
-  auto load = [](const float* at) {  // the gathered row is in shared memory
-    if constexpr (kAxes) return *reinterpret_cast<const float4*>(at);
-    else return __ldg(reinterpret_cast<const float4*>(at));
-  };
-  const float4 c0 = load(cs), c1 = load(cs + 4), s0 = load(cs + half), s1 = load(cs + half + 4);
+  float4 c0, c1, s0, s1;
+  if constexpr (kAxes) {  // the gathered row, in shared memory (gathered_place)
+    const float* cs = cs_row + 4 * u;
+    c0 = *reinterpret_cast<const float4*>(cs);
+    c1 = *reinterpret_cast<const float4*>(cs + half / 2);
+    s0 = *reinterpret_cast<const float4*>(cs + half);
+    s1 = *reinterpret_cast<const float4*>(cs + half + half / 2);
+  } else {
+    const float* cs = cs_row + 8 * u;
+    c0 = __ldg(reinterpret_cast<const float4*>(cs));
+    c1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
+    s0 = __ldg(reinterpret_cast<const float4*>(cs + half));
+    s1 = __ldg(reinterpret_cast<const float4*>(cs + half + 4));
+  }
   const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
   const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
   const uint32_t wa[4] = {A.x, A.y, A.z, A.w};
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kv_write_kernel(const __
           const int a = (int)(p.pair_axis[pair >> 3] >> (8 * (pair & 7))) & 255;
           const int at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
           const bool in = at >= 0 && at < p.max_position;  // else zeros; the token is not stored
-          cp_async_4(dst + (uint32_t)(j * p.rot_dim + e) * 4, p.cos_sin + (int64_t)(in ? at : 0) * p.rot_dim + e, in);
+          cp_async_4(dst + (uint32_t)(j * p.rot_dim + (e - pair) + gathered_place(pair, half)) * 4, p.cos_sin + (int64_t)(in ? at : 0) * p.rot_dim + e, in);
         }
       }
       cp_async_arrive(bar);
