@@ -56,9 +56,9 @@ __device__ __forceinline__ Part part_of(const Params& p, int64_t row, int kind, 
 }
 
 template <int D, bool FP16, int WPR>
-__global__ void __launch_bounds__(kMergeWarps * 32) row_merge_kernel(const Params p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, WPR == 1 ? 8 : 1) row_merge_kernel(const Params p) {
   constexpr int V = D / 32;   // dims of a lane
-  constexpr int U = 8;        // partials in flight
+  constexpr int U = WPR == 1 ? 4 : 8;  // partials in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.B * p.Hq;
   const int row = WPR == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x;

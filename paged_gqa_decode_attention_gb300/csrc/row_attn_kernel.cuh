@@ -468,7 +468,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = tid; b < p.B; b += kThreads) {
       // an empty sequence (a padded batch) has no say, and its table row is not read
       const int g = group_of(cu, P, b), n = len_of(b);
-      if (g >= 0 && n > 0) {
+      const unsigned on = __activemask();
+      const bool in = g >= 0 && n > 0;
+      const int g0 = __shfl_sync(on, g, __ffs(on) - 1);
+      if (__all_sync(on, g == g0)) {  // the warp's sequences are of one group
+        const int least = __reduce_min_sync(on, in ? n : 0x7fffffff);
+        const int row = __reduce_min_sync(on, in ? b : 0x7fffffff);
+        if (g0 >= 0 && lane == __ffs(on) - 1) {
+          atomicMin(shared_pages + g0, least);
+          atomicMin(shared_row + g0, row);
+        }
+      } else if (in) {
         atomicMin(shared_pages + g, n);
         atomicMin(shared_row + g, b);
       }
@@ -824,6 +834,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(p_full(t, h), (p_phase >> x) & 1);
         p_phase ^= 1u << x;
       };
+      auto p_test = [&](int t, int h) {  // p_wait if it would not wait
+        const int x = 2 * t + h;
+        if (!__all_sync(kFull, mbar_test(p_full(t, h), (p_phase >> x) & 1))) return false;
+        p_phase ^= 1u << x;
+        return true;
+      };
       // steps x 16 tokens from half h on, `terms` terms of the weights
       auto pv = [&](auto steps, auto terms, int t, int h, int vs, bool start) {
         const uint64_t vb = v_desc + (uint32_t)(vs * kTileU + h * kHalfTileU);
@@ -871,17 +887,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 4; ++x) qk(x & 1, x >> 1, x & 1 ? q1 : q0, slot, idesc_qk2);
           commit(kv_empty(slot));
           next_slot(slot, phase);
+          o_wait(0);
+          o_wait(1);
+          v_wait(pslot, pphase);
+          p_wait(0, 0);
           for (int i = 0; i < n; ++i) {
             const int vs = v_slot(pslot);
-            v_wait(pslot, pphase);
             const bool more = i + 1 < n;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int t = x & 1, h = x >> 1;
-              if (i == 0 && h == 0) o_wait(t);
-              p_wait(t, h);
+              const int t = x & 1, h = x >> 1, y = (x + 1) & 3;
               tc_fence_after();
               pv(Half{}, One{}, t, h, vs, i == 0 && h == 0);
+              // while the tensor pipe is at it: what the next step waits for
+              bool got = true;
+              if (x < 3 || more) got = p_test(y & 1, y >> 1);
               if (more) {
                 if (x == 0) {
                   wait(kv_full(slot), phase);
@@ -889,6 +909,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 qk(t, h, t ? q1 : q0, slot, idesc_qk2);
               }
+              if (!got) p_wait(y & 1, y >> 1);
+            }
+            if (more) {  // the next chunk's V
+              int ns = pslot;
+              uint32_t np = pphase;
+              next_slot(ns, np);
+              v_wait(ns, np);
             }
             commit(kv_empty(vs));
             next_slot(pslot, pphase);
@@ -1004,6 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = wq * 32 + lane;  // row of the tile, and token row that this thread clears
       const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
       const uint32_t s_addr = tS(t) + lane_base, o_addr = tO(t) + lane_base;
+      constexpr int kDims4Log = D == 128 ? 5 : 4;
       constexpr float kGrow = FP16 ? 1.f : 8.f;     // log2 of the growth that is let pass
       constexpr float kShift = FP16 ? 14.f : 0.f;   // log2 of the weights' factor
       const int cap_rows = ws_cap(p);
@@ -1173,7 +1201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (s.own) {
           // the four warps' parts, all dims at once (G <= 8) or half of them at a time
-          const int heads = small_rows, dims4 = G > 8 ? D / 8 : D / 4;  // rows and float4s of a round
+          const int heads = small_rows, dims4_log = G > 8 ? kDims4Log - 1 : kDims4Log;  // rows and float4s of a round
+          const int dims4 = 1 << dims4_log;
           float4* part4 = reinterpret_cast<float4*>(base + L::kOffJoin + t * kJoinBytes);  // [4][heads][dims4]
           float2* ml = reinterpret_cast<float2*>(base + L::kOffMl) + t * 64;               // [4][16]
           if (row_ok) ml[wq * 16 + lane] = make_float2(m, l);
@@ -1197,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!meet()) break;
             for (int i = r; i < G * dims4; i += kT) {
-              const int g = i / dims4, c = i - g * dims4;
+              const int g = i >> dims4_log, c = i & (dims4 - 1);
               float2 v[4];
               float M = -INFINITY, sum = 0.f;
 #pragma unroll
