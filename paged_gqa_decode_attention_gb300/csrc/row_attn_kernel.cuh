@@ -80,11 +80,12 @@ static_assert(sizeof(SeqPlan) == kPlanInts * 4, "plan entry");
 constexpr int kWide = 1 << 16;
 
 // What an item of n chunks costs, in the units that the cut counts: a chunk, and what comes on
-// top once. Chunk 0 stands for the fixed part too, so that it belongs to the CTA in whose
+// top once. (A unit is about 0.19 us: a wide chunk 2.1 us, an own one 1.5 us of the memory's
+// time, a segment of one own chunk 2.2 us.) Chunk 0 stands for the fixed part too, so that it belongs to the CTA in whose
 // range the item begins.
 enum ItemKind { kOwnItem, kTileItem, kWideItem };  // a sequence's own; shared, up to 128 rows; up to 256
-__device__ __forceinline__ int item_chunk(int kind) { return kind == kWideItem ? 5 : 4; }
-__device__ __forceinline__ int item_fixed(int kind) { return kind == kOwnItem ? 2 : 4; }
+__device__ __forceinline__ int item_chunk(int kind) { return kind == kWideItem ? 11 : kind == kTileItem ? 9 : 8; }
+__device__ __forceinline__ int item_fixed(int kind) { return kind == kOwnItem ? 4 : 8; }
 __device__ __forceinline__ int item_cost(int kind, int n) {
   return n > 0 ? item_fixed(kind) + n * item_chunk(kind) : 0;
 }
@@ -248,6 +249,11 @@ __device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -294,29 +300,53 @@ __device__ __forceinline__ float max32(const float* x) {
   return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
 }
 
+// tanh(y) / y for |y| <= 1/2 as a polynomial in y^2, off by at most 2^-26: a weighted least-squares
+// fit of the relative error on Chebyshev points, the weights drawn towards the largest errors
+// (Lawson, "Contributions to the theory of linear least maximum approximations", 1961).
+__device__ __forceinline__ constexpr float tanh_coeff(int i) {
+  return i == 0 ? 1.f : i == 1 ? -0.33333069f : i == 2 ? 0.13324779f : i == 3 ? -0.05298607f : 0.017135005f;
+}
+
 // Products q . k of 32 tokens to capped and biased scores in base-2 units; far: the first
-// token's distance from the context's last one (t - (L - 1)).
-__device__ __forceinline__ void score_mods(const Params& p, float* x, float slope, float far) {
-  if (p.cap > 0.f && p.cap <= 128.f) {
-    // c tanh(y) = c - 2 c / (1 + e^2y): off by at most a few 2^-24 c
-    const float y2 = 2.f * kLog2e * p.cap_in, c = p.cap * kLog2e;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_ftz(x[q] * y2) + 1.f));
-      x[q] = fmaf(-2.f * c, r, c);
-    }
-  } else if (p.cap > 0.f) {
-    // a large cap: small arguments by the series of tanh y, off by at most 2^-26 y below 1/4
+// token's distance from the context's last one (t - (L - 1)); live: the row counts.
+__device__ __forceinline__ void score_mods(const Params& p, float* x, float slope, float far, bool live) {
+  if (p.cap > 0.f) {
     const float c = p.cap * kLog2e;
+    float most = 0.f;
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const float y = x[q] * p.cap_in, y2 = y * y;
-      const float series =
-          fmaf(fmaf(fmaf(fmaf(62.f / 2835.f, y2, -17.f / 315.f), y2, 2.f / 15.f), y2, -1.f / 3.f), y2, 1.f) * y;
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_ftz(y * (2.f * kLog2e)) + 1.f));
-      x[q] = c * (fabsf(y) < 0.25f ? series : fmaf(-2.f, r, 1.f));
+    for (int q = 0; q < 32; ++q) most = fmaxf(most, fabsf(x[q]));
+    if (__all_sync(0xffffffffu, !live || most * fabsf(p.cap_in) <= 0.5f)) {
+      // what most caps see: two scores an instruction on the multiply-add pipe
+      const uint64_t in2 = f32x2(p.cap_in, p.cap_in);
+      uint64_t k2[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) k2[i] = f32x2(c * tanh_coeff(i), c * tanh_coeff(i));
+#pragma unroll
+      for (int q = 0; q < 32; q += 2) {
+        const uint64_t y = f32x2_mul(f32x2(x[q], x[q + 1]), in2), z = f32x2_mul(y, y);
+        uint64_t r = k2[4];
+#pragma unroll
+        for (int i = 3; i >= 0; --i) r = f32x2_fma(r, z, k2[i]);
+        f32x2_split(f32x2_mul(r, y), x[q], x[q + 1]);
+      }
+    } else if (p.cap <= 128.f) {
+      // c tanh(y) = c - 2 c / (1 + e^2y): off by at most a few 2^-24 c
+      const float y2 = 2.f * kLog2e * p.cap_in;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_ftz(x[q] * y2) + 1.f));
+        x[q] = fmaf(-2.f * c, r, c);
+      }
+    } else {  // a large cap: either, by the score
+#pragma unroll
+      for (int q = 0; q < 32; ++q) {
+        const float y = x[q] * p.cap_in, z = y * y;
+        const float poly = fmaf(fmaf(fmaf(fmaf(tanh_coeff(4), z, tanh_coeff(3)), z, tanh_coeff(2)), z, tanh_coeff(1)), z, tanh_coeff(0)) * y;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2_ftz(y * (2.f * kLog2e)) + 1.f));
+        x[q] = c * (fabsf(y) <= 0.5f ? poly : fmaf(-2.f, r, 1.f));
+      }
     }
   } else {
 #pragma unroll
@@ -1044,8 +1074,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int meets = 0;
       [[maybe_unused]] float slope = 0.f, far0 = 0.f;
       // products q . k of 32 tokens to scores in base-2 units, those outside [lo, hi) -inf
-      auto scores = [&](float* x, float far, bool part, int lo, int hi) {
-        if constexpr (MOD) score_mods(p, x, slope, far);
+      auto scores = [&](float* x, float far, bool row_on, bool part, int lo, int hi) {
+        if constexpr (MOD) score_mods(p, x, slope, far, row_on);
         else
 #pragma unroll
           for (int q = 0; q < 32; ++q) x[q] *= p.qscale;
@@ -1123,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float x[32];
               tmem_ld32(s_addr + j, x);
               tmem_ld_wait();
-              scores(x, far + (float)j, part, lo - j, hi - j);
+              scores(x, far + (float)j, row_ok, part, lo - j, hi - j);
               follow(max32(x));
               uint64_t sum2 = f32x2(0.f, 0.f);
               weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum2);
@@ -1144,8 +1174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
               float qs = p.qscale, top;
               if (MOD || part) {
-                scores(x, far + (float)j, part, lo - j, hi - j);
-                scores(x + 32, far + (float)(j + 32), part, lo - j - 32, hi - j - 32);
+                scores(x, far + (float)j, row_ok, part, lo - j, hi - j);
+                scores(x + 32, far + (float)(j + 32), row_ok, part, lo - j - 32, hi - j - 32);
                 qs = 1.f;
               } else if (qs < 0.f) {  // the largest scaled score is the least product's
 #pragma unroll
