@@ -322,6 +322,8 @@ class PagedDecodeAttention:
         are not empty). Sequences outside every group, and a prefix of 0,
         share nothing. block_table and context_lens hold whole contexts, as
         for ``run``. P <= 128. softcap and alibi_slopes as in ``run``."""
+        if cu_seqs is None or prefix_lens is None:
+            raise ValueError("cu_seqs and prefix_lens must be given")
         return self._run_rows(q, k_cache, v_cache, block_table, context_lens, scale, softcap,
                               alibi_slopes, out, stream, cu_seqs=cu_seqs, prefix_lens=prefix_lens)
 

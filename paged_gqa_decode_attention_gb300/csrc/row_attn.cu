@@ -16,6 +16,7 @@ namespace row {
 namespace {
 
 constexpr int kMergeWarps = 4;
+constexpr float kRoom = 10.f;  // weights carry a factor 2^-10: sums of large outputs stay finite
 // One warp a row from this many rows on: one block of four warps a row would take more than
 // one round of blocks (152 SMs x 8).
 constexpr int kManyRows = 1216;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, WPR == 1 ? 8 : 1) row_merge_
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= a;
     M = Mn;
-    const float w = l == -INFINITY ? 0.f : exp2f(l - M);
+    const float w = l == -INFINITY ? 0.f : exp2f(l - M - kRoom);
     float ws = w;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(kFull, ws, off);

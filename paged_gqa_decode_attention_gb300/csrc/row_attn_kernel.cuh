@@ -36,7 +36,8 @@
 // the rounded weights, so that they still sum to one and an error is only ever relative to
 // v_t - out. In a narrow one, which waits for memory, P is the sum of two 16-bit terms
 // (16 or 22 significant bits) and PV takes twice the MMAs. fp16 weights carry a factor 2^14,
-// so that weights down to 2^-28 of the running maximum keep all their bits.
+// so that weights down to 2^-28 of the running maximum keep all their bits; bf16 weights a
+// factor 2^-24, so that sums over 65536 tokens of V near the type's largest value stay finite.
 //
 // Warps 0-3 and 4-7: the pipes. Warp 8: page loads (TMA) into a ring of K and V slots, the
 // walk over segments. Warp 9: TMEM, both MMAs. Every wait is bounded.
@@ -116,7 +117,7 @@ struct Layout {
   // segment follows no wide one that still needs it), or at D 64 memory of its own
   static constexpr int kOffJoin = D == 128 ? kOffQ + kTile : kOffQ + 2 * kTile;
   static constexpr int kOffBar = kOffJoin + 2 * kJoinBytes;
-  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 16;
+  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 17;
   static constexpr int kOffMl = kOffBar + kBars * 8;  // [pipe][4 warps][16 rows] maximum and sum
   static constexpr int kOffTmem = kOffMl + 2 * 4 * 16 * 8;
   static constexpr int kOffSeg = kOffTmem + 16;
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto pv_done = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 8 + 2 * t + h); };
   auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 12 + t); };
   auto joint = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 14 + t); };
+  const uint32_t drained = bar0 + 8u * (kBar1 + 2 * kSegRing + 16);
   // small segments' queries: rows 32 w .. 32 w + G - 1 of a tile for w < 4, so that tiles 8
   // (16) rows further in the same memory hold those of four (two) segments
   const int small_rows = p.G > 8 ? 16 : 8, n_small = 32 / small_rows;
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(o_free(s), 4);
     }
+    mbar_init(drained, 1);
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(seg_full(s), 1);
       mbar_init(seg_empty(s), 9);
@@ -796,7 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) griddep_launch_dependents();
       Seg end = {};
       if (!failed) publish(end);
-      // no copy or MMA may be in flight when the CTA exits: wait for the last releases
+      // no copy may be in flight when the CTA exits: wait for the last releases, or after a
+      // failed wait for the copies themselves
+      if (failed) {
+        for (int i = max(0, fill - kSlots); i < fill; ++i) mbar_wait(kv_full(i % kSlots), (i / kSlots) & 1);
+        for (int i = max(0, qfill - 2); i < qfill; ++i) mbar_wait(q_full(i & 1), (i >> 1) & 1);
+        for (int i = max(0, qsmall - n_small); i < qsmall; ++i)
+          mbar_wait(q_full(2 + i % n_small), (i / n_small) & 1);
+      }
       for (int i = max(0, fill - kSlots); i < fill && !failed; ++i) wait(kv_empty(i % kSlots), (i / kSlots) & 1);
       for (int i = max(0, qfill - 2); i < qfill && !failed; ++i) wait(q_empty(i & 1), (i >> 1) & 1);
       for (int i = max(0, qsmall - n_small); i < qsmall && !failed; ++i)
@@ -1054,6 +1064,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           --pending;
         }
       }
+      // no MMA or arrival may be in flight when the CTA exits, not after a failed wait either
+      commit(drained);
+      failed |= !mbar_wait(drained, 0);
       failed = __any_sync(kFull, failed);
     } else {
       // ------------------------------- softmax -------------------------------
@@ -1063,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s_addr = tS(t) + lane_base, o_addr = tO(t) + lane_base;
       constexpr int kDims4Log = D == 128 ? 5 : 4;
       constexpr float kGrow = FP16 ? 1.f : 8.f;     // log2 of the growth that is let pass
-      constexpr float kShift = FP16 ? 14.f : 0.f;   // log2 of the weights' factor
+      constexpr float kShift = FP16 ? 14.f : -24.f;  // log2 of the weights' factor
       const int cap_rows = ws_cap(p);
       uint32_t s_phase[2] = {0, 0};  // of the halves of S; PV of the same steps completes in them too
       auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -1075,8 +1088,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       [[maybe_unused]] float slope = 0.f, far0 = 0.f;
       // products q . k of 32 tokens to scores in base-2 units, those outside [lo, hi) -inf
       auto scores = [&](float* x, float far, bool row_on, bool part, int lo, int hi) {
-        if constexpr (MOD) score_mods(p, x, slope, far, row_on);
-        else
+        if constexpr (MOD) {
+          if (part) {  // what masked columns hold must not choose the way of the others
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (q < lo || q >= hi) x[q] = 0.f;
+          }
+          score_mods(p, x, slope, far, row_on);
+        } else
 #pragma unroll
           for (int q = 0; q < 32; ++q) x[q] *= p.qscale;
         if (part) {
