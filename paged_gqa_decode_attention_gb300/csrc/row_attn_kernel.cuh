@@ -20,11 +20,9 @@
 //   S = Q . K^T  (Q 128 x D from shared memory, K 64 or 128 tokens x D)  tcgen05 kind::f16
 //   O += P . V   (P from TMEM, V chunk as an MN-major operand)
 // A wide segment (more than 128 rows) gives each pipe one of its two row tiles, and both
-// read every chunk; in a narrow one the pipes take alternate chunks. Both work on S in
-// halves of 64 tokens: while the warpgroup turns one half into weights, the tensor pipe
-// multiplies those of the other with V and fills it with the next chunk's scores. (With
-// whole tiles a pipe's chain QK, softmax, PV took 3970 cycles a chunk where its MMAs take
-// 1024.) A sequence's own item has only G rows: they stand in Q four times, once for the
+// read every chunk; in a narrow one the pipes take alternate chunks. S is turned into weights
+// in halves of 64 tokens, so that PV of the first half runs beside the softmax of the second,
+// and the tensor pipe works for one pipe while the other's warpgroup does its softmax. A sequence's own item has only G rows: they stand in Q four times, once for the
 // TMEM lanes of each warp of a pipe, and each warp takes a quarter of the chunk's tokens (its
 // P is zero elsewhere), with a maximum and a sum of its own; at the segment's end the four
 // parts are joined through shared memory. One thread owns one row, so maxima and sums need
@@ -425,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBar1 = 2 * kSlots + 2 * kQBars;
   auto seg_full = [&](int s) { return bar0 + 8u * (kBar1 + s); };
   auto seg_empty = [&](int s) { return bar0 + 8u * (kBar1 + kSegRing + s); };
-  // of pipe t and half h of its score tile
-  auto s_full = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 * t + h); };
+  // of pipe t, and of half h of its score tile
+  auto s_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 + t); };
   auto p_full = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 4 + 2 * t + h); };
   auto pv_done = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 8 + 2 * t + h); };
   auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 12 + t); };
@@ -455,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(joint(s), 4);
+      mbar_init(s_full(s), 1);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(s_full(s, h), 1);
         mbar_init(p_full(s, h), 4);
         mbar_init(pv_done(s, h), 1);
       }
@@ -820,7 +818,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // cost 650 cycles a step on their way to the tensor pipe. After a wait that ran out,
       // the rest is walked through without waiting.
       constexpr uint32_t idesc_qk = idesc_f16(kT, kT, !FP16, false, false);
-      constexpr uint32_t idesc_qk2 = idesc_f16(kT, kT / 2, !FP16, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(kT, D, !FP16, false, true);
       constexpr uint32_t kTileU = L::kTile >> 4, kHalfTileU = kHalf / 2 >> 4;  // in descriptor units
       // descriptors of the ring's first slot and of the first Q tile
@@ -844,17 +841,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto commit = [&](uint32_t bar) {
         if (elect_one()) mma_commit(bar);
       };
-      // scores of a half (64 tokens) or all of a chunk
-      auto qk = [&](int t, int h, uint32_t q_off, int sl, uint32_t idesc) {
-        const uint64_t qa = q_desc + q_off, kb = k_desc + (uint32_t)(sl * kTileU + h * kHalfTileU);
-        const uint32_t d = tS(t) + h * (kT / 2);
+      // scores of a chunk
+      auto qk = [&](int t, uint32_t q_off, int sl) {
+        const uint64_t qa = q_desc + q_off, kb = k_desc + (uint32_t)(sl * kTileU);
+        const uint32_t d = tS(t);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-            mma_f16_ss(d, qa + o, kb + o, idesc, i > 0 ? 1u : 0u);
+            mma_f16_ss(d, qa + o, kb + o, idesc_qk, i > 0 ? 1u : 0u);
           }
-          mma_commit(s_full(t, h));
+          mma_commit(s_full(t));
         }
       };
       auto v_slot = [&](int sl) { return sl + 1 == kSlots ? 0 : sl + 1; };
@@ -915,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pslot = slot;
         uint32_t pphase = phase;
         if (wide) {
-          // steps (pipe, half) in the order (0, 0) (1, 0) (0, 1) (1, 1)
+          // pipe 0's chunk (PV of its halves, the next chunk's scores), then pipe 1's
           const int f0 = qfill & 1, f1 = f0 ^ 1;
           const uint32_t q0 = f0 * kTileU, q1 = f1 * kTileU;
           wait(q_full(f0), (qfill >> 1) & 1);
@@ -923,8 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           qfill += 2;
           wait(kv_full(slot), phase);
           tc_fence_after();
-#pragma unroll
-          for (int x = 0; x < 4; ++x) qk(x & 1, x >> 1, x & 1 ? q1 : q0, slot, idesc_qk2);
+          qk(0, q0, slot);
+          qk(1, q1, slot);
           commit(kv_empty(slot));
           next_slot(slot, phase);
           o_wait(0);
@@ -935,21 +932,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int vs = v_slot(pslot);
             const bool more = i + 1 < n;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int t = x & 1, h = x >> 1, y = (x + 1) & 3;
+            for (int t = 0; t < 2; ++t) {
               tc_fence_after();
-              pv(Half{}, One{}, t, h, vs, i == 0 && h == 0);
+              pv(Half{}, One{}, t, 0, vs, i == 0);
+              p_wait(t, 1);
+              tc_fence_after();
+              pv(Half{}, One{}, t, 1, vs, false);
               // while the tensor pipe is at it: what the next step waits for
               bool got = true;
-              if (x < 3 || more) got = p_test(y & 1, y >> 1);
+              if (t == 0 || more) got = p_test(t ^ 1, 0);
               if (more) {
-                if (x == 0) {
+                if (t == 0) {
                   wait(kv_full(slot), phase);
                   tc_fence_after();
                 }
-                qk(t, h, t ? q1 : q0, slot, idesc_qk2);
+                qk(t, t ? q1 : q0, slot);
               }
-              if (!got) p_wait(y & 1, y >> 1);
+              if (!got) p_wait(t ^ 1, 0);
             }
             if (more) {  // the next chunk's V
               int ns = pslot;
@@ -976,8 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto scores = [&](int t) {
             wait(kv_full(slot), phase);
             tc_fence_after();
-            qk(t, 0, q0, slot, idesc_qk2);
-            qk(t, 1, q0, slot, idesc_qk2);
+            qk(t, q0, slot);
             commit(kv_empty(slot));
             next_slot(slot, phase);
           };
@@ -1034,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int sl = __shfl_sync(kFull, slot, 0), t = __shfl_sync(kFull, tq, 0);
             const int at = __shfl_sync(kFull, place * small_rows * 128 >> 4, 0);
-            qk(t, 0, (uint32_t)at, sl, idesc_qk);
+            qk(t, (uint32_t)at, sl);
             commit(kv_empty(sl));
             if (--qleft == 0) commit(q_empty(2 + place));
             next_slot(slot, phase);
@@ -1078,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr float kGrow = FP16 ? 1.f : 8.f;     // log2 of the growth that is let pass
       constexpr float kShift = FP16 ? 14.f : -24.f;  // log2 of the weights' factor
       const int cap_rows = ws_cap(p);
-      uint32_t s_phase[2] = {0, 0};  // of the halves of S; PV of the same steps completes in them too
+      uint32_t s_phase[2] = {0, 0};  // of PV of the halves, and of S (as of its first half)
       auto wait = [&](uint32_t bar, uint32_t parity) {
         const bool ok = mbar_wait(bar, parity);
         if (!__all_sync(kFull, ok)) failed = true;
@@ -1164,8 +1162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float far = far0 + (float)(i * kT);
 #pragma unroll 1
           for (int h = 0; h < (s.own ? 1 : 2); ++h) {
-            if (!wait(s_full(t, h), s_phase[h])) break;
-            tc_fence_after();
+            if (h == 0) {
+              if (!wait(s_full(t), s_phase[0])) break;
+              tc_fence_after();
+            }
             if (s.own) {
               // All 128 columns at once, 32 of them here.
               const int j = wq * 32;
