@@ -143,6 +143,24 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
 }
+// The low (high) half of w plus c: one instruction on the multiply-add pipe,
+// where taking the halves apart costs the integer pipe two.
+#define PDA_HALF_OP(op, type, which)                                            \
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\t" op ".rn.f32." type " %0, " \
+      which ", %2;\n\t}" : "=f"(r) : "r"(w), "f"(c))
+template <bool FP16>
+__device__ __forceinline__ float add_low(uint32_t w, float c) {
+  float r;
+  if constexpr (FP16) PDA_HALF_OP("add", "f16", "l"); else PDA_HALF_OP("add", "bf16", "l");
+  return r;
+}
+template <bool FP16>
+__device__ __forceinline__ float add_high(uint32_t w, float c) {
+  float r;
+  if constexpr (FP16) PDA_HALF_OP("add", "f16", "h"); else PDA_HALF_OP("add", "bf16", "h");
+  return r;
+}
+#undef PDA_HALF_OP
 
 // 32 consecutive columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
@@ -253,23 +271,11 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ float f32x2_sum(uint64_t v) {
-  float a, b;
-  f32x2_split(v, a, b);
-  return a + b;
-}
-
 // 32 scores x to weights 2^(x qs + neg): the TMEM columns at addr get 16 of first terms and,
-// with two terms, 16 of second ones; sum2 adds what was written.
+// with two terms, 16 of second ones; the sums add what was written.
 template <bool FP16, bool kTwo>
 __device__ __forceinline__ void weights(uint32_t addr, const float* x, uint64_t qs2, uint64_t neg2,
-                                        uint64_t& sum2) {
+                                        float& sum0, float& sum1) {
   uint32_t w[16], w2[16];
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
@@ -277,26 +283,35 @@ __device__ __forceinline__ void weights(uint32_t addr, const float* x, uint64_t 
     f32x2_split(f32x2_fma(f32x2(x[2 * q], x[2 * q + 1]), qs2, neg2), y0, y1);
     const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
     w[q] = pack16<FP16>(p0, p1);
-    const float2 f = unpack16<FP16>(w[q]);
     if constexpr (kTwo) {
+      const float2 f = unpack16<FP16>(w[q]);
       w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
-      sum2 = f32x2_add(sum2, f32x2(p0, p1));
+      sum0 += p0;
+      sum1 += p1;
     } else {
-      sum2 = f32x2_add(sum2, f32x2(f.x, f.y));
+      sum0 = add_low<FP16>(w[q], sum0);
+      sum1 = add_high<FP16>(w[q], sum1);
     }
   }
   tmem_st16(addr, w);
   if constexpr (kTwo) tmem_st16(addr + 16, w2);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max32(const float* x) {
   float a[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-  for (int q = 4; q < 32; q += 4) {
+  for (int q = 4; q < 28; q += 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], x[q + i]);
+    for (int i = 0; i < 4; ++i) a[i] = max3(a[i], x[q + i], x[q + i + 4]);
   }
-  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], x[28 + i]);
+  return max3(fmaxf(a[0], a[1]), a[2], a[3]);
 }
 
 // tanh(y) / y for |y| <= 1/2 as a polynomial in y^2, off by at most 2^-26: a weighted least-squares
@@ -1174,14 +1189,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
               scores(x, far + (float)j, row_ok, part, lo - j, hi - j);
               follow(max32(x));
-              uint64_t sum2 = f32x2(0.f, 0.f);
-              weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum2);
+              float sum0 = 0.f, sum1 = 0.f;
+              weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum0, sum1);
 #pragma unroll
               for (int q = 0; q < 32; ++q) x[q] = 0.f;
 #pragma unroll 1
               for (int c = 0; c < kT; c += 32)
                 if (c != j) tmem_st32(s_addr + c, x);
-              l += f32x2_sum(sum2);
+              l += sum0 + sum1;
               tmem_st_wait();
             } else if (warp_ok) {
               // Half the columns. (All 128 in registers, with the code that this unrolls to,
@@ -1204,15 +1219,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               top = fmaxf(max32(x), max32(x + 32)) * qs;
               follow(top);
               const uint64_t qs2 = f32x2(qs, qs), neg2 = shift(m);
-              uint64_t sum2 = f32x2(0.f, 0.f);
+              float sum0 = 0.f, sum1 = 0.f;
               if (s.wide) {
-                weights<FP16, false>(s_addr + j, x, qs2, neg2, sum2);
-                weights<FP16, false>(s_addr + j + 32, x + 32, qs2, neg2, sum2);
+                weights<FP16, false>(s_addr + j, x, qs2, neg2, sum0, sum1);
+                weights<FP16, false>(s_addr + j + 32, x + 32, qs2, neg2, sum0, sum1);
               } else {
-                weights<FP16, true>(s_addr + j, x, qs2, neg2, sum2);
-                weights<FP16, true>(s_addr + j + 32, x + 32, qs2, neg2, sum2);
+                weights<FP16, true>(s_addr + j, x, qs2, neg2, sum0, sum1);
+                weights<FP16, true>(s_addr + j + 32, x + 32, qs2, neg2, sum0, sum1);
               }
-              l += f32x2_sum(sum2);
+              l += sum0 + sum1;
               tmem_st_wait();
             }
             if (part && h == 0 && (!s.wide || t == 0)) {
