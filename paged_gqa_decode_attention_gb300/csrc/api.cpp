@@ -607,6 +607,9 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
   p.max_blocks = max_blocks;
   p.block_size = c.block_size;
   p.bs_log = c.block_size == 16 ? 4 : c.block_size == 32 ? 5 : 6;
+  p.spt = pda::row::kT / h->group;
+  p.tile_mul = (uint32_t)(((uint64_t)1 << 32) / (2 * p.spt) + 1);
+  p.group_mul = (uint32_t)((65536 + h->group - 1) / h->group);
   p.num_blocks = num_blocks;
   p.window = window;
   p.qscale = scale * pda::kLog2e;

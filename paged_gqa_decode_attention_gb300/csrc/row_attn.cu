@@ -38,11 +38,16 @@ struct Part {
     return next + seg * slab + pipe * cap;
   }
 };
+// x / per by per_mul = floor((2^32 - 1) / per): the product falls short by at most one.
+__device__ __forceinline__ int div_per(int x, int per, unsigned per_mul) {
+  const int q = (int)__umulhi((unsigned)x, per_mul);
+  return q + (x - q * per >= per);
+}
 __device__ __forceinline__ Part part_of(const Params& p, int64_t row, int kind, int start, int n,
-                                        int per, int tile, int r) {
+                                        int per, unsigned per_mul, int tile, int r) {
   Part d = {};
   if (n == 0) return d;
-  const int c0 = start / per, c1 = (start + item_cost(kind, n) - 1) / per;
+  const int c0 = div_per(start, per, per_mul), c1 = div_per(start + item_cost(kind, n) - 1, per, per_mul);
   d.kind = kind;
   d.n_chunks = n;
   d.x = c0 * per - start;
@@ -69,13 +74,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, WPR == 1 ? 8 : 1) row_merge_
   if (row >= rows) return;
   const int b = row / p.Hq, hq = row - b * p.Hq, h = hq / p.G, g = hq - h * p.G;
   const int per = p.plan[0];
+  const unsigned per_mul = (unsigned)p.plan[1];
   const SeqPlan s = reinterpret_cast<const SeqPlan*>(p.plan + kPlanInts)[b];
   const int pr = s.pre_row & (kWide - 1);
   const Part pre = part_of(p, row, s.pre_row >= kWide ? kWideItem : kTileItem,
-                           s.pre_start + h * s.pre_stride, s.pre_n, per, pr >= kT ? 1 : 0,
+                           s.pre_start + h * s.pre_stride, s.pre_n, per, per_mul, pr >= kT ? 1 : 0,
                            (pr & (kT - 1)) + g);
   const Part own = part_of(p, row, kOwnItem, s.own_start + h * item_cost(kOwnItem, s.own_n), s.own_n,
-                           per, 0, g);
+                           per, per_mul, 0, g);
   const int n = pre.n + own.n;
   float M = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll

@@ -24,10 +24,12 @@ struct Params {
   void* out;                    // [B, Hq, D]
   float* ws_o;                  // partial rows (normalised outputs), D floats each
   float* ws_lse;                // and their log-sum-exps, base 2
-  int* plan;                    // [1 + ...]: cost per CTA; then SeqPlan of each sequence
+  int* plan;                    // cost per CTA, 2^32 over it; from kPlanInts on SeqPlan of each sequence
   int* err;
   int B, P, Hq, Hkv, G, max_blocks, block_size;
   int bs_log;      // log2(block_size)
+  int spt;         // sequences of a row tile: kT / G
+  uint32_t tile_mul, group_mul;  // ceil(2^32 / (2 spt)), ceil(2^16 / G)
   int64_t num_blocks;
   int window;      // > 0: only the last `window` tokens
   float qscale;    // scale * log2(e)

@@ -92,7 +92,9 @@ __device__ __forceinline__ int item_cost(int kind, int n) {
 __device__ __forceinline__ int chunk_at(int kind, int n, int x) {
   if (x <= 0) return 0;
   const int c = item_chunk(kind), y = x - item_fixed(kind);
-  return y <= c ? min(1, n) : min(n, (y + c - 1) / c);
+  // ceil(y / c), the divisors written out so that none is a division
+  const int up = kind == kWideItem ? (y + 10) / 11 : kind == kTileItem ? (y + 8) / 9 : (y + 7) / 8;
+  return y <= c ? min(1, n) : min(n, up);
 }
 
 // Partial rows in the workspace: [B * Hq][2] of the segments that start a shared item (by
@@ -454,7 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* shared_pages = reinterpret_cast<int*>(base + L::kOffShared);  // of each group
   int* shared_row = reinterpret_cast<int*>(base + L::kOffRow);       // a sequence that holds them
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
-  const int G = p.G, spt = kT / G;  // sequences of a row tile
+  const int G = p.G, spt = p.spt;  // sequences of a row tile
+  // x / (2 spt) for x < 2^14 and the sequence of row r of a tile, without dividing
+  auto tile_of = [&](int x) { return (int)__umulhi((unsigned)x, p.tile_mul); };
+  auto seq_of = [&](int r) { return (int)((unsigned)r * p.group_mul >> 16); };
   bool failed = false;
 
   if (tid == 0) {
@@ -510,10 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   auto len_of = [&](int b) { return b == tid ? my_len : context_len(p, b); };
+  const int my_group = P > 0 && tid < p.B ? group_of(cu, P, tid) : -1;
+  auto group_at = [&](int b) { return P == 0 ? -1 : b == tid ? my_group : group_of(cu, P, b); };
   if (P > 0) {
     for (int b = tid; b < p.B; b += kThreads) {
       // an empty sequence (a padded batch) has no say, and its table row is not read
-      const int g = group_of(cu, P, b), n = len_of(b);
+      const int g = group_at(b), n = len_of(b);
       const unsigned on = __activemask();
       const bool in = g >= 0 && n > 0;
       const int g0 = __shfl_sync(on, g, __ffs(on) - 1);
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  auto tiles_of = [&](int g) { return (cu[g + 1] - cu[g] + 2 * spt - 1) / (2 * spt); };
+  auto tiles_of = [&](int g) { return tile_of(cu[g + 1] - cu[g] + 2 * spt - 1); };
   auto group_chunks = [&](int g) { return ((shared_pages[g] << p.bs_log) + kT - 1) / kT; };
   // the last tile of a group may be narrow, the others are wide
   auto last_kind = [&](int g, int tiles) { return cu[g + 1] - cu[g] - (tiles - 1) * 2 * spt > spt ? kWideItem : kTileItem; };
@@ -550,8 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int n_elem = P + p.B;
   if (tid < P) sum[tid] = tiles_of(tid) > 0 ? p.Hkv * group_cost(tid) : 0;
-  for (int b = tid; b < p.B; b += kThreads)
-    sum[P + b] = p.Hkv * item_cost(kOwnItem, own_part(p, len_of(b), seq_shared(b)).n);
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int g = group_at(b);
+    sum[P + b] = p.Hkv * item_cost(kOwnItem, own_part(p, len_of(b), g >= 0 ? shared_pages[g] : 0).n);
+  }
   __syncthreads();
   const int per_thread = (n_elem + kThreads - 1) / kThreads;
   const int e0 = min(n_elem, tid * per_thread), e1 = min(n_elem, e0 + per_thread);
@@ -596,13 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (blockIdx.x == gridDim.x - 1) {  // for the merge, by the CTA with the least left to do
-    if (tid == 0) p.plan[0] = per;
+    if (tid == 0) p.plan[0] = per, p.plan[1] = (int)(0xffffffffu / (unsigned)per);
     SeqPlan* plan = reinterpret_cast<SeqPlan*>(p.plan + kPlanInts);
     for (int b = tid; b < p.B; b += kThreads) {
       SeqPlan s = {};
-      const int g = P > 0 ? group_of(cu, P, b) : -1, len = len_of(b);
+      const int g = group_at(b), len = len_of(b);
       if (g >= 0 && shared_pages[g] > 0 && len > 0) {
-        const int i = b - cu[g], tile = i / (2 * spt), r = i - tile * 2 * spt;
+        const int i = b - cu[g], tile = tile_of(i), r = i - tile * 2 * spt;
         const int n_seq = min(2 * spt, cu[g + 1] - cu[g] - tile * 2 * spt);
         s.pre_n = group_chunks(g);
         s.pre_start = sum[g] + tile * item_cost(kWideItem, s.pre_n);
@@ -1137,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // own segments: every warp has the G rows, and a quarter of each chunk's tokens
         const int ri = s.own ? lane : r;
         const bool row_ok = ri < n_rows, warp_ok = s.own || wq * 32 < n_rows;
-        const int rs = ri / G, b = s.b0 + (s.wide && t ? spt : 0) + rs, hq = s.h * G + ri - rs * G;
+        const int rs = seq_of(ri), b = s.b0 + (s.wide && t ? spt : 0) + rs, hq = s.h * G + ri - rs * G;
         float m = -INFINITY, l = 0.f;  // running maximum (base 2), sum of the weights
         if constexpr (MOD) {
           slope = far0 = 0.f;

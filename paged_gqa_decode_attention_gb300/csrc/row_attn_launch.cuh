@@ -6,6 +6,8 @@
 namespace pda {
 namespace row {
 
+constexpr int64_t kSmallTokens = 1 << 18;  // tokens x kv heads of a call, at most, with unshared prefixes
+
 template <int D, bool FP16, bool MOD>
 cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                        const CUtensorMap& tq1, const Params& p, int ctas, cudaStream_t stream) {
@@ -20,8 +22,11 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   cfg.attrs = attr;
   // Not behind shared prefixes: started while the merge before it leaves the SMs, the CTAs
   // come to lie on them in any order, and a wide segment beside an own one on an SM pair
-  // slowed some of both (128 sequences of 64/8 heads behind 16384 tokens: 112 us for 97).
-  cfg.numAttrs = pdl_enabled() && p.P == 0 ? 1 : 0;
+  // slowed some of both (128 sequences of 64/8 heads behind 16384 tokens: 112 us for 97). A
+  // small call, whose segments are a chunk or two, gains by it (8 sequences of 32/8 heads
+  // behind 1504 tokens: 16.7 us for 17.4).
+  const int64_t tokens = (int64_t)p.B * p.max_blocks * p.block_size;
+  cfg.numAttrs = pdl_enabled() && (p.P == 0 || tokens * p.Hkv <= kSmallTokens) ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, row_attn_kernel<D, FP16, MOD>, tk, tv, tq, tq1, p);
 }
 
