@@ -2,8 +2,9 @@
 
 The computation lives in the CUDA library ``libpaged_decode_attn.so``
 (C ABI: ``include/paged_decode_attn.h``); this package is its Python binding
-(``PagedDecodeAttention``, ``merge``, ``plan``, ``rope_kv_write``), the in-tree build script and
-the seeded synthetic workload generators. Importing the package does not load
+(``PagedDecodeAttention`` with ``run`` and ``run_shared_prefix``, ``merge``, ``plan``,
+``rope_kv_write``, ``rope_axes_kv_write``, the cache movement and FP8 cache calls), the in-tree
+build script and the seeded synthetic workload generators. Importing the package does not load
 the CUDA library; the first call does, and raises if it is missing.
 """
 from ._binding import (ABI_VERSION, EXPORTS, PDA_BF16, PDA_EALIAS, PDA_ECUDA, PDA_EDEVICE,
