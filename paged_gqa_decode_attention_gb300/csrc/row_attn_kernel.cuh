@@ -1323,7 +1323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                if (v[q].x != -INFINITY) {  // the warp saw tokens
+                // the warp saw tokens (or only scores that are NaN, whose sum is NaN)
+                if (v[q].x != -INFINITY || v[q].y != 0.f) {
                   const float f = ex2_ftz(v[q].x - M);
                   const float4 o = part4[(q * heads + g) * dims4 + (c ^ (g & 7))];
                   sum = fmaf(f, v[q].y, sum);

@@ -94,6 +94,26 @@ def test_ids_out_of_range_read_zeros():
         assert a.check_device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(8, 2, 128, BF), (24, 2, 64, HF)])
+@pytest.mark.parametrize("seqs", [3, 40])  # queries of a tile, and of a wide one
+@pytest.mark.parametrize("softcap", [0.0, 6.0])
+def test_nan_in_a_query_or_a_key_reaches_its_rows_only(hq, hkv, d, dtype, seqs, softcap):
+    lens = [193 + 5 * i for i in range(seqs)]
+    q, k, v, table, ln = make(lens, hq, hkv, d, 16, dtype, [(0, seqs, 192)], seed=31)
+    want, tol = reference(q, k, v, table, ln, 0.1, softcap)
+    nan = torch.zeros(seqs, hq, dtype=torch.bool)
+    q[1, 3, 7] = float("nan")
+    nan[1, 3] = True
+    k[table[0, 12], 0, 1, 5] = float("nan")  # the first sequence's only token of its own
+    nan[0, hq // 2:] = True
+    cu, pre = ints(0, seqs), ints(192)
+    with handle(q, k, table) as a:
+        for out in (a.run_shared_prefix(q, k, v, table, ln, cu, pre, 0.1, softcap),
+                    a.run(q, k, v, table, ln, 0.1, softcap=softcap, window=10 ** 6)):
+            assert torch.isnan(out.cpu()[nan]).all()
+            check(out.cpu()[~nan], want[~nan], tol[~nan])
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("order", [1, -1])
 def test_growing_and_falling_scores(dtype, order):
