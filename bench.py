@@ -52,10 +52,10 @@ TC_KERNEL_SOURCES = ("partial_tc_kernel.cuh", "ptx.cuh", "split_merge.cuh", "pda
 ROPE_KERNEL_SOURCES = ("rope_kv_write.cu", "rope_math.cuh", "ptx.cuh", "pda_internal.h")
 NCU_TRAFFIC = {
     # workload: (bytes per launch, kernel sources, their SHA-256 at capture)
-    "long_b4_l32768": (540_590_848, TC_KERNEL_SOURCES,
-                       "5f7c4f5d4e941a995ca618c701d714645cd1f3a52cdab953b03567ef8bf72d58"),
-    "rope_prefill_t32768": (768_278_272, ROPE_KERNEL_SOURCES,
-                            "4fbbc0ed42893172acf68d4475cc7222f44220320fb80eb911cd4f91664f68e1"),
+    "long_b4_l32768": (540_119_040, TC_KERNEL_SOURCES,
+                       "b3707e56d3cfeceb9cbd332b344119e5759bf173aa62990c21f79915cb5a0a49"),
+    "rope_prefill_t32768": (768_056_064, ROPE_KERNEL_SOURCES,
+                            "a1bfd45bf99d47c5fbf8c520f1de24b037998536de24dadacac993acce2808da"),
 }
 
 
