@@ -24,7 +24,8 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
   // come to lie on them in any order, and a wide segment beside an own one on an SM pair
   // slowed some of both (128 sequences of 64/8 heads behind 16384 tokens: 112 us for 97). A
   // small call, whose segments are a chunk or two, gains by it (8 sequences of 32/8 heads
-  // behind 1504 tokens: 16.7 us for 17.4).
+  // behind 1504 tokens: 16.7 us for 17.4). Between them a limit of 2^20 or 2^22 in place of 2^18
+  // gains 2% at 16 sequences behind 4096 tokens and loses 7% at 64 of 64/8 heads behind 1024.
   const int64_t tokens = (int64_t)p.B * p.max_blocks * p.block_size;
   cfg.numAttrs = pdl_enabled() && (p.P == 0 || tokens * p.Hkv <= kSmallTokens) ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, row_attn_kernel<D, FP16, MOD>, tk, tv, tq, tq1, p);
