@@ -174,8 +174,8 @@ int paged_decode_attn_run_scaled(pda_handle handle, const void* q, const void* k
  * and, with window > 0, only the last `window` tokens (t >= L - window) attended to.
  * 16-bit K/V at head_dim 64 or 128, any group size up to 16 (else
  * PDA_EUNSUPPORTED); batch <= 16384; `out` has cfg->dtype. The weights enter the
- * product with V as the sum of two 16-bit terms (16 significant bits with bf16, 22
- * with fp16). The
+ * product with V as the sum of two 16-bit terms: off by at most 2^-16 of themselves with
+ * bf16; with fp16 by 2^-22 of themselves or 2^-39 of the largest, whichever is more. The
  * work is cut evenly over the GPU; two launches. */
 int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k_cache,
                                  const void* v_cache, const int32_t* block_table,
@@ -187,12 +187,10 @@ int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k
  * their contexts: for i < num_prefixes (<= 128), the sequences cu_seqs[i] ..
  * cu_seqs[i + 1] - 1 have the same ids in their block_table rows for the
  * first prefix_lens[i] tokens, and those blocks are read once for all of them
- * (tiles of up to 256 query rows of a kv head; of tiles of more than 128, the weights
- * are rounded to one 16-bit term, 8 or 11 significant bits, and the result is divided by
- * the sum of the rounded ones). cu_seqs [num_prefixes + 1] and
+ * (tiles of up to 256 query rows of a kv head). cu_seqs [num_prefixes + 1] and
  * prefix_lens [num_prefixes] are int32 on the device; block_table and
- * context_lens hold whole contexts, and the result is that of
- * paged_decode_attn_run. Of a prefix, whole blocks are shared, and no more than the
+ * context_lens hold whole contexts; the formula is that of paged_decode_attn_run_scored
+ * and so are the weights' bits, in tiles of any size. Of a prefix, whole blocks are shared, and no more than the
  * shortest context of the group that is not empty holds; a group of one and
  * a sequence outside every group share nothing. Rows of a group that
  * do not name the same blocks are the caller's mistake: the ids of the first

@@ -30,13 +30,12 @@
 // no exchange. The running maximum is only followed when it grows by more than a threshold
 // (2^8 in bf16, 2 in fp16), which spares nearly every rescaling of O; the final division
 // makes up for it.
-// In a wide segment P is rounded to 16 bits once: a weight is off by at most 2^-8 (bf16) or
-// 2^-11 (fp16) of itself, as much as the output's own rounding, and the denominator adds
-// the rounded weights, so that they still sum to one and an error is only ever relative to
-// v_t - out. In a narrow one, which waits for memory, P is the sum of two 16-bit terms
-// (16 or 22 significant bits) and PV takes twice the MMAs. fp16 weights carry a factor 2^14,
-// so that weights down to 2^-28 of the running maximum keep all their bits; bf16 weights a
-// factor 2^-24, so that sums over 65536 tokens of V near the type's largest value stay finite.
+// P is the sum of two 16-bit terms, and PV takes twice the MMAs: a weight is off by at most
+// 2^-16 of itself in bf16; in fp16, whose weights carry a factor 2^14, by 2^-22 of itself or
+// 2^-39 of the running maximum (below 2^-17 of which the second term is subnormal), whichever
+// is more. The denominator adds the weights before their rounding. bf16 weights carry a factor
+// 2^-24, so that sums over 65536 tokens of V near the type's largest value stay finite (values
+// of V below 2^-110 lose bits to it).
 //
 // Warps 0-3 and 4-7: the pipes. Warp 8: page loads (TMA) into a ring of K and V slots, the
 // walk over segments. Warp 9: TMEM, both MMAs. Every wait is bounded.
@@ -158,24 +157,6 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
 }
-// The low (high) half of w plus c: one instruction on the multiply-add pipe,
-// where taking the halves apart costs the integer pipe two.
-#define PDA_HALF_OP(op, type, which)                                            \
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\t" op ".rn.f32." type " %0, " \
-      which ", %2;\n\t}" : "=f"(r) : "r"(w), "f"(c))
-template <bool FP16>
-__device__ __forceinline__ float add_low(uint32_t w, float c) {
-  float r;
-  if constexpr (FP16) PDA_HALF_OP("add", "f16", "l"); else PDA_HALF_OP("add", "bf16", "l");
-  return r;
-}
-template <bool FP16>
-__device__ __forceinline__ float add_high(uint32_t w, float c) {
-  float r;
-  if constexpr (FP16) PDA_HALF_OP("add", "f16", "h"); else PDA_HALF_OP("add", "bf16", "h");
-  return r;
-}
-#undef PDA_HALF_OP
 
 // 32 consecutive columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
@@ -286,9 +267,9 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 32 scores x to weights 2^(x qs + neg): the TMEM columns at addr get 16 of first terms and,
-// with two terms, 16 of second ones; the sums add what was written.
-template <bool FP16, bool kTwo>
+// 32 scores x to weights 2^(x qs + neg): the TMEM columns at addr get 16 of first terms and 16
+// of second ones; the sums add the weights as they were before.
+template <bool FP16>
 __device__ __forceinline__ void weights(uint32_t addr, const float* x, uint64_t qs2, uint64_t neg2,
                                         float& sum0, float& sum1) {
   uint32_t w[16], w2[16];
@@ -298,18 +279,13 @@ __device__ __forceinline__ void weights(uint32_t addr, const float* x, uint64_t 
     f32x2_split(f32x2_fma(f32x2(x[2 * q], x[2 * q + 1]), qs2, neg2), y0, y1);
     const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
     w[q] = pack16<FP16>(p0, p1);
-    if constexpr (kTwo) {
-      const float2 f = unpack16<FP16>(w[q]);
-      w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
-      sum0 += p0;
-      sum1 += p1;
-    } else {
-      sum0 = add_low<FP16>(w[q], sum0);
-      sum1 = add_high<FP16>(w[q], sum1);
-    }
+    const float2 f = unpack16<FP16>(w[q]);
+    w2[q] = pack16<FP16>(p0 - f.x, p1 - f.y);
+    sum0 += p0;
+    sum1 += p1;
   }
   tmem_st16(addr, w);
-  if constexpr (kTwo) tmem_st16(addr + 16, w2);
+  tmem_st16(addr + 16, w2);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -914,13 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_phase ^= 1u << x;
         return true;
       };
-      // steps x 16 tokens from half h on, `terms` terms of the weights
-      auto pv = [&](auto steps, auto terms, int t, int h, int vs, bool start) {
+      // steps x 16 tokens from half h on, both terms of the weights
+      auto pv = [&](auto steps, int t, int h, int vs, bool start) {
         const uint64_t vb = v_desc + (uint32_t)(vs * kTileU + h * kHalfTileU);
         const uint32_t pa = tS(t) + h * (kT / 2), o = tO(t);
         if (elect_one()) {
 #pragma unroll
-          for (int u = 0; u < decltype(terms)::value; ++u) {
+          for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int j = 0; j < decltype(steps)::value; ++j)
               mma_f16_ts(o, pa + (j >> 1) * 32 + u * 16 + (j & 1) * 8, vb + (uint32_t)(j * 2048 >> 4), idesc_pv,
@@ -929,8 +905,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(pv_done(t, h));
         }
       };
-      using One = std::integral_constant<int, 1>;
-      using Two = std::integral_constant<int, 2>;
       using Half = std::integral_constant<int, kT / 32>;
       using Whole = std::integral_constant<int, kT / 16>;
       int n = 0, own = 0, par = 0;
@@ -971,10 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               tc_fence_after();
-              pv(Half{}, One{}, t, 0, vs, i == 0);
+              pv(Half{}, t, 0, vs, i == 0);
               p_wait(t, 1);
               tc_fence_after();
-              pv(Half{}, One{}, t, 1, vs, false);
+              pv(Half{}, t, 1, vs, false);
               // while the tensor pipe is at it: what the next step waits for
               bool got = true;
               if (t == 0 || more) got = p_test(t ^ 1, 0);
@@ -1030,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 2; ++h) {
               p_wait(t, h);
               tc_fence_after();
-              pv(Half{}, Two{}, t, h, vs, i < 2 && h == 0);
+              pv(Half{}, t, h, vs, i < 2 && h == 0);
             }
             commit(kv_empty(vs));
             next_slot(pslot, pphase);
@@ -1090,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p_wait(tp, 0);
           tc_fence_after();
           const int vs = __shfl_sync(kFull, v_slot(pslot), 0), t = __shfl_sync(kFull, tp, 0);
-          pv(Whole{}, Two{}, t, 0, vs, vi < 2);
+          pv(Whole{}, t, 0, vs, vi < 2);
           commit(kv_empty(vs));
           next_slot(pslot, pphase);
           tp ^= 1;
@@ -1212,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               scores(x, far + (float)j, row_ok, part, lo - j, hi - j);
               follow(max32(x));
               float sum0 = 0.f, sum1 = 0.f;
-              weights<FP16, true>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum0, sum1);
+              weights<FP16>(s_addr + j, x, f32x2(1.f, 1.f), shift(m), sum0, sum1);
 #pragma unroll
               for (int q = 0; q < 32; ++q) x[q] = 0.f;
 #pragma unroll 1
@@ -1242,13 +1216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               follow(top);
               const uint64_t qs2 = f32x2(qs, qs), neg2 = shift(m);
               float sum0 = 0.f, sum1 = 0.f;
-              if (s.wide) {
-                weights<FP16, false>(s_addr + j, x, qs2, neg2, sum0, sum1);
-                weights<FP16, false>(s_addr + j + 32, x + 32, qs2, neg2, sum0, sum1);
-              } else {
-                weights<FP16, true>(s_addr + j, x, qs2, neg2, sum0, sum1);
-                weights<FP16, true>(s_addr + j + 32, x + 32, qs2, neg2, sum0, sum1);
-              }
+              weights<FP16>(s_addr + j, x, qs2, neg2, sum0, sum1);
+              weights<FP16>(s_addr + j + 32, x + 32, qs2, neg2, sum0, sum1);
               l += sum0 + sum1;
               tmem_st_wait();
             }
