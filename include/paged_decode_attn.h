@@ -172,6 +172,8 @@ int paged_decode_attn_run_scaled(pda_handle handle, const void* q, const void* k
  *   s = softcap * tanh(s / softcap)             if softcap > 0
  *   s = s + alibi_slopes[hq] * (t - (L - 1))    if alibi_slopes (fp32 [Hq], device) is not NULL
  * and, with window > 0, only the last `window` tokens (t >= L - window) attended to.
+ * scale * log2(e), softcap * log2(e) and 2 log2(e) scale / softcap must be finite in fp32,
+ * and scale / softcap a normal number (unless scale is 0).
  * 16-bit K/V at head_dim 64 or 128, any group size up to 16 (else
  * PDA_EUNSUPPORTED); batch <= 16384; `out` has cfg->dtype. The weights enter the
  * product with V as the sum of two 16-bit terms: off by at most 2^-16 of themselves with

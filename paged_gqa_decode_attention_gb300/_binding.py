@@ -340,6 +340,8 @@ class PagedDecodeAttention:
         rows = block_table.shape
         if len(rows) != 2 or rows[0] != B or context_lens.shape != (B,):
             raise ValueError("block_table must be [batch, max_blocks] and context_lens [batch]")
+        if 0.0 < softcap < 1e-45:  # would reach the library as 0: no cap
+            raise ValueError("softcap is below fp32's range")
         if out is None:
             out = torch.empty_like(q)
         elif out.shape != shape:

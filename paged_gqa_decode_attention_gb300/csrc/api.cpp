@@ -544,8 +544,12 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
   if (!std::isfinite(scale)) return fail(PDA_EINVAL, "scale is not finite");
   if (!std::isfinite(softcap) || softcap < 0.f)
     return fail(PDA_EINVAL, "softcap must be finite and >= 0 (0: none)");
-  if (softcap > 0.f && !std::isfinite(scale / softcap))
-    return fail(PDA_EINVAL, "scale / softcap is not finite");
+  // the kernel's factors: none may overflow, and scale / softcap must keep its bits
+  if (!std::isfinite(scale * pda::kLog2e) || !std::isfinite(softcap * pda::kLog2e))
+    return fail(PDA_EINVAL, "scale * log2(e) and softcap * log2(e) must be finite");
+  if (softcap > 0.f && scale != 0.f &&
+      (!std::isnormal(scale / softcap) || !std::isfinite(scale / softcap * (2.f * pda::kLog2e))))
+    return fail(PDA_EINVAL, "scale / softcap is outside fp32's normal range");
   if (window < 0) return fail(PDA_EINVAL, "window < 0 (0: none)");
   if (batch == 0) return PDA_OK;
   if (!q || !k_cache || !v_cache || !block_table || !context_lens || !out)
