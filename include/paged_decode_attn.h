@@ -175,7 +175,10 @@ int paged_decode_attn_run_scaled(pda_handle handle, const void* q, const void* k
  * scale * log2(e), softcap * log2(e) and 2 log2(e) scale / softcap must be finite in fp32,
  * and scale / softcap a normal number (unless scale is 0).
  * 16-bit K/V at head_dim 64 or 128, any group size up to 16 (else
- * PDA_EUNSUPPORTED); batch <= 16384; `out` has cfg->dtype. The weights enter the
+ * PDA_EUNSUPPORTED); batch <= 16384, and batch * Hkv * (8 n + 6) <= 2^30 for the n chunks of 128
+ * tokens that max_blocks * block_size tokens, or window + block_size - 1 if less, may have
+ * (batch * Hkv * (8 n + 21) with prefixes; else PDA_EUNSUPPORTED), max_blocks * block_size
+ * <= 2^31 - 129; `out` has cfg->dtype. The weights enter the
  * product with V as the sum of two 16-bit terms: off by at most 2^-16 of themselves with
  * bf16; with fp16 by 2^-22 of themselves or 2^-39 of the largest, whichever is more. The
  * work is cut evenly over the GPU; two launches. */

@@ -566,11 +566,13 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
        reinterpret_cast<uintptr_t>(cu_seqs) | reinterpret_cast<uintptr_t>(prefix_lens) |
        reinterpret_cast<uintptr_t>(alibi_slopes)) & 3u)
     return fail(PDA_EINVAL, "block_table, context_lens, cu_seqs, prefix_lens and alibi_slopes must be 4-byte aligned");
-  // what the kernel counts in 32 bits: up to 11 a chunk of 128 tokens and 14 an item, for every
-  // sequence's own tokens and every group's (at most one row tile a sequence)
-  const int64_t chunks = ((int64_t)max_blocks * c.block_size + pda::row::kT - 1) / pda::row::kT;
-  if (2 * (int64_t)batch * c.num_kv_heads * 14 * (chunks + 1) > INT_MAX)
-    return fail(PDA_EINVAL, "batch * num_kv_heads * max_blocks is too large for this call");
+  int64_t tokens = (int64_t)max_blocks * c.block_size;  // a context's, or those in the pages that its window touches
+  if (tokens > INT_MAX - pda::row::kT)
+    return fail(PDA_EUNSUPPORTED, "this call takes contexts of up to 2^31 - 129 tokens");
+  if (window > 0 && (int64_t)window + c.block_size - 1 < tokens) tokens = (int64_t)window + c.block_size - 1;
+  if (pda::row::most_cost(batch, c.num_kv_heads, tokens, num_prefixes > 0) > pda::row::kMostCost)
+    return fail(PDA_EUNSUPPORTED,
+                "batch * num_kv_heads * (max_blocks * block_size, or the window, in chunks of 128) is too large for this call");
   const size_t n_q = (size_t)batch * c.num_q_heads * c.head_dim;
   const size_t cache_bytes = (size_t)num_blocks * c.block_size * c.num_kv_heads * c.head_dim * 2;
   if (overlaps(out, n_q * 2, q, n_q * 2) || overlaps(out, n_q * 2, k_cache, cache_bytes) ||

@@ -43,6 +43,16 @@ inline int64_t workspace_rows(int64_t batch, int num_q_heads, int group, int cta
   return 4 * batch * num_q_heads + 2 * rows * ctas;
 }
 
+// What the items of a call may cost at most, in the units that the kernel's plan adds up in 32
+// bits (item_cost): 6 + 8 a chunk for a sequence's own part of `tokens`. Behind prefixes its
+// chunks are one more (both parts end in a part of a chunk), and of a shared item's 14 + 11 a
+// chunk a sequence bears half at most: a row tile of 2 kT / G rows is that of two sequences or more.
+inline int64_t most_cost(int64_t batch, int num_kv_heads, int64_t tokens, bool prefixes) {
+  const int64_t chunks = (tokens + kT - 1) / kT;
+  return batch * num_kv_heads * (prefixes ? 6 + 7 + 8 * (chunks + 1) : 6 + 8 * chunks);
+}
+constexpr int64_t kMostCost = int64_t{1} << 30;  // half of what 32 bits hold: room for a CTA's range on top
+
 // 16-bit K/V, head dim 64 or 128, any group size up to 16.
 inline bool supported(int group, int head_dim) {
   return group >= 1 && group <= 16 && (head_dim == 64 || head_dim == 128);
