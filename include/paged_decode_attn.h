@@ -108,11 +108,14 @@ const char* paged_decode_attn_last_error(void);
 
 /* Validate `cfg`, select cfg->device, and allocate the handle plus its
  * device workspace: max_batch * Hq * max_splits * (head_dim + 1) floats of
- * split partials (at least the rows that paged_decode_attn_run_scored and
- * paged_decode_attn_run_shared_prefix need: 4 * max_batch * Hq, and two rows per
- * SM for each of up to 128 rows of max_batch * Hq / Hkv), max_batch * Hkv ints of split tickets (the last split of a
+ * split partials, max_batch * Hkv ints of split tickets (the last split of a
  * sequence's kv head to finish merges the splits; tickets return to zero by
  * the end of every call) and a small error-word area, all zeroed.
+ * paged_decode_attn_run_scored and paged_decode_attn_run_shared_prefix need r rows of
+ * head_dim + 1 floats, r = 4 * min(max_batch, 16384) * Hq, and for each SM two times
+ * min(128, max_batch * Hq / Hkv): where the split partials are fewer, create allocates them
+ * beside, and where it cannot, the handle serves every other call and these two return
+ * PDA_ENOMEM.
  * Returns PDA_OK and stores the handle in *out_handle, or an error (and
  * *out_handle = NULL). Configuration errors are reported before any CUDA call. */
 int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle);

@@ -341,8 +341,12 @@ struct pda_handle_s {
   alignas(64) CUtensorMap tmap_k;
   alignas(64) CUtensorMap tmap_v;
   // Row-tiled calls (shared prefixes, capped and biased scores): null where the geometry
-  // has none. They use ws_o and ws_lse too.
+  // has none. Their partials lie in ws_o and ws_lse where those are large enough, else in
+  // memory of their own (row_ws; row_o null where it could not be had).
   int* row_plan = nullptr;  // [1 + max_batch][pda::row::kPlanInts]
+  void* row_ws = nullptr;
+  float* row_o = nullptr;
+  float* row_lse = nullptr;
 };
 
 namespace {
@@ -537,6 +541,7 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
   const pda_config& c = h->cfg;
   if (c.kv_fp8) return fail(PDA_EUNSUPPORTED, "this call needs 16-bit K/V caches");
   if (!h->row_plan) return fail(PDA_EUNSUPPORTED, "this call needs head_dim 64 or 128");
+  if (!h->row_o) return fail(PDA_ENOMEM, "create could not allocate this call's workspace");
   if (batch < 0 || batch > c.max_batch) return fail(PDA_EINVAL, "batch out of [0, max_batch]");
   if (batch > pda::row::kMaxBatch) return fail(PDA_EUNSUPPORTED, "this call takes up to 16384 sequences");
   if (num_prefixes < 0) return fail(PDA_EINVAL, "num_prefixes < 0");
@@ -601,8 +606,8 @@ int run_rows(pda_handle h, const void* q, const void* k_cache, const void* v_cac
   p.prefix_lens = prefix_lens;
   p.slopes = alibi_slopes;
   p.out = out;
-  p.ws_o = h->ws_o;
-  p.ws_lse = h->ws_lse;
+  p.ws_o = h->row_o;
+  p.ws_lse = h->row_lse;
   p.plan = h->row_plan;
   p.err = h->err;
   p.B = batch;
@@ -709,8 +714,9 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
         pda::partial_ctas_per_sm_hint(pda::kPartialCudaCore, h->group, cfg->head_dim);
     h->cc_ctas_per_sm = occ_cc < hint_cc ? occ_cc : hint_cc;
   }
-  size_t rows = (size_t)cfg->max_batch * cfg->num_q_heads * cfg->max_splits;
+  const size_t rows = (size_t)cfg->max_batch * cfg->num_q_heads * cfg->max_splits;
   const bool row_calls = !kv8 && pda::row::supported(h->group, cfg->head_dim);
+  size_t row_rows = 0;  // of partials that the row-tiled calls need
   if (row_calls) {
     e = pda::row::prepare(cfg->head_dim, cfg->dtype);
     if (e != cudaSuccess) {
@@ -718,8 +724,7 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
       return cuda_fail("cudaFuncSetAttribute", e);
     }
     const int most = cfg->max_batch < pda::row::kMaxBatch ? cfg->max_batch : pda::row::kMaxBatch;
-    const size_t need = (size_t)pda::row::workspace_rows(most, cfg->num_q_heads, h->group, h->num_sms);
-    if (need > rows) rows = need;
+    row_rows = (size_t)pda::row::workspace_rows(most, cfg->num_q_heads, h->group, h->num_sms);
   }
   const size_t o_bytes = rows * cfg->head_dim * sizeof(float);
   const size_t lse_bytes = ((rows * sizeof(float)) + 255) & ~size_t(255);
@@ -739,10 +744,25 @@ int paged_decode_attn_create(const pda_config* cfg, pda_handle* out_handle) {
   h->err = reinterpret_cast<int*>(static_cast<char*>(h->ws) + o_bytes + lse_bytes);
   h->counters = reinterpret_cast<int*>(static_cast<char*>(h->ws) + o_bytes + lse_bytes + err_bytes);
   if (row_calls) h->row_plan = reinterpret_cast<int*>(static_cast<char*>(h->ws) + plan_off);
+  if (row_calls && row_rows <= rows) {
+    h->row_o = h->ws_o;
+    h->row_lse = h->ws_lse;
+  } else if (row_calls) {
+    // Not all handles make these calls: one that cannot have their memory serves the others.
+    const size_t row_o_bytes = row_rows * cfg->head_dim * sizeof(float);
+    if (cudaMalloc(&h->row_ws, row_o_bytes + row_rows * sizeof(float)) == cudaSuccess) {
+      h->row_o = static_cast<float*>(h->row_ws);
+      h->row_lse = reinterpret_cast<float*>(static_cast<char*>(h->row_ws) + row_o_bytes);
+    } else {
+      h->row_ws = nullptr;
+      cudaGetLastError();
+    }
+  }
   e = cudaMemset(h->err, 0, err_bytes + h->counter_bytes);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     cudaFree(h->ws);
+    cudaFree(h->row_ws);
     delete h;
     return cuda_fail("cudaMemset", e);
   }
@@ -755,6 +775,7 @@ void paged_decode_attn_destroy(pda_handle h) {
   if (h->ws) {
     DeviceGuard guard(h->cfg.device);
     cudaFree(h->ws);
+    cudaFree(h->row_ws);
   }
   delete h;
 }
