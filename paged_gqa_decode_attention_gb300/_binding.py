@@ -559,6 +559,14 @@ def rope_axes_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     Hkv = k.shape[1]
     if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
         raise ValueError("k and v must be [T, Hkv, D] with q's T and D")
+    if cos_sin_cache.dim() != 2:
+        raise ValueError("cos_sin_cache must be [max_position, rot_dim]")
+    try:
+        axes = bytes(list(pair_axis))  # of the integers, not of an array's memory or so many zeros
+    except TypeError:
+        raise ValueError("pair_axis must be a sequence of integers") from None
+    if len(axes) != cos_sin_cache.shape[1] // 2:
+        raise ValueError("pair_axis must hold rot_dim / 2 axes")
     dev = _cuda_device(k_cache)
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
@@ -567,14 +575,9 @@ def rope_axes_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positi
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape or shape[2:] != (Hkv, D):
         raise ValueError("caches must be [num_blocks, block_size, Hkv, D]")
-    if cos_sin_cache.dim() != 2:
-        raise ValueError("cos_sin_cache must be [max_position, rot_dim]")
     if positions.dim() != 2 or positions.shape[1] != T or slot_mapping.shape != (T,):
         raise ValueError("positions must be [axes, T] and slot_mapping [T]")
     max_pos, rot_dim = cos_sin_cache.shape
-    axes = bytes(pair_axis)
-    if len(axes) != rot_dim // 2:
-        raise ValueError("pair_axis must hold rot_dim / 2 axes")
     qp, qs = _rows16("q", q, dev, dt)
     kp, ks = _rows16("k", k, dev, dt)
     vp, vs = _rows16("v", v, dev, dt)
