@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import threading
 
@@ -340,6 +341,12 @@ class PagedDecodeAttention:
         rows = block_table.shape
         if len(rows) != 2 or rows[0] != B or context_lens.shape != (B,):
             raise ValueError("block_table must be [batch, max_blocks] and context_lens [batch]")
+        try:
+            window = operator.index(window)
+        except TypeError:
+            raise ValueError("window must be an integer") from None
+        # the library takes 32 bits; beyond them every context is within the window, or it is refused
+        window = max(-1, min(window, 2 ** 31 - 1))
         if 0.0 < softcap < 1e-45:  # would reach the library as 0: no cap
             raise ValueError("softcap is below fp32's range")
         if out is None:
@@ -366,7 +373,7 @@ class PagedDecodeAttention:
         head = (self.handle, *p[:5], B, rows[1], cache[0])
         if cu_seqs is None:
             status = self.lib.paged_decode_attn_run_scored(*head, scale, softcap, slopes,
-                                                           int(window), p[5], stream)
+                                                           window, p[5], stream)
         else:
             status = self.lib.paged_decode_attn_run_shared_prefix(
                 *head, p[-2], p[-1], prefix_lens.shape[0], scale, softcap, slopes, p[5], stream)
