@@ -45,7 +45,7 @@ inline int64_t workspace_rows(int64_t batch, int num_q_heads, int group, int cta
 
 // What the items of a call may cost at most, in the units that the kernel's plan adds up in 32
 // bits (item_cost): 6 + 8 a chunk for a sequence's own part of `tokens`. Behind prefixes its
-// chunks are one more (both parts end in a part of a chunk), and of a shared item's 14 + 11 a
+// chunks are one more (both parts end in a part of a chunk), and of a shared item's 14 + 14 a
 // chunk a sequence bears half at most: a row tile of 2 kT / G rows is that of two sequences or more.
 inline int64_t most_cost(int64_t batch, int num_kv_heads, int64_t tokens, bool prefixes) {
   const int64_t chunks = (tokens + kT - 1) / kT;

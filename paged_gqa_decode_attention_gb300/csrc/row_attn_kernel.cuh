@@ -89,13 +89,15 @@ static_assert(sizeof(SeqPlan) == kPlanInts * 4, "plan entry");
 constexpr int kWide = 1 << 16;
 
 // What an item of n chunks costs, in the units that the cut counts: a chunk, and what comes on
-// top once. (A unit is about 0.19 us: a wide chunk 2.1 us, an own one 1.5 us of the memory's
-// time, a segment of one own chunk 2.2 us. Fixed parts of 4 / 8, 4 / 14, 8 / 16 and 12 / 24
-// for own and shared items: 96 sequences of 32 to 4096 tokens at 64/8 heads 68.8, 68.8, 65.4,
-// 66.7 us; 64 sequences behind 8192 tokens 45.7, 44.7, 47.4, 49.0 us.) Chunk 0 stands for the fixed part too, so that it belongs to the CTA in whose
-// range the item begins.
+// top once. (A unit is about 0.19 us: a wide chunk 2.7 us, an own one 1.5 us of the memory's
+// time, a segment of one own chunk 2.2 us. A wide chunk at 11, 12, 13, 14, 15 and 16: 128
+// sequences of 64/8 heads behind 16384 tokens 101.6, 101.6, 98.9, 97.4, 97.2, 100.3 us. Fixed
+// parts of 4 / 14, 6 / 14, 8 / 16 and 6 / 20 for own and shared items: the same 102.6, 98.0,
+// 100.8, 97.9 us, 96 sequences of 32 to 4096 tokens at 64/8 heads 69.3, 65.2, 65.5, 65.3 us.)
+// Chunk 0 stands for the fixed part too, so that it belongs to the CTA in whose range the item
+// begins.
 enum ItemKind { kOwnItem, kTileItem, kWideItem };  // a sequence's own; shared, up to 128 rows; up to 256
-__device__ __forceinline__ int item_chunk(int kind) { return kind == kWideItem ? 11 : kind == kTileItem ? 9 : 8; }
+__device__ __forceinline__ int item_chunk(int kind) { return kind == kWideItem ? 14 : kind == kTileItem ? 9 : 8; }
 __device__ __forceinline__ int item_fixed(int kind) { return kind == kOwnItem ? 6 : 14; }
 __device__ __forceinline__ int item_cost(int kind, int n) {
   return n > 0 ? item_fixed(kind) + n * item_chunk(kind) : 0;
@@ -105,7 +107,7 @@ __device__ __forceinline__ int chunk_at(int kind, int n, int x) {
   if (x <= 0) return 0;
   const int c = item_chunk(kind), y = x - item_fixed(kind);
   // ceil(y / c), the divisors written out so that none is a division
-  const int up = kind == kWideItem ? (y + 10) / 11 : kind == kTileItem ? (y + 8) / 9 : (y + 7) / 8;
+  const int up = kind == kWideItem ? (y + 13) / 14 : kind == kTileItem ? (y + 8) / 9 : (y + 7) / 8;
   return y <= c ? min(1, n) : min(n, up);
 }
 
