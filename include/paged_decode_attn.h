@@ -184,7 +184,10 @@ int paged_decode_attn_run_scaled(pda_handle handle, const void* q, const void* k
  * <= 2^31 - 129; `out` has cfg->dtype. The weights enter the
  * product with V as the sum of two 16-bit terms: off by at most 2^-16 of themselves with
  * bf16; with fp16 by 2^-22 of themselves or 2^-39 of the largest, whichever is more. The
- * work is cut evenly over the GPU; two launches. */
+ * work is cut evenly over the GPU; two launches. An infinity in a row of V that a head attends
+ * to makes its dim of that head's result an infinity or NaN (zero terms of other weights meet
+ * it), as in paged_decode_attn_run on the tensor-core kernel; other dims, heads of other kv
+ * heads and other sequences are not touched. */
 int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k_cache,
                                  const void* v_cache, const int32_t* block_table,
                                  const int32_t* context_lens, int batch, int max_blocks,
