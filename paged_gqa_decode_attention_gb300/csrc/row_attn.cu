@@ -17,9 +17,11 @@ namespace {
 
 constexpr int kMergeWarps = 4;
 constexpr float kRoom = 10.f;  // weights carry a factor 2^-10: sums of large outputs stay finite
-// One warp a row from this many rows on: one block of four warps a row would take more than
-// one round of blocks (152 SMs x 8).
-constexpr int kManyRows = 1216;
+// One warp a row from this many rows an SM on: a block of four warps a row, as below, then takes
+// more than a round or two of blocks. (Whole calls with one warp and with four, 64/8 heads: 768
+// rows behind 4096 shared tokens 25.0 and 22.2 us, 1024 rows of own tokens 25.8 and 26.8, 1536
+// rows 27.1 and 28.8 us, 1536 behind shared tokens 28.2 and 30.4, 6144 rows 40.0 and 50.3.)
+constexpr int kManyRowsPerSm = 8;
 
 // The workspace rows of one part of a row's context.
 struct Part {
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, WPR == 1 ? 8 : 1) row_merge_
 }
 
 template <int D, bool FP16>
-cudaError_t launch_merge_rows(const Params& p, cudaStream_t stream) {
+cudaError_t launch_merge_rows(const Params& p, int num_sms, cudaStream_t stream) {
   const int rows = p.B * p.Hq;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kMergeWarps * 32);
@@ -179,7 +181,7 @@ cudaError_t launch_merge_rows(const Params& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  if (rows >= kManyRows) {
+  if (rows >= num_sms * kManyRowsPerSm) {
     cfg.gridDim = dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps));
     return cudaLaunchKernelEx(&cfg, row_merge_kernel<D, FP16, 1>, p);
   }
@@ -210,10 +212,10 @@ cudaError_t launch(int head_dim, int dtype, const CUtensorMap& tk, const CUtenso
   cudaError_t e;
   if (head_dim == 64) {
     e = (dtype == 1 ? launch_fp16_d64 : launch_bf16_d64)(tk, tv, tq, tq1, p, num_sms, stream);
-    if (e == cudaSuccess) e = dtype == 1 ? launch_merge_rows<64, true>(p, stream) : launch_merge_rows<64, false>(p, stream);
+    if (e == cudaSuccess) e = dtype == 1 ? launch_merge_rows<64, true>(p, num_sms, stream) : launch_merge_rows<64, false>(p, num_sms, stream);
   } else {
     e = (dtype == 1 ? launch_fp16_d128 : launch_bf16_d128)(tk, tv, tq, tq1, p, num_sms, stream);
-    if (e == cudaSuccess) e = dtype == 1 ? launch_merge_rows<128, true>(p, stream) : launch_merge_rows<128, false>(p, stream);
+    if (e == cudaSuccess) e = dtype == 1 ? launch_merge_rows<128, true>(p, num_sms, stream) : launch_merge_rows<128, false>(p, num_sms, stream);
   }
   return e;
 }
