@@ -17,13 +17,13 @@
 //
 // Inside a CTA two pipes, each a softmax warpgroup with one TMEM score tile S (128 rows x
 // 128 tokens, fp32), whose columns then hold the weights P (16 bits), and one output tile O:
-//   S = Q . K^T  (Q 128 x D from shared memory, K 64 or 128 tokens x D)  tcgen05 kind::f16
+//   S = Q . K^T  (Q 128 x D from shared memory, K 128 tokens x D)  tcgen05 kind::f16
 //   O += P . V   (P from TMEM, V chunk as an MN-major operand)
 // A wide segment (more than 128 rows) gives each pipe one of its two row tiles, and both
-// read every chunk; in a narrow one the pipes take alternate chunks. S is turned into weights
-// in halves of 64 tokens, so that PV of the first half runs beside the softmax of the second,
-// and the tensor pipe works for one pipe while the other's warpgroup does its softmax. A
-// sequence's own item has only G rows: they stand in Q four times, once for the
+// read every chunk; in a narrow one the pipes take alternate chunks. S of a shared chunk is
+// turned into weights in halves of 64 tokens, so that PV of the first half runs beside the
+// softmax of the second; the tensor pipe works for one pipe while the other's warpgroup does
+// its softmax. A sequence's own item has only G rows: they stand in Q four times, once for the
 // TMEM lanes of each warp of a pipe, and each warp takes a quarter of the chunk's tokens (its
 // P is zero elsewhere), with a maximum and a sum of its own; at the segment's end the four
 // parts are joined through shared memory. One thread owns one row, so maxima and sums need
@@ -40,15 +40,16 @@
 // Warps 0-3 and 4-7: the pipes. Warp 8: page loads (TMA) into a ring of K and V slots, the
 // walk over segments. Warp 9: TMEM, both MMAs. Every wait is bounded.
 //
-// Measured (GB300, back to back, merge included; bf16, head dim 128; the first case's K/V,
-// 84 MB, stays in the L2, the others' does not). 128 sequences of 64/8
-// heads behind 16384 shared tokens, 32 own ones: 86.5 us, 796 TFLOP/s (697 us without
-// sharing); the MMAs alone take 36 us at the rate of a large library product, a wide chunk's
-// softmax on two warps a scheduler about 3000 of its 3500 cycles: it bounds. 16 sequences
-// (128 rows) behind 65536 tokens: 68 us, 4.0 TB/s (493 us); the ring's 160 KiB bound, which
-// holds a V chunk until both halves of its PV are done. Own tokens only: 4 x 32768 at 32/8
-// heads 90 us, capped 93 us (6.0 and 5.8 TB/s of a copy's 6.7); 96 x 1024 at 64/8 heads 76
-// us, capped 79 us. The plan, launches and merge are 9 us of a call that has little to do.
+// Measured (GB300, calls in a graph, merge included; bf16, head dim 128; the first case's K/V,
+// 84 MB, stays in the L2, the others' does not). 128 sequences of 64/8 heads behind 16384
+// shared tokens, 32 own ones: 98 us, 700 TFLOP/s (697 us without sharing), capped 148 us; the
+// MMAs alone, two for each weight, take 54 us at the rate of a large library product. A wide
+// chunk takes 2.2 us, some 4300 cycles, of which the tensor pipe works 3072: its softmax, on two
+// warps a scheduler, bounds. 16 sequences (128 rows) behind 65536 tokens: 69 us, 3.9 TB/s (494
+// us); the ring's 160 KiB bound, which holds a V chunk until both halves of its PV are done. Own
+// tokens only: 4 x 32768 at 32/8 heads 90 us, capped 94 us (6.0 and 5.7 TB/s of a copy's 6.7);
+// 96 x 1024 at 64/8 heads 77 us, capped 80 us. The plan, launches and merge are 9 us of a call
+// that has little to do.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -89,7 +90,7 @@ static_assert(sizeof(SeqPlan) == kPlanInts * 4, "plan entry");
 constexpr int kWide = 1 << 16;
 
 // What an item of n chunks costs, in the units that the cut counts: a chunk, and what comes on
-// top once. (A unit is about 0.19 us: a wide chunk 2.7 us, an own one 1.5 us of the memory's
+// top once. (A unit is about 0.16 us: a wide chunk 2.2 us, an own one 1.5 us of the memory's
 // time, a segment of one own chunk 2.2 us. A wide chunk at 11, 12, 13, 14, 15 and 16: 128
 // sequences of 64/8 heads behind 16384 tokens 101.6, 101.6, 98.9, 97.4, 97.2, 100.3 us. Fixed
 // parts of 4 / 14, 6 / 14, 8 / 16 and 6 / 20 for own and shared items: the same 102.6, 98.0,
@@ -131,7 +132,7 @@ struct Layout {
   // segment follows no wide one that still needs it), or at D 64 memory of its own
   static constexpr int kOffJoin = D == 128 ? kOffQ + kTile : kOffQ + 2 * kTile;
   static constexpr int kOffBar = kOffJoin + 2 * kJoinBytes;
-  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 17;
+  static constexpr int kBars = 2 * kSlots + 2 * kQBars + 2 * kSegRing + 15;
   static constexpr int kOffMl = kOffBar + kBars * 8;  // [pipe][4 warps][16 rows] maximum and sum
   static constexpr int kOffTmem = kOffMl + 2 * 4 * 16 * 8;
   static constexpr int kOffSeg = kOffTmem + 16;
@@ -307,7 +308,8 @@ __device__ __forceinline__ float max32(const float* x) {
   return max3(fmaxf(a[0], a[1]), a[2], a[3]);
 }
 
-// tanh(y) / y for |y| <= 1/2 as a polynomial in y^2, off by at most 2^-26: a weighted least-squares
+// tanh(y) / y for |y| <= 1/2 as a polynomial in y^2, off by at most 2^-25 (a score capped by way of
+// it, with all roundings in fp32, by at most 2^-22.6 of itself): a weighted least-squares
 // fit of the relative error on Chebyshev points, the weights drawn towards the largest errors
 // (Lawson, "Contributions to the theory of linear least maximum approximations", 1961).
 __device__ __forceinline__ constexpr float tanh_coeff(int i) {
@@ -432,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto seg_full = [&](int s) { return bar0 + 8u * (kBar1 + s); };
   auto seg_empty = [&](int s) { return bar0 + 8u * (kBar1 + kSegRing + s); };
   // of pipe t, and of half h of its score tile
-  auto s_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 + t); };
-  auto p_full = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 4 + 2 * t + h); };
-  auto pv_done = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 8 + 2 * t + h); };
-  auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 12 + t); };
-  auto joint = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 14 + t); };
-  const uint32_t drained = bar0 + 8u * (kBar1 + 2 * kSegRing + 16);
+  auto s_full = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + t); };
+  auto p_full = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 2 + 2 * t + h); };
+  auto pv_done = [&](int t, int h) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 6 + 2 * t + h); };
+  auto o_free = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 10 + t); };
+  auto joint = [&](int t) { return bar0 + 8u * (kBar1 + 2 * kSegRing + 12 + t); };
+  const uint32_t drained = bar0 + 8u * (kBar1 + 2 * kSegRing + 14);
   // small segments' queries: rows 32 w .. 32 w + G - 1 of a tile for w < 4, so that tiles 8
   // (16) rows further in the same memory hold those of four (two) segments
   const int small_rows = p.G > 8 ? 16 : 8, n_small = 32 / small_rows;
