@@ -181,13 +181,13 @@ int paged_decode_attn_run_scaled(pda_handle handle, const void* q, const void* k
  * PDA_EUNSUPPORTED); batch <= 16384, and batch * Hkv * (8 n + 6) <= 2^30 for the n chunks of 128
  * tokens that max_blocks * block_size tokens, or window + block_size - 1 if less, may have
  * (batch * Hkv * (8 n + 21) with prefixes; else PDA_EUNSUPPORTED), max_blocks * block_size
- * <= 2^31 - 129; `out` has cfg->dtype. The weights enter the
- * product with V as the sum of two 16-bit terms: off by at most 2^-16 of themselves with
- * bf16; with fp16 by 2^-22 of themselves or 2^-39 of the largest, whichever is more. The
- * work is cut evenly over the GPU; two launches. An infinity in a row of V that a head attends
- * to makes its dim of that head's result an infinity or NaN (zero terms of other weights meet
- * it), as in paged_decode_attn_run on the tensor-core kernel; other dims, heads of other kv
- * heads and other sequences are not touched. */
+ * <= 2^31 - 129; `out` has cfg->dtype. The work is cut evenly over the GPU; two launches.
+ * The weights enter the product with V as the sum of two 16-bit terms: off by at most 2^-16
+ * of themselves with bf16; with fp16 by 2^-22 of themselves or 2^-39 of the largest,
+ * whichever is more. (bf16 values of V below 2^-110 lose bits besides.) An infinity in a row
+ * of V that a head attends to makes its dim of that head's result an infinity or NaN (zero
+ * terms of other weights meet it), as in paged_decode_attn_run on the tensor-core kernel;
+ * other dims, heads of other kv heads and other sequences are not touched. */
 int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k_cache,
                                  const void* v_cache, const int32_t* block_table,
                                  const int32_t* context_lens, int batch, int max_blocks,
@@ -200,14 +200,13 @@ int paged_decode_attn_run_scored(pda_handle handle, const void* q, const void* k
  * first prefix_lens[i] tokens, and those blocks are read once for all of them
  * (tiles of up to 256 query rows of a kv head). cu_seqs [num_prefixes + 1] and
  * prefix_lens [num_prefixes] are int32 on the device; block_table and
- * context_lens hold whole contexts; the formula is that of paged_decode_attn_run_scored
- * and so are the weights' bits, in tiles of any size. Of a prefix, whole blocks are shared, and no more than the
- * shortest context of the group that is not empty holds; a group of one and
- * a sequence outside every group share nothing. Rows of a group that
- * do not name the same blocks are the caller's mistake: the ids of the first
- * sequence that is not empty are the ones read. cu_seqs that does not ascend within
- * [0, batch] is recorded (code 6 of paged_decode_attn_check_device_error), and the
- * call then shares nothing. */
+ * context_lens hold whole contexts; formula, limits and precision are those of
+ * paged_decode_attn_run_scored, whatever a group's size. Of a prefix, whole blocks are
+ * shared, and no more than the shortest context of the group that is not empty holds; a
+ * group of one and a sequence outside every group share nothing. Rows of a group that do
+ * not name the same blocks are the caller's mistake: the ids of the first sequence that is
+ * not empty are the ones read. cu_seqs that does not ascend within [0, batch] is recorded
+ * (code 6 of paged_decode_attn_check_device_error), and the call then shares nothing. */
 int paged_decode_attn_run_shared_prefix(pda_handle handle, const void* q, const void* k_cache,
                                         const void* v_cache, const int32_t* block_table,
                                         const int32_t* context_lens, int batch, int max_blocks,
