@@ -44,12 +44,12 @@
 // 84 MB, stays in the L2, the others' does not). 128 sequences of 64/8 heads behind 16384
 // shared tokens, 32 own ones: 98 us, 700 TFLOP/s (697 us without sharing), capped 148 us; the
 // MMAs alone, two for each weight, take 54 us at the rate of a large library product. A wide
-// chunk takes 2.2 us, some 4300 cycles, of which the tensor pipe works 3072: its softmax, on two
-// warps a scheduler, bounds. 16 sequences (128 rows) behind 65536 tokens: 69 us, 3.9 TB/s (494
-// us); the ring's 160 KiB bound, which holds a V chunk until both halves of its PV are done. Own
-// tokens only: 4 x 32768 at 32/8 heads 90 us, capped 94 us (6.0 and 5.7 TB/s of a copy's 6.7);
-// 96 x 1024 at 64/8 heads 77 us, capped 80 us. The plan, launches and merge are 9 us of a call
-// that has little to do.
+// chunk takes 2.2 us, some 4300 cycles, of which the tensor pipe works nearly three quarters:
+// its softmax, on two warps a scheduler, bounds. 16 sequences (128 rows) behind 65536 tokens:
+// 69 us, 3.9 TB/s (494 us); the ring's 160 KiB bound, which holds a V chunk until both halves
+// of its PV are done. Own tokens only: 4 x 32768 at 32/8 heads 90 us, capped 94 us (6.0 and
+// 5.7 TB/s of a copy's 6.7); 96 x 1024 at 64/8 heads 77 us, capped 80 us. The plan, launches
+// and merge are 9 us of a call that has little to do.
 #pragma once
 
 #include <cuda_bf16.h>
